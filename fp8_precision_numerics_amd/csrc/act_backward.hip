@@ -1,0 +1,267 @@
+// Gradients through an activation, cast to FP8 in both orientations.
+//
+//   fp8_act_backward    d = dy act'(z)                         [M x N]
+//   fp8_gated_backward  d = [ dh u act'(g) | dh act(g) ]       [M x 2F], gu = [g | u]
+//
+//   q = round_to_fp8(d * scale), q_t its transpose (what the weight gradient's
+//   GEMM takes as its K-contiguous operand), amax = max |d|, and for the first
+//   dbias_n = sum_m d.
+//
+// HBM-bound: one read of the inputs, one write of each orientation.  A workgroup
+// takes 128 x 128 tiles of d (gated: the gate's and the up projection's tile of
+// the same 128 x 128 of dh, so that dh is read once); codes go out row-major
+// straight from the registers and column-major through LDS with 4 x 4 byte
+// transposes.  A workgroup walks down one strip of 128 columns, so the bias
+// gradient's column sums stay in its registers over the strip: one fp32 partial
+// row per walk goes to the workspace, added up in a fixed order by
+// column_sums_kernel.
+#include <type_traits>
+
+#include "activation.hpp"
+#include "launch.hpp"
+#include "stats.hpp"
+#include "transpose.hpp"
+
+namespace fp8mi {
+namespace {
+
+constexpr int kNT = 256;
+
+struct BackArgs {
+  const void* dy;        // [M x N] (gated: dh)
+  const uint16_t* z;     // [M x N] bf16 (gated: [M x 2N]); null where the activation is none
+  const float* scale;
+  uint8_t* q;            // may be null
+  uint8_t* q_t;          // may be null
+  uint32_t* amax_bits;
+  unsigned long long* sat;
+  uint4* stat_slots;     // one per workgroup, or null
+  float* col_partials;   // [walks x N] fp32, or null
+  int64_t M, N;
+  int walks;             // workgroups per column strip
+};
+
+// Eight consecutive values of a row-major matrix, widened.
+template <int XT>
+__device__ __forceinline__ void load8f(const void* p, int64_t elem, float* f) {
+  if constexpr (XT == kBF16) {
+    const uint4 v = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p) + elem);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      f[2 * k] = bf16_lo(w[k]);
+      f[2 * k + 1] = bf16_hi(w[k]);
+    }
+  } else {
+    const float4 a = reinterpret_cast<const float4*>(p)[elem / 4], b = reinterpret_cast<const float4*>(p)[elem / 4 + 1];
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  }
+}
+
+// Tile 0 of LDS holds the codes of d (gated: of the gate's part), tile 1 those of
+// the up projection's part.
+template <int XT, int FMT, int ACT, bool GATED, bool STATS>
+__global__ __launch_bounds__(kNT) void act_backward_kernel(BackArgs a) {
+  constexpr int TILES = GATED ? 2 : 1;
+  __shared__ __attribute__((aligned(16))) uint8_t tile[TILES][kTile * kPitch];
+  const int t = threadIdx.x;
+  const int vi = t & 15, rr0 = t >> 4;  // the lane's 8 columns and first row (of 16 passes 16 rows apart: 8)
+  const int64_t strips = (a.N + kTile - 1) / kTile;
+  const int64_t strip = blockIdx.x % strips, walk = blockIdx.x / strips;
+  const int64_t col0 = strip * kTile, c = col0 + vi * 8;
+  const int64_t ldq = GATED ? 2 * a.N : a.N;
+  const int64_t row_tiles = (a.M + kTile - 1) / kTile;
+  const float s = *a.scale;
+  LaneStats st;
+  float db[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int64_t rt = walk; rt < row_tiles; rt += a.walks) {
+    const int64_t row0 = rt * kTile;
+    // Four passes' loads are issued before the first is used.
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      float dy[4][8], z[4][8], u[GATED ? 4 : 1][8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t r = row0 + rr0 + (half * 4 + i) * 16;
+        if (r < a.M && c < a.N) {
+          load8f<XT>(a.dy, r * a.N + c, dy[i]);
+          if constexpr (GATED) {
+            load8f<kBF16>(a.z, r * ldq + c, z[i]);
+            load8f<kBF16>(a.z, r * ldq + a.N + c, u[i]);
+          } else if constexpr (ACT != kActNone) {
+            load8f<kBF16>(a.z, r * a.N + c, z[i]);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int rr = rr0 + (half * 4 + i) * 16;
+        const int64_t r = row0 + rr;
+        if (r < a.M && c < a.N) {
+          float d[8], e[GATED ? 8 : 1];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            float val, slope;
+            act_value_slope<ACT>(ACT == kActNone && !GATED ? 0.0f : z[i][k], &val, &slope);
+            if constexpr (GATED) {
+              d[k] = dy[i][k] * u[i][k] * slope;
+              e[k] = dy[i][k] * val;
+            } else {
+              d[k] = ACT == kActNone ? dy[i][k] : dy[i][k] * slope;
+              db[k] += d[k];
+            }
+          }
+          const uint2 cd = encode8<FMT, STATS>(d, s, st);
+          if (a.q) *reinterpret_cast<uint2*>(a.q + r * ldq + c) = cd;
+          uint32_t* dst = reinterpret_cast<uint32_t*>(tile[0] + rr * kPitch + vi * 8);
+          dst[0] = cd.x;
+          dst[1] = cd.y;
+          if constexpr (GATED) {
+            const uint2 ce = encode8<FMT, STATS>(e, s, st);
+            if (a.q) *reinterpret_cast<uint2*>(a.q + r * ldq + a.N + c) = ce;
+            uint32_t* up = reinterpret_cast<uint32_t*>(tile[TILES - 1] + rr * kPitch + vi * 8);
+            up[0] = ce.x;
+            up[1] = ce.y;
+          }
+        }
+      }
+    }
+    if (a.q_t) {  // M and N are multiples of 16 here
+      __syncthreads();
+#pragma unroll
+      for (int h = 0; h < TILES; ++h)
+        transposed_store(tile[h], a.q_t + (int64_t)h * a.N * a.M, a.M, a.N, row0, col0, t);
+      __syncthreads();
+    }
+  }
+  if constexpr (!GATED) {
+    if (a.col_partials) {
+      // the 16 lanes of each column group add up in LDS (the tile's space), in a fixed order
+      __syncthreads();
+      float* sum = reinterpret_cast<float*>(tile[0]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum[rr0 * kTile + vi * 8 + k] = db[k];
+      __syncthreads();
+      if (t < kTile && col0 + t < a.N) {
+        float v = 0.0f;
+#pragma unroll
+        for (int g = 0; g < 16; ++g) v += sum[g * kTile + t];
+        a.col_partials[walk * a.N + col0 + t] = v;
+      }
+    }
+  }
+  if constexpr (STATS) block_finish<kNT / 64>(st.amax(), wave_sum_u32(st.sat), a.amax_bits, a.sat, a.stat_slots);
+}
+
+// out[n] = sum over the rows of partials [count x cols]: 16 columns a workgroup,
+// 16 lanes down the rows of each, then a tree in LDS.
+__global__ __launch_bounds__(256) void column_sums_kernel(const float* __restrict__ partials, int count, int64_t cols,
+                                                          float* __restrict__ out) {
+  __shared__ float buf[16][17];
+  const int cx = threadIdx.x & 15, ry = threadIdx.x >> 4;
+  const int64_t c = (int64_t)blockIdx.x * 16 + cx;
+  float v = 0.0f;
+  if (c < cols) {
+    int r = ry;
+    for (; r + 112 < count; r += 128) {
+      float p[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) p[u] = partials[(int64_t)(r + 16 * u) * cols + c];
+      v += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+    }
+    for (; r < count; r += 16) v += partials[(int64_t)r * cols + c];
+  }
+  buf[ry][cx] = v;
+  __syncthreads();
+#pragma unroll
+  for (int half = 8; half > 0; half >>= 1) {
+    if (ry < half) buf[ry][cx] += buf[ry + half][cx];
+    __syncthreads();
+  }
+  if (ry == 0 && c < cols) out[c] = buf[0][cx];
+}
+
+template <int XT, int FMT, int ACT, bool GATED>
+void back_run(const BackArgs& a, bool stats, unsigned grid, hipStream_t st) {
+  if (stats) hipLaunchKernelGGL((act_backward_kernel<XT, FMT, ACT, GATED, true>), dim3(grid), dim3(kNT), 0, st, a);
+  else hipLaunchKernelGGL((act_backward_kernel<XT, FMT, ACT, GATED, false>), dim3(grid), dim3(kNT), 0, st, a);
+}
+
+template <int XT, int FMT, bool GATED>
+void back_act(const BackArgs& a, int act, bool stats, unsigned grid, hipStream_t st) {
+  if (act == kActRelu) back_run<XT, FMT, kActRelu, GATED>(a, stats, grid, st);
+  else if (act == kActSilu) back_run<XT, FMT, kActSilu, GATED>(a, stats, grid, st);
+  else if (act == kActGelu) back_run<XT, FMT, kActGelu, GATED>(a, stats, grid, st);
+  else back_run<XT, FMT, kActNone, GATED>(a, stats, grid, st);
+}
+
+template <bool GATED>
+hipError_t back_launch(BackArgs a, int xtype, int fmt, int act, float* dbias, float* amax, void* workspace,
+                       size_t workspace_bytes, hipStream_t st) {
+  const bool stats = amax || a.sat;
+  const int64_t strips = (a.N + kTile - 1) / kTile, row_tiles = (a.M + kTile - 1) / kTile;
+  const bool empty = a.M * a.N == 0;
+  // As many walks a strip as fill the device with 8 workgroups a compute unit.
+  int64_t walks = empty ? 0 : persistent_groups(8) / strips;
+  if (!empty) walks = walks < 1 ? 1 : (walks > row_tiles ? row_tiles : walks);
+  // The workspace holds the bias gradient's partial rows, then the statistics' slots.
+  uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
+  if (dbias && !empty) {
+    const int64_t fit = (int64_t)(workspace_bytes / (a.N * sizeof(float)));  // >= 1: checked by the entry point
+    if (walks > fit) walks = fit;
+    a.col_partials = reinterpret_cast<float*>(ws);
+    const size_t used = ((size_t)walks * a.N * sizeof(float) + 15) & ~size_t(15);
+    ws = used < workspace_bytes ? ws + used : nullptr;
+    workspace_bytes = ws ? workspace_bytes - used : 0;
+  }
+  const int64_t groups = walks * strips;
+  if (stats && ws && workspace_bytes >= (size_t)groups * sizeof(uint4)) a.stat_slots = reinterpret_cast<uint4*>(ws);
+  if (stats && !a.stat_slots) {
+    const hipError_t e = launch_clear_stats(amax, a.sat, st);
+    if (e != hipSuccess) return e;
+  }
+  a.walks = (int)walks;
+  if (!empty) {
+    if (xtype == kBF16) {
+      if (fmt == kE4M3) back_act<kBF16, kE4M3, GATED>(a, act, stats, (unsigned)groups, st);
+      else back_act<kBF16, kE5M2, GATED>(a, act, stats, (unsigned)groups, st);
+    } else {
+      if (fmt == kE4M3) back_act<kF32, kE4M3, GATED>(a, act, stats, (unsigned)groups, st);
+      else back_act<kF32, kE5M2, GATED>(a, act, stats, (unsigned)groups, st);
+    }
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (dbias) {
+    e = launch_column_sums(a.col_partials, (int)walks, a.N, dbias, st);
+    if (e != hipSuccess) return e;
+  }
+  if (a.stat_slots) return launch_reduce_stats(a.stat_slots, (int)groups, amax, a.sat, st);
+  return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_column_sums(const float* partials, int count, int64_t cols, float* out, hipStream_t stream) {
+  if (cols == 0) return hipSuccess;
+  hipLaunchKernelGGL(column_sums_kernel, dim3((unsigned)((cols + 15) / 16)), dim3(256), 0, stream, partials, count,
+                     cols, out);
+  return hipGetLastError();
+}
+
+hipError_t launch_act_backward(const void* dy, int xtype, const uint16_t* z, int act, int64_t M, int64_t N, int fmt,
+                               const float* scale, uint8_t* q, uint8_t* q_t, float* dbias, float* amax,
+                               unsigned long long* sat, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const BackArgs a{dy, z, scale, q, q_t, reinterpret_cast<uint32_t*>(amax), sat, nullptr, nullptr, M, N, 0};
+  return back_launch<false>(a, xtype, fmt, act, dbias, amax, workspace, workspace_bytes, stream);
+}
+
+hipError_t launch_gated_backward(const void* dh, int xtype, const uint16_t* gu, int act, int64_t M, int64_t F, int fmt,
+                                 const float* scale, uint8_t* q, uint8_t* q_t, float* amax, unsigned long long* sat,
+                                 void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const BackArgs a{dh, gu, scale, q, q_t, reinterpret_cast<uint32_t*>(amax), sat, nullptr, nullptr, M, F, 0};
+  return back_launch<true>(a, xtype, fmt, act, nullptr, amax, workspace, workspace_bytes, stream);
+}
+
+}  // namespace fp8mi

@@ -6,6 +6,7 @@
 #include <atomic>
 
 #include "fp8mi.h"
+#include "epilogue.hpp"
 #include "launch.hpp"
 
 namespace {
@@ -22,6 +23,8 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 bool fmt_ok(int f) { return f == FP8MI_E4M3 || f == FP8MI_E5M2; }
 bool dtype_ok(int d) { return d == FP8MI_F32 || d == FP8MI_BF16; }
 bool accum_ok(int a) { return a == FP8MI_ACCUM_EXACT || a == FP8MI_ACCUM_MFMA_FP8; }
+
+bool act_ok(int a) { return a == FP8MI_ACT_NONE || a == FP8MI_ACT_RELU || a == FP8MI_ACT_SILU || a == FP8MI_ACT_GELU; }
 
 int check_device() {
   int dev = -1;
@@ -71,6 +74,8 @@ const char* fp8mi_status_string(int status) {
     case FP8MI_ERR_LAUNCH: return "kernel launch failed";
     case FP8MI_ERR_DEVICE: return "no usable gfx950 device is current";
     case FP8MI_ERR_ACCUM: return "unknown accumulation mode";
+    case FP8MI_ERR_ACT: return "unknown activation";
+    case FP8MI_ERR_WORKSPACE: return "the workspace is too small";
     default: return "unknown status";
   }
 }
@@ -295,6 +300,180 @@ int fp8_grouped_gemm(const uint8_t* A, const float* sinv_a, const uint8_t* B, co
   if (dev != FP8MI_OK) return dev;
   return launched(fp8mi::launch_grouped_gemm(A, sinv_a, B, sinv_b, m_offsets, G, total_m, N, K, C,
                                              ctype, accum, (hipStream_t)stream));
+}
+
+namespace {
+
+// What the two norm entry points share; FP8MI_OK means "go on".
+int check_norm(const void* x, const void* residual, const void* weight, int xtype, int64_t rows, int64_t cols,
+               float eps, int fmt, const void* sum_out, const uint8_t* q) {
+  if (!dtype_ok(xtype)) return FP8MI_ERR_DTYPE;
+  if (!fmt_ok(fmt)) return FP8MI_ERR_FORMAT;
+  if (!dims_ok(rows, cols) || cols > kMaxDim || !(eps >= 0.0f)) return FP8MI_ERR_SHAPE;
+  if ((cols & 15) != 0) return FP8MI_ERR_ALIGN;
+  if (sum_out && !residual) return FP8MI_ERR_NULL;
+  if (rows * cols == 0) return FP8MI_OK;
+  if (!x || !weight || !q) return FP8MI_ERR_NULL;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(sum_out) || !aligned16(q))
+    return FP8MI_ERR_ALIGN;
+  return FP8MI_OK;
+}
+
+// What the GEMMs with a feed-forward epilogue share; `width`: output columns, `brows`: rows of B.
+int check_epi_gemm(const uint8_t* A, int fa, const uint8_t* B, int fb, int64_t M, int64_t width, int64_t brows,
+                   int64_t K, const float* sinv_a, const float* sinv_b, int act, const void* y, int ytype,
+                   const float* out_scale, const void* z, float* amax, unsigned long long* sat, int accum,
+                   bool* nothing) {
+  *nothing = false;
+  if (!fmt_ok(fa) || !fmt_ok(fb)) return FP8MI_ERR_FORMAT;
+  if (!act_ok(act)) return FP8MI_ERR_ACT;
+  if (ytype != FP8MI_OUT_F32 && ytype != FP8MI_OUT_BF16 && ytype != FP8MI_OUT_E4M3 && ytype != FP8MI_OUT_E5M2)
+    return FP8MI_ERR_DTYPE;
+  if (!accum_ok(accum)) return FP8MI_ERR_ACCUM;
+  if (M < 0 || width < 0 || K <= 0 || M > kMaxDim || brows > kMaxDim || K > kMaxGemmK) return FP8MI_ERR_SHAPE;
+  if (!dims_ok(M, K) || !dims_ok(brows, K) || !dims_ok(M, brows)) return FP8MI_ERR_SHAPE;
+  if ((K & 15) != 0) return FP8MI_ERR_ALIGN;
+  if (((M + 127) / 128) * ((brows + 127) / 128 + 1) > kMaxDim) return FP8MI_ERR_SHAPE;
+  const bool fp8 = ytype == FP8MI_OUT_E4M3 || ytype == FP8MI_OUT_E5M2;
+  if ((amax || sat) && !fp8) return FP8MI_ERR_DTYPE;
+  if (M == 0 || width == 0) {
+    *nothing = !amax && !sat;
+    return FP8MI_OK;
+  }
+  if (!A || !B || !sinv_a || !sinv_b || !y || (fp8 && !out_scale)) return FP8MI_ERR_NULL;
+  if (!aligned16(A) || !aligned16(B) || !aligned16(y) || !aligned16(z)) return FP8MI_ERR_ALIGN;
+  return FP8MI_OK;
+}
+
+// What the two activation gradients share; `ld`: columns of d.
+int check_act_back(const void* dy, int xtype, const uint16_t* z, bool need_z, int act, int64_t M, int64_t N,
+                   int64_t ld, int fmt, const float* scale, const uint8_t* q, const uint8_t* q_t, bool stats,
+                   const void* workspace, size_t workspace_bytes) {
+  if (!dtype_ok(xtype)) return FP8MI_ERR_DTYPE;
+  if (!fmt_ok(fmt)) return FP8MI_ERR_FORMAT;
+  if (!act_ok(act)) return FP8MI_ERR_ACT;
+  if (!dims_ok(M, ld) || ld > kMaxDim || (M + 127) / 128 > kMaxDim) return FP8MI_ERR_SHAPE;
+  if ((N & 15) != 0 || (q_t && (M & 15) != 0)) return FP8MI_ERR_ALIGN;
+  if (!q && !q_t && !stats) return FP8MI_ERR_NULL;
+  if (workspace && (!aligned16(workspace) || workspace_bytes < 16)) return FP8MI_ERR_ALIGN;
+  if (M * N == 0) return FP8MI_OK;
+  if (!dy || !scale || (need_z && !z)) return FP8MI_ERR_NULL;
+  if (!aligned16(dy) || !aligned16(z) || !aligned16(q) || !aligned16(q_t)) return FP8MI_ERR_ALIGN;
+  return FP8MI_OK;
+}
+
+}  // namespace
+
+int fp8_rmsnorm_quantize(const void* x, const void* residual, const void* weight, int xtype, int64_t rows,
+                         int64_t cols, float eps, int fmt, const float* scale, void* sum_out, uint8_t* q, float* rstd,
+                         float* amax, unsigned long long* sat, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+  const int bad = check_norm(x, residual, weight, xtype, rows, cols, eps, fmt, sum_out, q);
+  if (bad != FP8MI_OK) return bad;
+  if (workspace && (!aligned16(workspace) || workspace_bytes < 16)) return FP8MI_ERR_ALIGN;
+  if (rows * cols == 0 && !amax && !sat) return FP8MI_OK;
+  if (rows * cols != 0 && !scale) return FP8MI_ERR_NULL;
+  const int dev = check_device();
+  if (dev != FP8MI_OK) return dev;
+  return launched(fp8mi::launch_rmsnorm_quantize(x, residual, weight, xtype, rows, cols, eps, fmt, scale, sum_out, q,
+                                                 rstd, amax, sat, workspace, workspace_bytes, (hipStream_t)stream));
+}
+
+int fp8_rmsnorm_quantize_blockwise(const void* x, const void* residual, const void* weight, int xtype, int64_t rows,
+                                   int64_t cols, float eps, int fmt, void* sum_out, uint8_t* q, float* scale_inv,
+                                   float* rstd, void* stream) {
+  const int bad = check_norm(x, residual, weight, xtype, rows, cols, eps, fmt, sum_out, q);
+  if (bad != FP8MI_OK) return bad;
+  if (rows * cols == 0) return FP8MI_OK;
+  if (!scale_inv) return FP8MI_ERR_NULL;
+  const int dev = check_device();
+  if (dev != FP8MI_OK) return dev;
+  return launched(fp8mi::launch_rmsnorm_quantize_blockwise(x, residual, weight, xtype, rows, cols, eps, fmt, sum_out,
+                                                           q, scale_inv, rstd, (hipStream_t)stream));
+}
+
+int fp8_rmsnorm_backward(const void* dy, const void* h, const float* rstd, const void* weight, const void* dresidual,
+                         int xtype, int64_t rows, int64_t cols, void* dx, float* dweight, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  if (!dtype_ok(xtype)) return FP8MI_ERR_DTYPE;
+  if (!dims_ok(rows, cols) || cols > kMaxDim) return FP8MI_ERR_SHAPE;
+  if ((cols & 15) != 0) return FP8MI_ERR_ALIGN;
+  if (workspace && !aligned16(workspace)) return FP8MI_ERR_ALIGN;
+  if (rows * cols == 0 && (cols == 0 || !dweight)) return FP8MI_OK;
+  if (rows != 0) {
+    if (!dy || !h || !rstd || !weight || !dx) return FP8MI_ERR_NULL;
+    if (!aligned16(dy) || !aligned16(h) || !aligned16(weight) || !aligned16(dresidual) || !aligned16(dx))
+      return FP8MI_ERR_ALIGN;
+    if (dweight && !workspace) return FP8MI_ERR_NULL;
+    if (dweight && workspace_bytes < (size_t)cols * sizeof(float)) return FP8MI_ERR_WORKSPACE;
+  }
+  const int dev = check_device();
+  if (dev != FP8MI_OK) return dev;
+  return launched(fp8mi::launch_rmsnorm_backward(dy, h, rstd, weight, dresidual, xtype, rows, cols, dx, dweight,
+                                                 workspace, workspace_bytes, (hipStream_t)stream));
+}
+
+int fp8_gemm_gated(const uint8_t* A, int fa, const uint8_t* B, int fb, int64_t M, int64_t F, int64_t K,
+                   const float* sinv_a, const float* sinv_b, int act, void* h, int htype, const float* out_scale,
+                   uint16_t* gu, float* amax, unsigned long long* sat, int accum, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+  if (F > kMaxDim / 2) return FP8MI_ERR_SHAPE;
+  if (workspace && !aligned16(workspace)) return FP8MI_ERR_ALIGN;
+  bool nothing;
+  const int bad = check_epi_gemm(A, fa, B, fb, M, F, 2 * F, K, sinv_a, sinv_b, act, h, htype, out_scale, gu, amax, sat,
+                                 accum, &nothing);
+  if (bad != FP8MI_OK || nothing) return bad;
+  const int dev = check_device();
+  if (dev != FP8MI_OK) return dev;
+  const fp8mi::EpiArgs epi{h, gu, nullptr, nullptr, out_scale, reinterpret_cast<uint32_t*>(amax), sat, act, htype};
+  return launched(fp8mi::launch_gemm_gated(A, fa, B, fb, M, F, K, sinv_a, sinv_b, epi, accum, (hipStream_t)stream));
+}
+
+int fp8_gemm_fused(const uint8_t* A, int fa, const uint8_t* B, int fb, int64_t M, int64_t N, int64_t K,
+                   const float* sinv_a, const float* sinv_b, const uint16_t* bias, int act, const uint16_t* residual,
+                   void* y, int ytype, const float* out_scale, uint16_t* z, float* amax, unsigned long long* sat,
+                   int accum, void* workspace, size_t workspace_bytes, void* stream) {
+  if (workspace && !aligned16(workspace)) return FP8MI_ERR_ALIGN;
+  bool nothing;
+  const int bad = check_epi_gemm(A, fa, B, fb, M, N, N, K, sinv_a, sinv_b, act, y, ytype, out_scale, z, amax, sat,
+                                 accum, &nothing);
+  if (bad != FP8MI_OK || nothing) return bad;
+  if (!aligned16(bias) || !aligned16(residual)) return FP8MI_ERR_ALIGN;
+  const int dev = check_device();
+  if (dev != FP8MI_OK) return dev;
+  const fp8mi::EpiArgs epi{y, z, bias, residual, out_scale, reinterpret_cast<uint32_t*>(amax), sat, act, ytype};
+  return launched(fp8mi::launch_gemm_fused(A, fa, B, fb, M, N, K, sinv_a, sinv_b, epi, accum, (hipStream_t)stream));
+}
+
+int fp8_act_backward(const void* dy, int xtype, const uint16_t* z, int act, int64_t M, int64_t N, int fmt,
+                     const float* scale, uint8_t* q, uint8_t* q_t, float* dbias, float* amax, unsigned long long* sat,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  const int bad = check_act_back(dy, xtype, z, act != FP8MI_ACT_NONE, act, M, N, N, fmt, scale, q, q_t,
+                                 amax || sat || dbias, workspace, workspace_bytes);
+  if (bad != FP8MI_OK) return bad;
+  if (M * N == 0 && !amax && !sat && (!dbias || N == 0)) return FP8MI_OK;
+  if (dbias && M * N != 0) {
+    if (!workspace) return FP8MI_ERR_NULL;
+    if (workspace_bytes < (size_t)N * sizeof(float)) return FP8MI_ERR_WORKSPACE;
+  }
+  const int dev = check_device();
+  if (dev != FP8MI_OK) return dev;
+  return launched(fp8mi::launch_act_backward(dy, xtype, z, act, M, N, fmt, scale, q, q_t, dbias, amax, sat, workspace,
+                                             workspace_bytes, (hipStream_t)stream));
+}
+
+int fp8_gated_backward(const void* dh, int xtype, const uint16_t* gu, int act, int64_t M, int64_t F, int fmt,
+                       const float* scale, uint8_t* q, uint8_t* q_t, float* amax, unsigned long long* sat,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+  if (F < 0 || F > kMaxDim / 2) return FP8MI_ERR_SHAPE;
+  const int bad = check_act_back(dh, xtype, gu, true, act, M, F, 2 * F, fmt, scale, q, q_t, amax || sat, workspace,
+                                 workspace_bytes);
+  if (bad != FP8MI_OK) return bad;
+  if (M * F == 0 && !amax && !sat) return FP8MI_OK;
+  const int dev = check_device();
+  if (dev != FP8MI_OK) return dev;
+  return launched(fp8mi::launch_gated_backward(dh, xtype, gu, act, M, F, fmt, scale, q, q_t, amax, sat, workspace,
+                                               workspace_bytes, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -25,6 +25,7 @@
 
 #include <type_traits>
 
+#include "epilogue.hpp"
 #include "gemm_tile.hpp"
 
 namespace fp8mi {
@@ -119,7 +120,13 @@ __device__ __forceinline__ int bt_lds_offset(int krow, int col) {
 
 constexpr uint32_t kOutOfRange = 0x80000000u;  // above any operand size these loads allow (< 2^31 bytes)
 
-template <int BM, int BN, int NW, bool BT = false>
+// PAIR (nonzero: the gated product; B stores F rows of the gate projection, then
+// F of the up projection, n_end = F): tile rows hold PAIR gate rows, then the same
+// PAIR rows of the up projection, and so on, so that a matrix-core block of gate
+// columns and its block of up columns land in the same lanes.  A load's 8 rows lie
+// in one block, so each load takes one of two resources (the gate's and the up
+// projection's rows from the tile start to F); rows past F read as zero.
+template <int BM, int BN, int NW, bool BT = false, int PAIR = 0>
 struct SlabLoader {
   static constexpr int LQA = BM / 8 / NW, LQB = BN / 8 / NW;  // direct-load instructions per wave per step
   static constexpr int PER = (LQA + LQB + kDmaGroups - 1) / kDmaGroups;
@@ -127,6 +134,7 @@ struct SlabLoader {
   static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "tile rows must split evenly over the wavefronts");
   static_assert(NW % 2 == 0, "the swizzle of a lane's load must not depend on its row group");
   static_assert(!BT || (BN >= 128 && BN <= 1024 && 128 % (RPB * NW) == 0), "BT slab shape");
+  static_assert(PAIR == 0 || (!BT && PAIR % 16 == 0 && BN % (2 * PAIR) == 0), "PAIR slab shape");
   const uint8_t* A;
   const uint8_t* B;
   int64_t m0, m_end, n0, n_end;
@@ -134,6 +142,19 @@ struct SlabLoader {
   int ldb;            // BT: bytes per K row of B (= N)
   uint32_t voff_bt;   // BT: the lane's offset in the first K row group, or kOutOfRange
   __amdgpu_buffer_rsrc_t ra, rb;
+  __amdgpu_buffer_rsrc_t rb_up;  // PAIR: the up projection's rows
+  int lane_off;                  // PAIR: the lane's offset inside a group of 8 rows, for either parity of the group
+
+  // PAIR: tile row of the first row of load e (an 8-row group) inside its
+  // projection, and whether that is the up projection (both wave-uniform).
+  static __device__ __forceinline__ int pair_row(int e) {
+    constexpr int P = PAIR ? PAIR : 16;
+    return (8 * e / (2 * P)) * P + 8 * e % P;
+  }
+  static __device__ __forceinline__ bool pair_up(int e) {
+    constexpr int P = PAIR ? PAIR : 16;
+    return (8 * e / P) & 1;
+  }
 
   __device__ __forceinline__ SlabLoader(const uint8_t* A_, int64_t m0_, int64_t m_end_, const uint8_t* B_,
                                         int64_t n0_, int64_t n_end_, int K_, int w_, int lane)
@@ -141,7 +162,13 @@ struct SlabLoader {
     ra = operand_rsrc(A + m0 * K, m_end - m0, K);
     const int lrow = w * 8 + (lane >> 3);
     voff = lrow * K + (((lane & 7) ^ lds_swz(lrow)) & 7) * 16;
-    if constexpr (BT) {
+    if constexpr (PAIR) {
+      ldb = K;
+      voff_bt = 0;
+      rb = operand_rsrc(B + n0 * K, n_end - n0, K);
+      rb_up = operand_rsrc(B + (n_end + n0) * K, n_end - n0, K);
+      lane_off = voff - w * 8 * K;  // row lane >> 3 of a group; the swizzled granule has the group's parity, that of w
+    } else if constexpr (BT) {
       ldb = (int)n_end;
       rb = operand_rsrc(B, K, ldb);  // the whole [K x N] matrix
       const int r = w * RPB + lane / (BN / 16);                  // K row of load 0 (same parity for every load)
@@ -168,7 +195,10 @@ struct SlabLoader {
       if (d < LQA) dma_lds16(ra, la + d * NW * 1024, voff + d * NW * 8 * K, k0);
       else if constexpr (BT)  // a full step: every K row exists, only the column needs the range check
         dma_lds16(rb, lb + (d - LQA) * NW * 1024, (int)voff_bt, ((d - LQA) * NW * RPB + k0) * ldb);
-      else dma_lds16(rb, lb + (d - LQA) * NW * 1024, voff + (d - LQA) * NW * 8 * K, k0);
+      else if constexpr (PAIR) {
+        const int e = w + (d - LQA) * NW;
+        dma_lds16(pair_up(e) ? rb_up : rb, lb + (d - LQA) * NW * 1024, lane_off + pair_row(e) * K, k0);
+      } else dma_lds16(rb, lb + (d - LQA) * NW * 1024, voff + (d - LQA) * NW * 8 * K, k0);
     }
     __builtin_amdgcn_sched_barrier(0);
   }
@@ -182,6 +212,17 @@ struct SlabLoader {
 #pragma unroll
       for (int d = 0; d < LQB; ++d)
         dma_lds16(rb, lb + d * NW * 1024, (int)(voff_bt + (uint32_t)((d * NW * RPB + kt * kBK) * ldb)), 0);
+    } else if constexpr (PAIR) {
+      const int g = t & 7, k = kt * kBK + g * 16;
+#pragma unroll
+      for (int j = 0; j < BN * 8 / (64 * NW); ++j) {
+        const int row = (t >> 3) + j * 8 * NW;
+        const int64_t r = n0 + (row / (2 * PAIR)) * PAIR + row % PAIR;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r < n_end && k < K)
+          v = *reinterpret_cast<const uint4*>(B + (r + ((row / PAIR) & 1 ? n_end : 0)) * K + k);
+        *reinterpret_cast<uint4*>(dst + BM * kBK + lds_granule(row, g)) = v;
+      }
     } else {
       tile_load_zero_fill<BN, 64 * NW>(B, K, n0, n_end, kt * kBK, K, dst + BM * kBK, t);
     }
@@ -520,11 +561,14 @@ __device__ __forceinline__ uint2 lds_read_tr8(const uint8_t* p) {
   return make_uint2((uint32_t)r[0], (uint32_t)r[1]);
 }
 
-template <int BM, int BN, int WM, int WN, int FA, int FB, int OUT, int MODE, bool BT = false>
+// ARGS: RequantArgs, or (epilogue.hpp) FusedEpi or GatedEpi, which replace the
+// output's writing by the feed-forward epilogues (OUT is then kF32, the type in
+// which the tile is staged, and C is unused).
+template <int BM, int BN, int WM, int WN, int FA, int FB, int OUT, int MODE, bool BT = false, class ARGS = RequantArgs>
 __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, int M, int N, int K,
     const float* __restrict__ sinv_a, const float* __restrict__ sinv_b, void* __restrict__ C,
-    int tiles_m, int tiles_n, int group_m, RequantArgs rq, MxScales mxs) {
+    int tiles_m, int tiles_n, int group_m, ARGS rq, MxScales mxs) {
   constexpr int NW = WM * WN, NT = 64 * NW;
   constexpr int WTM = BM / WM, WTN = BN / WN;
   // Output block of one matrix-core instruction: 16x16 (FP8 paths), 32x32 (bf16 paths).
@@ -532,6 +576,11 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(
   constexpr bool MXE = MODE == kAccumMxExact;
   constexpr bool MXS = MX || MXE;  // stages carry the step's E8M0 block scales
   constexpr int BLK = (MODE == kAccumExact || MXE) ? 32 : 16;
+  constexpr bool EPI = is_epilogue<ARGS>::value;
+  constexpr bool GATED = std::is_same<ARGS, GatedEpi>::value;
+  constexpr int PAIR = GATED ? BLK : 0;
+  constexpr int OUT_BN = GATED ? BN / 2 : BN;  // output columns of a tile
+  static_assert(!EPI || (OUT == kF32 && !MXS), "the feed-forward epilogues stage fp32 tiles");
   constexpr int FM = WTM / BLK, FN = WTN / BLK;
   static_assert(FM >= 1 && FN >= 1 && WTM % BLK == 0 && WTN % BLK == 0, "wave tile shape");
   // A stage: the A slab, the B slab, and (MXFP8) their block scales.
@@ -545,11 +594,11 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(
   const int t = threadIdx.x, lane = t & 63;
   const int w = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wm = w / WN, wn = w % WN;
-  const int64_t m_base = (int64_t)tm * BM, n_base = (int64_t)tn * BN;
+  const int64_t m_base = (int64_t)tm * BM, n_base = (int64_t)tn * OUT_BN;
   const int nk = (K + kBK - 1) / kBK;
   const bool ragged_k = (K % kBK) != 0;
 
-  const SlabLoader<BM, BN, NW, BT> slabs(A, m_base, M, B, n_base, N, K, w, lane);
+  const SlabLoader<BM, BN, NW, BT, PAIR> slabs(A, m_base, M, B, n_base, N, K, w, lane);
   static_assert(!BT || !MXS, "MXFP8 operands are K-contiguous");
   auto issue_direct = [&](uint8_t* dst, int kt, int g) {
     slabs.issue(dst, kt, g);
@@ -644,12 +693,27 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(
     constexpr int PASS = pass_rows<BM>(2 * STAGE, TW::ROWB);
     static_assert(PASS == BM || OUT == kF32 || OUT == kBF16, "FP8 tiles go out in one pass");
     TW tw{smem, PASS};
+    if constexpr (EPI) {
+      EpiPass<BN, NT, PASS, PAIR, TW> pass(rq, M, N, m_base, n_base, t);
+      LaneStats st;
+      const uint32_t seen = rq.amax_bits ? __hip_atomic_load(rq.amax_bits, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0u;
 #pragma unroll 1
-    for (int r0 = 0; r0 < BM; r0 += PASS) {
-      __syncthreads();  // the LDS is free: K loop or previous pass done
-      emit(r0, r0 + PASS, tw);
-      __syncthreads();
-      tw.flush(C, M, N, m_base + r0, n_base, t);
+      for (int r0 = 0; r0 < BM; r0 += PASS) {
+        pass.prefetch(r0);
+        __syncthreads();
+        emit(r0, r0 + PASS, tw);
+        __syncthreads();
+        pass.flush(tw, r0, st);
+      }
+      if (rq.amax_bits || rq.sat) publish_epilogue_stats(rq, st, seen, lane);
+    } else {
+#pragma unroll 1
+      for (int r0 = 0; r0 < BM; r0 += PASS) {
+        __syncthreads();  // the LDS is free: K loop or previous pass done
+        emit(r0, r0 + PASS, tw);
+        __syncthreads();
+        tw.flush(C, M, N, m_base + r0, n_base, t);
+      }
     }
   };
   // `rows(r_lo, r_hi, writer, mask)`: write_tile with the bounds tests of the

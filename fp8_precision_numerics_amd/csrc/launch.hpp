@@ -8,6 +8,8 @@
 
 namespace fp8mi {
 
+struct EpiArgs;  // epilogue.hpp
+
 // The delayed-scaling history step a cast may run right after itself
 // (fp8_quantize_update); `history` null = none.
 struct HistoryArgs {
@@ -79,5 +81,45 @@ hipError_t launch_quantize_mx(const void* x, int xtype, int64_t rows, int64_t co
 
 hipError_t launch_gemm_mx(const uint8_t* A, int fa, const uint8_t* sa, const uint8_t* B, int fb, const uint8_t* sb,
                           int64_t M, int64_t N, int64_t K, void* C, int ctype, int accum, hipStream_t stream);
+
+// Clears the statistics outputs (either may be null) before kernels that update
+// them with atomics.
+hipError_t launch_clear_stats(float* amax, unsigned long long* sat, hipStream_t stream);
+
+// Reduces `count` workgroup partials (stats.hpp) into the statistics outputs.
+hipError_t launch_reduce_stats(const void* partials, int count, float* amax, unsigned long long* sat,
+                               hipStream_t stream);
+
+// out[n] = sum of column n of partials [count x cols], in a fixed order.
+hipError_t launch_column_sums(const float* partials, int count, int64_t cols, float* out, hipStream_t stream);
+
+hipError_t launch_rmsnorm_quantize(const void* x, const void* residual, const void* weight, int xtype, int64_t rows,
+                                   int64_t cols, float eps, int fmt, const float* scale, void* sum_out, uint8_t* q,
+                                   float* rstd, float* amax, unsigned long long* sat, void* workspace,
+                                   size_t workspace_bytes, hipStream_t stream);
+
+hipError_t launch_rmsnorm_quantize_blockwise(const void* x, const void* residual, const void* weight, int xtype,
+                                             int64_t rows, int64_t cols, float eps, int fmt, void* sum_out, uint8_t* q,
+                                             float* scale_inv, float* rstd, hipStream_t stream);
+
+hipError_t launch_rmsnorm_backward(const void* dy, const void* h, const float* rstd, const void* weight,
+                                   const void* dres, int xtype, int64_t rows, int64_t cols, void* dx, float* dweight,
+                                   void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+hipError_t launch_act_backward(const void* dy, int xtype, const uint16_t* z, int act, int64_t M, int64_t N, int fmt,
+                               const float* scale, uint8_t* q, uint8_t* q_t, float* dbias, float* amax,
+                               unsigned long long* sat, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+hipError_t launch_gated_backward(const void* dh, int xtype, const uint16_t* gu, int act, int64_t M, int64_t F, int fmt,
+                                 const float* scale, uint8_t* q, uint8_t* q_t, float* amax, unsigned long long* sat,
+                                 void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+hipError_t launch_gemm_fused(const uint8_t* A, int fa, const uint8_t* B, int fb, int64_t M, int64_t N, int64_t K,
+                             const float* sinv_a, const float* sinv_b, const EpiArgs& epi, int accum,
+                             hipStream_t stream);
+
+hipError_t launch_gemm_gated(const uint8_t* A, int fa, const uint8_t* B, int fb, int64_t M, int64_t F, int64_t K,
+                             const float* sinv_a, const float* sinv_b, const EpiArgs& epi, int accum,
+                             hipStream_t stream);
 
 }  // namespace fp8mi

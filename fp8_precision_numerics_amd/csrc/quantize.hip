@@ -24,6 +24,8 @@
 
 #include "device_common.hpp"
 #include "launch.hpp"
+#include "stats.hpp"
+#include "transpose.hpp"
 
 namespace fp8mi {
 namespace {
@@ -37,40 +39,6 @@ __global__ void zero_outputs_kernel(uint32_t* amax_bits, unsigned long long* sat
   if (threadIdx.x == 0) {
     if (amax_bits) *amax_bits = 0u;
     if (sat) *sat = 0ull;
-  }
-}
-
-// Fold (per-lane amax bits, per-wave saturation count) into the global outputs:
-// either one partial per workgroup (`partials` non-null: slot blockIdx.x gets
-// {amax bits, 0, count lo, count hi}, reduced afterwards by
-// reduce_partials_kernel) or device-scope atomics on the outputs.  The atomics
-// on one address are serialised across the chip (about 4 ns each on MI355X,
-// ~4 us for a 512-workgroup grid); the partials cost one tiny extra kernel.
-__device__ __forceinline__ void block_finish(uint32_t amx, uint32_t wave_cnt, uint32_t* amax_bits,
-                                             unsigned long long* sat, uint4* partials) {
-  __shared__ uint32_t s_max[kWaves];
-  __shared__ uint32_t s_cnt[kWaves];
-  amx = wave_max_u32(amx);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  if (lane == 0) {
-    s_max[wave] = amx;
-    s_cnt[wave] = wave_cnt;
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    uint32_t m = s_max[0];
-    unsigned long long c = s_cnt[0];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) {
-      m = m > s_max[w] ? m : s_max[w];
-      c += s_cnt[w];
-    }
-    if (partials) {
-      partials[blockIdx.x] = make_uint4(m, 0u, (uint32_t)c, (uint32_t)(c >> 32));
-    } else {
-      if (amax_bits) atomicMax(amax_bits, m);
-      if (sat && c) atomicAdd(sat, c);
-    }
   }
 }
 
@@ -163,6 +131,23 @@ __global__ __launch_bounds__(kThreads) void reduce_partials_kernel(const uint4* 
   }
   if (hs.status && flags) *hs.status |= flags;
 }
+
+}  // namespace
+
+hipError_t launch_clear_stats(float* amax, unsigned long long* sat, hipStream_t stream) {
+  hipLaunchKernelGGL(zero_outputs_kernel, dim3(1), dim3(64), 0, stream, reinterpret_cast<uint32_t*>(amax), sat);
+  return hipGetLastError();
+}
+
+hipError_t launch_reduce_stats(const void* partials, int count, float* amax, unsigned long long* sat,
+                               hipStream_t stream) {
+  hipLaunchKernelGGL(reduce_partials_kernel, dim3(1), dim3(kThreads), 0, stream,
+                     reinterpret_cast<const uint4*>(partials), count, reinterpret_cast<uint32_t*>(amax), sat,
+                     HistoryArgs{});
+  return hipGetLastError();
+}
+
+namespace {
 
 // One fp32 value copied on the device (stream-ordered, capturable).
 __global__ void copy_scalar_kernel(const float* __restrict__ src, float* __restrict__ dst) {
@@ -373,7 +358,7 @@ __global__ __launch_bounds__(kThreads) void quantize_flat_kernel(
     }
     if constexpr (WQ) q[i] = encode1<FMT>(p);
   }
-  block_finish(amx, wcnt, amax_bits, sat, partials);
+  block_finish<kWaves>(amx, wcnt, amax_bits, sat, partials);
 }
 
 // ---------------------------------------------------------------------------
@@ -384,22 +369,6 @@ __global__ __launch_bounds__(kThreads) void quantize_flat_kernel(
 // stores into 4 rows of q_t (eight lanes cover 128 contiguous bytes of one
 // q_t row).  Requires rows % 16 == 0 and cols % 16 == 0.
 // ---------------------------------------------------------------------------
-constexpr int kTile = 128;
-constexpr int kPitch = 132;
-
-__device__ __forceinline__ void transpose4x4(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, uint32_t& c0,
-                                             uint32_t& c1, uint32_t& c2, uint32_t& c3) {
-  // w_r holds columns 0..3 of row r (byte k = column k); c_k gets rows 0..3 of column k.
-  const uint32_t t0 = __builtin_amdgcn_perm(w1, w0, 0x05010400u);  // w0.b0 w1.b0 w0.b1 w1.b1
-  const uint32_t t1 = __builtin_amdgcn_perm(w3, w2, 0x05010400u);  // w2.b0 w3.b0 w2.b1 w3.b1
-  const uint32_t t2 = __builtin_amdgcn_perm(w1, w0, 0x07030602u);  // w0.b2 w1.b2 w0.b3 w1.b3
-  const uint32_t t3 = __builtin_amdgcn_perm(w3, w2, 0x07030602u);  // w2.b2 w3.b2 w2.b3 w3.b3
-  c0 = __builtin_amdgcn_perm(t1, t0, 0x05040100u);
-  c1 = __builtin_amdgcn_perm(t1, t0, 0x07060302u);
-  c2 = __builtin_amdgcn_perm(t3, t2, 0x05040100u);
-  c3 = __builtin_amdgcn_perm(t3, t2, 0x07060302u);
-}
-
 template <int XT, int FMT, bool WQ, bool SAT>
 __global__ __launch_bounds__(kThreads) void quantize_transpose_kernel(
     const void* __restrict__ x, int64_t rows, int64_t cols, const float* __restrict__ scale,
@@ -482,25 +451,10 @@ __global__ __launch_bounds__(kThreads) void quantize_transpose_kernel(
     }
   }
   __syncthreads();
-  {
-    const int rg = t & 7, cq = t >> 3;
-    const int64_t c = col0 + cq * 4, r = row0 + rg * 16;
-    if (c < cols && r < rows) {
-      uint32_t w[16];
-#pragma unroll
-      for (int j = 0; j < 16; ++j) w[j] = *reinterpret_cast<const uint32_t*>(tile + (rg * 16 + j) * kPitch + cq * 4);
-      uint32_t o[4][4];
-#pragma unroll
-      for (int b = 0; b < 4; ++b)
-        transpose4x4(w[4 * b], w[4 * b + 1], w[4 * b + 2], w[4 * b + 3], o[b][0], o[b][1], o[b][2], o[b][3]);
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        *reinterpret_cast<uint4*>(q_t + (c + k) * rows + r) = make_uint4(o[0][k], o[1][k], o[2][k], o[3][k]);
-    }
-  }
+  transposed_store(tile, q_t, rows, cols, row0, col0, t);
   __syncthreads();  // the LDS tile is rewritten by the next iteration
   }
-  block_finish(amx, wcnt, amax_bits, sat, partials);
+  block_finish<kWaves>(amx, wcnt, amax_bits, sat, partials);
 }
 
 // ---------------------------------------------------------------------------

@@ -1,0 +1,96 @@
+// The amax (as fp32 bits) and saturation count of an FP8 output, gathered over
+// a grid: lanes to workgroup here, workgroups to the outputs either through one
+// 16-byte partial per workgroup, reduced afterwards by reduce_partials_kernel
+// (quantize.hip), or by device-scope atomics.  Both are a maximum and an integer
+// sum, so the result does not depend on the order.
+#pragma once
+
+#include "device_common.hpp"
+
+namespace fp8mi {
+
+// Fold (per-lane amax bits, per-wave saturation count) into the global outputs:
+// either one partial per workgroup (`partials` non-null: slot blockIdx.x gets
+// {amax bits, 0, count lo, count hi}, reduced afterwards by
+// reduce_partials_kernel) or device-scope atomics on the outputs.  The atomics
+// on one address are serialised across the chip (about 4 ns each on MI355X,
+// ~4 us for a 512-workgroup grid); the partials cost one tiny extra kernel.
+template <int WAVES>
+__device__ __forceinline__ void block_finish(uint32_t amx, uint32_t wave_cnt, uint32_t* amax_bits,
+                                             unsigned long long* sat, uint4* partials) {
+  __shared__ uint32_t s_max[WAVES];
+  __shared__ uint32_t s_cnt[WAVES];
+  amx = wave_max_u32(amx);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (lane == 0) {
+    s_max[wave] = amx;
+    s_cnt[wave] = wave_cnt;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    uint32_t m = s_max[0];
+    unsigned long long c = s_cnt[0];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) {
+      m = m > s_max[w] ? m : s_max[w];
+      c += s_cnt[w];
+    }
+    if (partials) {
+      partials[blockIdx.x] = make_uint4(m, 0u, (uint32_t)c, (uint32_t)(c >> 32));
+    } else {
+      if (amax_bits) atomicMax(amax_bits, m);
+      if (sat && c) atomicAdd(sat, c);
+    }
+  }
+}
+
+// One lane's running amax and saturation count over the values it encodes.
+// The common case (no NaN among the scaled values) takes the short encoder and a
+// float maximum; otherwise the full rule and bit-pattern maxima (NaN above Inf).
+struct LaneStats {
+  float maxf = 0.0f;
+  uint32_t max_bits = 0u;
+  uint32_t sat = 0u;
+  __device__ __forceinline__ uint32_t amax() const {
+    const uint32_t m = f2u(maxf);  // non-negative floats order as their bit patterns
+    return m > max_bits ? m : max_bits;
+  }
+};
+
+// Codes of eight values y times `scale` (byte i of the pair = value i).  STATS:
+// also folds |y| and the count of |y * scale| > max into `st`.
+template <int FMT, bool STATS>
+__device__ __forceinline__ uint2 encode8(const float* y, float scale, LaneStats& st) {
+  float p[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) p[e] = y[e] * scale;
+  if constexpr (STATS) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) st.sat += __builtin_fabsf(p[e]) > Fp8Traits<FMT>::max_value ? 1u : 0u;
+  }
+  // A NaN among the products shows in their sum (as do opposite infinities,
+  // which then only take the longer way to the same codes).
+  const float t = ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+  uint2 c;
+  if (__builtin_expect(t == t, 1)) {
+    c.x = encode4_finite<FMT>(p[0], p[1], p[2], p[3]);
+    c.y = encode4_finite<FMT>(p[4], p[5], p[6], p[7]);
+    if constexpr (STATS) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) st.maxf = __builtin_fmaxf(st.maxf, __builtin_fabsf(y[e]));
+    }
+  } else {
+    c.x = encode4<FMT>(p[0], p[1], p[2], p[3]);
+    c.y = encode4<FMT>(p[4], p[5], p[6], p[7]);
+    if constexpr (STATS) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t m = f2u(y[e]) & 0x7FFFFFFFu;
+        st.max_bits = m > st.max_bits ? m : st.max_bits;
+      }
+    }
+  }
+  return c;
+}
+
+}  // namespace fp8mi

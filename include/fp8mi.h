@@ -78,7 +78,9 @@ typedef enum {
   FP8MI_ERR_DTYPE = -5,   /* unknown fp8mi_dtype                                 */
   FP8MI_ERR_LAUNCH = -6,  /* the HIP runtime rejected a kernel launch            */
   FP8MI_ERR_DEVICE = -7,  /* no usable gfx950 device is current                  */
-  FP8MI_ERR_ACCUM = -8    /* unknown fp8mi_accum                                 */
+  FP8MI_ERR_ACCUM = -8,   /* unknown fp8mi_accum                                 */
+  FP8MI_ERR_ACT = -9,     /* unknown fp8mi_activation                            */
+  FP8MI_ERR_WORKSPACE = -10 /* the workspace is too small for what was asked     */
 } fp8mi_status;
 
 /* Human-readable name of a status code (static storage; never NULL). */
@@ -399,6 +401,166 @@ FP8MI_API int fp8_quantize_blockwise(const void* x, int xtype, int64_t rows, int
 FP8MI_API int fp8_grouped_gemm(const uint8_t* A, const float* sinv_a, const uint8_t* B, const float* sinv_b,
                      const int32_t* m_offsets, int32_t G, int64_t total_m, int64_t N, int64_t K,
                      void* C, int ctype, int accum, void* stream);
+
+/*
+ * The feed-forward operators around the GEMM: the norm in front of it, the
+ * gated projections, the product with its epilogue, and their gradients.
+ *
+ * Activations, all taken in fp32:
+ *   FP8MI_ACT_NONE  z
+ *   FP8MI_ACT_RELU  max(z, 0)
+ *   FP8MI_ACT_SILU  z / (1 + exp(-z))
+ *   FP8MI_ACT_GELU  z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2
+ * A NaN stays NaN.  `workspace` is scratch of the caller, 16-B aligned, as for
+ * fp8_quantize: its contents on entry do not matter, and two calls in flight at
+ * once must not share one.  bf16 arguments are bit patterns (uint16_t).
+ */
+typedef enum { FP8MI_ACT_NONE = 0, FP8MI_ACT_RELU = 1, FP8MI_ACT_SILU = 2, FP8MI_ACT_GELU = 3 } fp8mi_activation;
+typedef enum { FP8MI_OUT_F32 = 0, FP8MI_OUT_BF16 = 1, FP8MI_OUT_E4M3 = 2, FP8MI_OUT_E5M2 = 3 } fp8mi_output;
+
+/*
+ * fp8_rmsnorm_quantize — residual addition, root-mean-square norm and the cast
+ * with a given (delayed) scale, in one pass over the row.
+ *
+ *   h = round_to_xtype(x + residual)            (x without a residual)
+ *   r = 1 / sqrt(mean over the row of h^2 + eps)  (fp32 sums)
+ *   y = h * r * weight                          (fp32)
+ *   q = round_to_fp8(fp32(y * scale)), as fp8_quantize
+ *   amax = max |y| (bit patterns: NaN above Inf), sat = #{ |y * scale| > max }
+ *
+ * x, residual  device, [rows x cols] of xtype; residual may be NULL.
+ * weight       device, [cols] of xtype.
+ * scale        device, 1 fp32.
+ * sum_out      device, [rows x cols] of xtype, receives h; or NULL.  Needs a
+ *              residual.  It may be x or the residual itself (updated in place).
+ * q            device, [rows x cols] uint8.
+ * rstd         device, [rows] fp32, receives r (what the gradient needs); or NULL.
+ * amax, sat    device, 1 fp32 / 1 uint64, overwritten, or NULL.
+ * workspace    device scratch or NULL: with it the statistics are gathered in up
+ *              to workspace_bytes / 16 slots, without it with atomics.
+ * cols must be a multiple of 16; x, residual, weight, sum_out and q 16-B aligned;
+ * eps >= 0.  rows * cols may be 0 (then amax = 0 and sat = 0).
+ */
+FP8MI_API int fp8_rmsnorm_quantize(const void* x, const void* residual, const void* weight, int xtype, int64_t rows,
+                         int64_t cols, float eps, int fmt, const float* scale, void* sum_out, uint8_t* q, float* rstd,
+                         float* amax, unsigned long long* sat, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * fp8_rmsnorm_quantize_blockwise — the same with current scaling per 128 values
+ * of a row, as fp8_quantize_blockwise with block_rows = 1 (the A operand of
+ * fp8_grouped_gemm).
+ *
+ * scale_inv  device, [rows x ceil(cols/128)] fp32.
+ */
+FP8MI_API int fp8_rmsnorm_quantize_blockwise(const void* x, const void* residual, const void* weight, int xtype,
+                                   int64_t rows, int64_t cols, float eps, int fmt, void* sum_out, uint8_t* q,
+                                   float* scale_inv, float* rstd, void* stream);
+
+/*
+ * fp8_rmsnorm_backward — gradient of y = h * r * weight.
+ *
+ *   g = dy * weight
+ *   dx = round_to_xtype(r * (g - h * r^2 * mean over the row of (g * h)) + dresidual)
+ *   dweight[n] = sum over the rows of dy * h * r
+ *
+ * dy, h       device, [rows x cols] of xtype (h: the forward's sum_out, or its x).
+ * rstd        device, [rows] fp32, from the forward.
+ * weight      device, [cols] of xtype.
+ * dresidual   device, [rows x cols] of xtype, the gradient that reaches h past the
+ *             norm (the residual branch's), or NULL.
+ * dx          device, [rows x cols] of xtype: the gradient of h, hence of x and of
+ *             the forward's residual.  It may be dy or dresidual itself.
+ * dweight     device, [cols] fp32, overwritten, or NULL.
+ * workspace   device scratch, needed with dweight: one fp32 row of cols values per
+ *             workgroup (at least one row, else FP8MI_ERR_WORKSPACE; up to 1024
+ *             rows are used).  The sums' order is fixed for a given device, shape
+ *             and workspace size.
+ * cols must be a multiple of 16; all 16-B aligned.
+ */
+FP8MI_API int fp8_rmsnorm_backward(const void* dy, const void* h, const float* rstd, const void* weight,
+                         const void* dresidual, int xtype, int64_t rows, int64_t cols, void* dx, float* dweight,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * fp8_gemm_gated — gated feed-forward product, both projections in one kernel.
+ *
+ *   s = sinv_a * sinv_b
+ *   g[m][f] = s * sum_k dec_fa(A[m][k]) dec_fb(B[f][k])
+ *   u[m][f] = s * sum_k dec_fa(A[m][k]) dec_fb(B[F + f][k])
+ *   h = act(g) * u                                (fp32, then rounded as htype says)
+ *
+ * A          device, [M x K] codes.
+ * B          device, [2F x K] codes: the gate's F rows, then the up projection's.
+ * h          device, [M x F] of htype (fp8mi_output); FP8: round_to_fp8(fp32(h * out_scale)).
+ * out_scale  device, 1 fp32, needed for FP8 outputs.
+ * gu         device, [M x 2F] bf16, receives g and u (what the gradient needs), or NULL.
+ * amax, sat  device, of the unscaled h / of h * out_scale, overwritten, or NULL; FP8 outputs only.
+ * accum      fp8mi_accum, as for fp8_gemm.  Products of at most 64 rows use the exact
+ *            arithmetic in both modes.
+ * workspace  device scratch or NULL: products of few tiles are split along K over
+ *            it where that pays.
+ * K must be a multiple of 16, K <= 2^23; A, B, h, gu 16-B aligned.  Any M and F.
+ */
+FP8MI_API int fp8_gemm_gated(const uint8_t* A, int fa, const uint8_t* B, int fb, int64_t M, int64_t F, int64_t K,
+                   const float* sinv_a, const float* sinv_b, int act, void* h, int htype, const float* out_scale,
+                   uint16_t* gu, float* amax, unsigned long long* sat, int accum, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/*
+ * fp8_gemm_fused — matrix product with bias, activation and residual.
+ *
+ *   z = sinv_a * sinv_b * sum_k dec_fa(A[m][k]) dec_fb(B[n][k]) + bias[n]
+ *   y = act(z) + residual[m][n]                   (fp32, then rounded as ytype says)
+ *
+ * A, B       device, [M x K] and [N x K] codes.
+ * bias       device, [N] bf16, or NULL.
+ * residual   device, [M x N] bf16, or NULL; may be y where y is bf16.
+ * y          device, [M x N] of ytype (fp8mi_output), as h of fp8_gemm_gated.
+ * z          device, [M x N] bf16, receives z (what the gradient needs), or NULL.
+ * The other arguments and the rules are fp8_gemm_gated's; bias and residual are
+ * 16-B aligned.
+ */
+FP8MI_API int fp8_gemm_fused(const uint8_t* A, int fa, const uint8_t* B, int fb, int64_t M, int64_t N, int64_t K,
+                   const float* sinv_a, const float* sinv_b, const uint16_t* bias, int act, const uint16_t* residual,
+                   void* y, int ytype, const float* out_scale, uint16_t* z, float* amax, unsigned long long* sat,
+                   int accum, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * fp8_act_backward — gradient through fp8_gemm_fused's epilogue, cast for the two
+ * gradient GEMMs.
+ *
+ *   d = dy * act'(z),   q = round_to_fp8(fp32(d * scale)),   dbias[n] = sum_m d
+ *
+ * dy         device, [M x N] of xtype.
+ * z          device, [M x N] bf16, from the forward; not read where act is FP8MI_ACT_NONE (may be NULL).
+ * scale      device, 1 fp32.
+ * q          device, [M x N] uint8 (A operand of the data gradient), or NULL.
+ * q_t        device, [N x M] uint8 (A operand of the weight gradient), or NULL; needs M a multiple of 16.
+ * dbias      device, [N] fp32, overwritten, or NULL.
+ * amax, sat  device, of the unscaled d / of d * scale, overwritten, or NULL.
+ * workspace  device scratch, needed with dbias (at least one fp32 row of N values, else
+ *            FP8MI_ERR_WORKSPACE; more rows let more workgroups run); the statistics
+ *            take what is left of it.
+ * One of q, q_t, dbias, amax, sat is needed.  N must be a multiple of 16; dy, z, q and
+ * q_t 16-B aligned.  The sums' order is fixed, as fp8_rmsnorm_backward's.
+ */
+FP8MI_API int fp8_act_backward(const void* dy, int xtype, const uint16_t* z, int act, int64_t M, int64_t N, int fmt,
+                     const float* scale, uint8_t* q, uint8_t* q_t, float* dbias, float* amax, unsigned long long* sat,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * fp8_gated_backward — gradient through fp8_gemm_gated's epilogue.
+ *
+ *   d = [ dh * u * act'(g) | dh * act(g) ]   [M x 2F],   q = round_to_fp8(fp32(d * scale))
+ *
+ * dh         device, [M x F] of xtype.
+ * gu         device, [M x 2F] bf16, from the forward.
+ * q, q_t     device, [M x 2F] and [2F x M] uint8, or NULL.
+ * The other arguments and the rules are fp8_act_backward's, F in the place of N.
+ */
+FP8MI_API int fp8_gated_backward(const void* dh, int xtype, const uint16_t* gu, int act, int64_t M, int64_t F, int fmt,
+                       const float* scale, uint8_t* q, uint8_t* q_t, float* amax, unsigned long long* sat,
+                       void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }
