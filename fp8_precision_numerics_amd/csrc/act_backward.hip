@@ -41,28 +41,26 @@ struct BackArgs {
   int walks;             // workgroups per column strip
 };
 
-// Eight consecutive values of a row-major matrix, widened.
+// Eight consecutive values of a row-major matrix as loaded (nontemporal: read once).
 template <int XT>
-__device__ __forceinline__ void load8f(const void* p, int64_t elem, float* f) {
-  if constexpr (XT == kBF16) {
-    const uint4 v = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p) + elem);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      f[2 * k] = bf16_lo(w[k]);
-      f[2 * k + 1] = bf16_hi(w[k]);
-    }
-  } else {
-    const float4 a = reinterpret_cast<const float4*>(p)[elem / 4], b = reinterpret_cast<const float4*>(p)[elem / 4 + 1];
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+struct Raw8 {
+  typedef unsigned int vec4 __attribute__((ext_vector_type(4)));
+  vec4 v[XT == kBF16 ? 1 : 2];
+  __device__ __forceinline__ void load(const void* p, uint32_t elem) {
+    const vec4* src = reinterpret_cast<const vec4*>(reinterpret_cast<const uint8_t*>(p) + elem * (XT == kBF16 ? 2u : 4u));
+    v[0] = __builtin_nontemporal_load(src);
+    if constexpr (XT == kF32) v[1] = __builtin_nontemporal_load(src + 1);
   }
-}
+  __device__ __forceinline__ float get(int k) const {
+    if constexpr (XT == kBF16) return (k & 1) ? bf16_hi(v[0][k >> 1]) : bf16_lo(v[0][k >> 1]);
+    else return u2f(v[k >> 2][k & 3]);
+  }
+};
 
 // Tile 0 of LDS holds the codes of d (gated: of the gate's part), tile 1 those of
 // the up projection's part.
 template <int XT, int FMT, int ACT, bool GATED, bool STATS>
-__global__ __launch_bounds__(kNT) void act_backward_kernel(BackArgs a) {
+__global__ __launch_bounds__(kNT, 4) void act_backward_kernel(BackArgs a) {
   constexpr int TILES = GATED ? 2 : 1;
   __shared__ __attribute__((aligned(16))) uint8_t tile[TILES][kTile * kPitch];
   const int t = threadIdx.x;
@@ -72,60 +70,75 @@ __global__ __launch_bounds__(kNT) void act_backward_kernel(BackArgs a) {
   const int64_t col0 = strip * kTile, c = col0 + vi * 8;
   const int64_t ldq = GATED ? 2 * a.N : a.N;
   const int64_t row_tiles = (a.M + kTile - 1) / kTile;
+  const uint32_t off_n = (uint32_t)(rr0 * a.N + vi * 8), off_q = (uint32_t)(rr0 * ldq + vi * 8);
   const float s = *a.scale;
   LaneStats st;
   float db[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   for (int64_t rt = walk; rt < row_tiles; rt += a.walks) {
     const int64_t row0 = rt * kTile;
-    // Four passes' loads are issued before the first is used.
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      float dy[4][8], z[4][8], u[GATED ? 4 : 1][8];
+    // Pass i covers rows row0 + 16 i + rr0.  Addresses: a uniform base per pass plus the
+    // lane's 32-bit offset, the same for every pass.  Four passes' loads are issued
+    // before the first is used, held as they were loaded: widened, they took 256
+    // registers and left one wave a SIMD (416 us against @US@ us for 8192 x 2 x 16384).
+    auto passes = [&](int i0, auto whole) {
+      Raw8<XT> dy[4];
+      Raw8<kBF16> z[4], u[GATED ? 4 : 1];
+      auto inside = [&](int i) { return decltype(whole)::value || (row0 + i * 16 + rr0 < a.M && c < a.N); };
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int64_t r = row0 + rr0 + (half * 4 + i) * 16;
-        if (r < a.M && c < a.N) {
-          load8f<XT>(a.dy, r * a.N + c, dy[i]);
+        const int64_t base = row0 + (i0 + i) * 16;
+        if (inside(i0 + i)) {
+          dy[i].load(reinterpret_cast<const uint8_t*>(a.dy) + (base * a.N + col0) * (XT == kBF16 ? 2 : 4), off_n);
           if constexpr (GATED) {
-            load8f<kBF16>(a.z, r * ldq + c, z[i]);
-            load8f<kBF16>(a.z, r * ldq + a.N + c, u[i]);
+            z[i].load(a.z + base * ldq + col0, off_q);
+            u[i].load(a.z + base * ldq + a.N + col0, off_q);
           } else if constexpr (ACT != kActNone) {
-            load8f<kBF16>(a.z, r * a.N + c, z[i]);
+            z[i].load(a.z + base * a.N + col0, off_n);
           }
         }
       }
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int rr = rr0 + (half * 4 + i) * 16;
-        const int64_t r = row0 + rr;
-        if (r < a.M && c < a.N) {
+        const int64_t base = row0 + (i0 + i) * 16;
+        if (inside(i0 + i)) {
           float d[8], e[GATED ? 8 : 1];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             float val, slope;
-            act_value_slope<ACT>(ACT == kActNone && !GATED ? 0.0f : z[i][k], &val, &slope);
+            const float g = dy[i].get(k);
             if constexpr (GATED) {
-              d[k] = dy[i][k] * u[i][k] * slope;
-              e[k] = dy[i][k] * val;
+              act_value_slope<ACT>(z[i].get(k), &val, &slope);
+              d[k] = g * u[i].get(k) * slope;
+              e[k] = g * val;
+            } else if constexpr (ACT != kActNone) {
+              act_value_slope<ACT>(z[i].get(k), &val, &slope);
+              d[k] = g * slope;
             } else {
-              d[k] = ACT == kActNone ? dy[i][k] : dy[i][k] * slope;
-              db[k] += d[k];
+              d[k] = g;
             }
+            if constexpr (!GATED) db[k] += d[k];
           }
-          const uint2 cd = encode8<FMT, STATS>(d, s, st);
-          if (a.q) *reinterpret_cast<uint2*>(a.q + r * ldq + c) = cd;
-          uint32_t* dst = reinterpret_cast<uint32_t*>(tile[0] + rr * kPitch + vi * 8);
-          dst[0] = cd.x;
-          dst[1] = cd.y;
-          if constexpr (GATED) {
-            const uint2 ce = encode8<FMT, STATS>(e, s, st);
-            if (a.q) *reinterpret_cast<uint2*>(a.q + r * ldq + a.N + c) = ce;
-            uint32_t* up = reinterpret_cast<uint32_t*>(tile[TILES - 1] + rr * kPitch + vi * 8);
-            up[0] = ce.x;
-            up[1] = ce.y;
-          }
+          auto put = [&](const float* f, int h) {
+            const uint2 cd = encode8<FMT>(f, s, STATS, STATS && a.sat, st);
+            if (a.q) *reinterpret_cast<uint2*>(a.q + base * ldq + h * a.N + col0 + off_q) = cd;
+            if (a.q_t) {
+              uint32_t* dst = reinterpret_cast<uint32_t*>(tile[h] + ((i0 + i) * 16 + rr0) * kPitch + vi * 8);
+              dst[0] = cd.x;
+              dst[1] = cd.y;
+            }
+          };
+          put(d, 0);
+          if constexpr (GATED) put(e, TILES - 1);
         }
+        __builtin_amdgcn_sched_barrier(0);  // one pass's values at a time: mixed, the passes spill
       }
+    };
+    const bool interior = row0 + kTile <= a.M && col0 + kTile <= a.N;
+#pragma unroll 1
+    for (int i0 = 0; i0 < 8; i0 += 4) {
+      if (interior) passes(i0, std::true_type{});
+      else passes(i0, std::false_type{});
     }
     if (a.q_t) {  // M and N are multiples of 16 here
       __syncthreads();

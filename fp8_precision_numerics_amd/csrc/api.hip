@@ -15,6 +15,7 @@ constexpr int64_t kMaxDim = 0x7FFFFFFF;             // kernels index rows/cols w
 constexpr int64_t kMaxGemmK = int64_t(1) << 23;     // 256 rows x K bytes of a tile slab in a 32-bit buffer offset
 constexpr int64_t kMaxGroupedK = int64_t(1) << 22;  // 512 rows x K bytes (the grouped kernels' widest slab)
 constexpr int64_t kMaxBufferBytes = 0x7FFFFFFF;     // any offset a buffer load carries in one 32-bit register
+constexpr int64_t kMaxBackCols = int64_t(1) << 25;  // 16 rows of d in a 32-bit byte offset (fp32)
 constexpr int64_t kMaxElems = (int64_t)1 << 40;     // sanity bound on any one tensor
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_device_ok[kMaxDevices];         // 0 unknown, 1 gfx950, -1 not usable
@@ -352,7 +353,7 @@ int check_act_back(const void* dy, int xtype, const uint16_t* z, bool need_z, in
   if (!dtype_ok(xtype)) return FP8MI_ERR_DTYPE;
   if (!fmt_ok(fmt)) return FP8MI_ERR_FORMAT;
   if (!act_ok(act)) return FP8MI_ERR_ACT;
-  if (!dims_ok(M, ld) || ld > kMaxDim || (M + 127) / 128 > kMaxDim) return FP8MI_ERR_SHAPE;
+  if (!dims_ok(M, ld) || ld > kMaxBackCols || (M + 127) / 128 > kMaxDim) return FP8MI_ERR_SHAPE;
   if ((N & 15) != 0 || (q_t && (M & 15) != 0)) return FP8MI_ERR_ALIGN;
   if (!q && !q_t && !stats) return FP8MI_ERR_NULL;
   if (workspace && (!aligned16(workspace) || workspace_bytes < 16)) return FP8MI_ERR_ALIGN;
@@ -425,8 +426,9 @@ int fp8_gemm_gated(const uint8_t* A, int fa, const uint8_t* B, int fb, int64_t M
   if (bad != FP8MI_OK || nothing) return bad;
   const int dev = check_device();
   if (dev != FP8MI_OK) return dev;
-  const fp8mi::EpiArgs epi{h, gu, nullptr, nullptr, out_scale, reinterpret_cast<uint32_t*>(amax), sat, act, htype};
-  return launched(fp8mi::launch_gemm_gated(A, fa, B, fb, M, F, K, sinv_a, sinv_b, epi, accum, (hipStream_t)stream));
+  const fp8mi::EpiArgs epi{h, gu, nullptr, nullptr, out_scale, reinterpret_cast<uint32_t*>(amax), sat, act, htype, nullptr, 1};
+  return launched(fp8mi::launch_gemm_gated(A, fa, B, fb, M, F, K, sinv_a, sinv_b, epi, accum, workspace, workspace_bytes,
+                                           (hipStream_t)stream));
 }
 
 int fp8_gemm_fused(const uint8_t* A, int fa, const uint8_t* B, int fb, int64_t M, int64_t N, int64_t K,
@@ -441,8 +443,9 @@ int fp8_gemm_fused(const uint8_t* A, int fa, const uint8_t* B, int fb, int64_t M
   if (!aligned16(bias) || !aligned16(residual)) return FP8MI_ERR_ALIGN;
   const int dev = check_device();
   if (dev != FP8MI_OK) return dev;
-  const fp8mi::EpiArgs epi{y, z, bias, residual, out_scale, reinterpret_cast<uint32_t*>(amax), sat, act, ytype};
-  return launched(fp8mi::launch_gemm_fused(A, fa, B, fb, M, N, K, sinv_a, sinv_b, epi, accum, (hipStream_t)stream));
+  const fp8mi::EpiArgs epi{y, z, bias, residual, out_scale, reinterpret_cast<uint32_t*>(amax), sat, act, ytype, nullptr, 1};
+  return launched(fp8mi::launch_gemm_fused(A, fa, B, fb, M, N, K, sinv_a, sinv_b, epi, accum, workspace, workspace_bytes,
+                                           (hipStream_t)stream));
 }
 
 int fp8_act_backward(const void* dy, int xtype, const uint16_t* z, int act, int64_t M, int64_t N, int fmt,

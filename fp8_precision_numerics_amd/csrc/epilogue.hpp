@@ -30,6 +30,11 @@ struct EpiArgs {
   unsigned long long* sat;  // may be null
   int act;
   int out;                  // kF32, kBF16, kYE4M3, kYE5M2
+  // Split products: `split` workgroups share a tile's K, and each writes its fp32
+  // sums (not yet scaled) to partials [split x M x N] (gated [split x M x 2N]),
+  // which epilogue_partials_kernel adds up and finishes.  1: no split.
+  float* partials;
+  int split;
 };
 
 template <class T>
@@ -128,12 +133,8 @@ __device__ __forceinline__ void epilogue8(const EpiArgs& a, float* c, const floa
       for (int e = 0; e < 8; ++e)
         if (e >= left) c[e] = 0.0f;
     }
-    uint2 q;
-    if (a.amax_bits || a.sat) {
-      q = a.out == kYE4M3 ? encode8<kE4M3, true>(c, scale, st) : encode8<kE5M2, true>(c, scale, st);
-    } else {
-      q = a.out == kYE4M3 ? encode8<kE4M3, false>(c, scale, st) : encode8<kE5M2, false>(c, scale, st);
-    }
+    const bool amax = a.amax_bits != nullptr, sat = a.sat != nullptr;
+    const uint2 q = a.out == kYE4M3 ? encode8<kE4M3>(c, scale, amax, sat, st) : encode8<kE5M2>(c, scale, amax, sat, st);
     uint8_t* y = reinterpret_cast<uint8_t*>(a.y) + m * N + n;
     if (vec) {
       typedef unsigned int vec2 __attribute__((ext_vector_type(2)));
@@ -195,7 +196,11 @@ __device__ __forceinline__ void publish_epilogue_stats(const EpiArgs& a, const L
 // layout), taken out eight columns at a time.  Gated tiles hold PAIR gate columns,
 // then the same PAIR columns of the up projection, and so on; an output tile is
 // BN / 2 wide.  A thread keeps its columns over its rows, so it loads the bias
-// once; its residual values are requested before the pass is staged.
+// once; its residual values are requested two rows ahead, the first two before the
+// pass is staged.
+// The row loop is rolled on purpose: unrolled, the kernel had 85 KiB of code, each
+// instruction of the epilogue ran once a pass, and fetching them from memory cost
+// about 40 us a launch (2048 x 4096 x 4096: @ROLLED@).
 template <int BN, int NT, int PASS, int PAIR, class TW>
 struct EpiPass {
   static constexpr bool GATED = PAIR != 0;
@@ -205,55 +210,94 @@ struct EpiPass {
   static_assert(NT % CPR == 0 && PASS % SWEEP == 0, "whole sweeps");
   const EpiArgs& a;
   int64_t M, N, m0, n;
-  int c, r0, left;
+  int r0, left, col;
   bool vec;
   float bias[8];
-  uint4 res[GATED ? 1 : ROWS];
+  uint4 res[2];
   float scale;
   __device__ __forceinline__ EpiPass(const EpiArgs& a_, int64_t M_, int64_t N_, int64_t m_base, int64_t n_base, int t)
       : a(a_), M(M_), N(N_), m0(m_base) {
-    c = t % CPR;
+    const int c = t % CPR;
     r0 = t / CPR;
     n = n_base + c * 8;
+    constexpr int P = GATED ? PAIR : 8;
+    col = GATED ? (c * 8 / P) * 2 * P + c * 8 % P : c * 8;  // staged column of the first value
     left = n < N ? (int)(N - n < 8 ? N - n : 8) : 0;
     vec = (N & 7) == 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) bias[e] = 0.0f;
+    uint4 b = make_uint4(0u, 0u, 0u, 0u);
     if constexpr (!GATED) {
-      if (a.bias && left) unpack_bf16x8(load_bf16x8(a.bias + n, vec, left), bias);
+      if (a.bias && left) b = load_bf16x8(a.bias + n, vec, left);
     }
+    unpack_bf16x8(b, bias);
+    res[0] = res[1] = make_uint4(0u, 0u, 0u, 0u);
     scale = (a.out == kYE4M3 || a.out == kYE5M2) ? *a.out_scale : 1.0f;
   }
-  __device__ __forceinline__ void prefetch(int pass_row) {
+  __device__ __forceinline__ void request(int pass_row, int i, uint4* to) const {
     if constexpr (!GATED) {
+      const int64_t m = m0 + pass_row + r0 + i * SWEEP;
+      if (a.residual && left && i < ROWS && m < M) *to = load_bf16x8(a.residual + m * N + n, vec, left);
+    }
+  }
+  __device__ __forceinline__ void prefetch(int pass_row) {
+    if (a.split > 1) return;
+    request(pass_row, 0, &res[0]);
+    request(pass_row, 1, &res[1]);
+  }
+  __device__ __forceinline__ void take(const TW& tw, int r, int from, float* to) const {
 #pragma unroll
-      for (int i = 0; i < ROWS; ++i) {
-        const int64_t m = m0 + pass_row + r0 + i * SWEEP;
-        res[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (a.residual && left && m < M) res[i] = load_bf16x8(a.residual + m * N + n, vec, left);
+    for (int h = 0; h < 2; ++h) {
+      const v4f f = *reinterpret_cast<const v4f*>(tw.lds + tw.pos(r, (from + 4 * h) * 4));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) to[4 * h + e] = f[e];
+    }
+  }
+  // A split product's pass: the sums as they are, into this part's partials.
+  __device__ __forceinline__ void flush_partials(const TW& tw, int pass_row, float* partials) const {
+    if (!left) return;
+    const int64_t ld = GATED ? 2 * N : N;
+#pragma unroll 1
+    for (int r = r0; r < PASS; r += SWEEP) {
+      const int64_t m = m0 + pass_row + r;
+      if (m >= M) break;
+#pragma unroll
+      for (int p = 0; p < (GATED ? 2 : 1); ++p) {
+        float* dst = partials + m * ld + p * N + n;
+        float v[8];
+        take(tw, r, col + p * PAIR, v);
+        if (vec) {
+          reinterpret_cast<v4f*>(dst)[0] = (v4f){v[0], v[1], v[2], v[3]};
+          reinterpret_cast<v4f*>(dst)[1] = (v4f){v[4], v[5], v[6], v[7]};
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (e < left) dst[e] = v[e];
+        }
       }
     }
   }
-  __device__ __forceinline__ void flush(const TW& tw, int pass_row, LaneStats& st) const {
+  __device__ __forceinline__ void flush(const TW& tw, int pass_row, LaneStats& st) {
     if (!left) return;
-#pragma unroll
+    // the next row's values come from LDS while the present row is worked on
+    float nv[8], nu[GATED ? 8 : 1];
+    take(tw, r0, col, nv);
+    if constexpr (GATED) take(tw, r0, col + PAIR, nu);
+#pragma unroll 1
     for (int i = 0; i < ROWS; ++i) {
       const int r = r0 + i * SWEEP;
       const int64_t m = m0 + pass_row + r;
       if (m >= M) break;
-      float v[8], up[GATED ? 8 : 1], rs[8];
-      const int col = GATED ? (c * 8 / (GATED ? PAIR : 1)) * 2 * PAIR + c * 8 % (GATED ? PAIR : 1) : c * 8;
-      auto take = [&](int from, float* to) {
+      float v[8], up[8], rs[8];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const v4f f = *reinterpret_cast<const v4f*>(tw.lds + tw.pos(r, (from + 4 * h) * 4));
-#pragma unroll
-          for (int e = 0; e < 4; ++e) to[4 * h + e] = f[e];
-        }
-      };
-      take(col, v);
-      if constexpr (GATED) take(col + PAIR, up);
-      else unpack_bf16x8(res[i], rs);
+      for (int e = 0; e < 8; ++e) {
+        v[e] = nv[e];
+        if constexpr (GATED) up[e] = nu[e];
+      }
+      unpack_bf16x8(res[0], rs);
+      res[0] = res[1];
+      request(pass_row, i + 2, &res[1]);
+      const int rn = i + 1 < ROWS ? r + SWEEP : r;
+      take(tw, rn, col, nv);
+      if constexpr (GATED) take(tw, rn, col + PAIR, nu);
       epilogue8<GATED>(a, v, up, bias, rs, m, n, N, vec, left, scale, st);
     }
   }

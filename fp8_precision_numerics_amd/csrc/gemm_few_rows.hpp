@@ -8,7 +8,7 @@
 namespace fp8mi {
 
 // Rows that the kernel takes at most.
-constexpr int64_t kFewRows = 64;
+constexpr int64_t kFewRows = 16;
 
 // A [M x K], B [N x K] (gated: [2N x K]) codes, K contiguous; M in [1, kFewRows].
 hipError_t launch_gemm_few_rows(const uint8_t* A, int fa, const uint8_t* B, int fb, int64_t M, int64_t N, int64_t K,

@@ -15,10 +15,11 @@ namespace fp8mi {
 
 hipError_t launch_gemm_gated(const uint8_t* A, int fa, const uint8_t* B, int fb, int64_t M, int64_t N, int64_t K,
                              const float* sinv_a, const float* sinv_b, const EpiArgs& args, int accum,
-                             hipStream_t stream) {
+                             void* workspace, size_t workspace_bytes, hipStream_t stream) {
   GatedEpi epi;
   static_cast<EpiArgs&>(epi) = args;
-  return epi_launch(A, fa, B, fb, M, N, K, sinv_a, sinv_b, epi, accum, stream);
+  epi.partials = reinterpret_cast<float*>(workspace);
+  return epi_launch(A, fa, B, fb, M, N, K, sinv_a, sinv_b, epi, accum, workspace ? workspace_bytes : 0, stream);
 }
 
 }  // namespace fp8mi

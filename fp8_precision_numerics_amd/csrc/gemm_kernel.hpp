@@ -590,23 +590,41 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(
   __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * STAGE + (MXE ? kMxRefBytes : 0)];
 
   int tm, tn;
-  tile_coords(blockIdx.x, tiles_m, tiles_n, group_m, &tm, &tn);
+  int pid = blockIdx.x, part = 0;
+  if constexpr (EPI) {  // a split product: the parts of K one after the other
+    part = pid / (tiles_m * tiles_n);
+    pid -= part * (tiles_m * tiles_n);
+  }
+  tile_coords(pid, tiles_m, tiles_n, group_m, &tm, &tn);
   const int t = threadIdx.x, lane = t & 63;
   const int w = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wm = w / WN, wn = w % WN;
   const int64_t m_base = (int64_t)tm * BM, n_base = (int64_t)tn * OUT_BN;
-  const int nk = (K + kBK - 1) / kBK;
-  const bool ragged_k = (K % kBK) != 0;
+  // K steps kt0 .. kt0 + nk - 1 (all of them, unless split), the last one ragged or not.
+  int nk = (K + kBK - 1) / kBK, kt0 = 0;
+  bool ragged_k = (K % kBK) != 0;
+  if constexpr (EPI) {
+    if (rq.split > 1) {
+      const int per = (nk + rq.split - 1) / rq.split;
+      kt0 = part * per;
+      if (kt0 + per < nk) {
+        nk = per;
+        ragged_k = false;
+      } else {
+        nk = nk - kt0;  // at least 1: the launcher leaves no part empty
+      }
+    }
+  }
 
   const SlabLoader<BM, BN, NW, BT, PAIR> slabs(A, m_base, M, B, n_base, N, K, w, lane);
   static_assert(!BT || !MXS, "MXFP8 operands are K-contiguous");
   auto issue_direct = [&](uint8_t* dst, int kt, int g) {
-    slabs.issue(dst, kt, g);
+    slabs.issue(dst, kt + kt0, g);
     if constexpr (MXS) {
       if (g == 0) MxScaleLoader<BM, BN, NW>(mxs, m_base, M, n_base, N, K, w, lane).issue(dst + SLABS, kt);
     }
   };
-  auto stage_ragged = [&](int kt, int stage) { slabs.ragged(smem + stage * STAGE, kt, t); };
+  auto stage_ragged = [&](int kt, int stage) { slabs.ragged(smem + stage * STAGE, kt + kt0, t); };
 
   // Fragment reads.  FP8 path (16x16x128): lane l takes row l & 15 of a
   // 16-row block and the 32-byte K slice l >> 4 (granules 2h, 2h+1).  bf16
@@ -630,7 +648,8 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(
 
   uint8_t* const s0 = smem;
   uint8_t* const s1 = smem + STAGE;
-  const int nfull = K / kBK;
+  int nfull = K / kBK;
+  if constexpr (EPI) nfull = ragged_k ? nk - 1 : nk;  // of this part
 
   // Four outputs c (already x sinv_a x sinv_b) of tile row r, columns n..n+3,
   // into the staged pass (row r - r_lo).  The FP8 outputs are round_to_fp8 of
@@ -695,17 +714,21 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(
     TW tw{smem, PASS};
     if constexpr (EPI) {
       EpiPass<BN, NT, PASS, PAIR, TW> pass(rq, M, N, m_base, n_base, t);
+      const bool whole = rq.split <= 1;
+      float* partials = rq.partials + (whole ? 0 : (int64_t)part * M * (GATED ? 2 * (int64_t)N : (int64_t)N));
       LaneStats st;
-      const uint32_t seen = rq.amax_bits ? __hip_atomic_load(rq.amax_bits, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0u;
+      const uint32_t seen =
+          whole && rq.amax_bits ? __hip_atomic_load(rq.amax_bits, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0u;
 #pragma unroll 1
       for (int r0 = 0; r0 < BM; r0 += PASS) {
         pass.prefetch(r0);
         __syncthreads();
         emit(r0, r0 + PASS, tw);
         __syncthreads();
-        pass.flush(tw, r0, st);
+        if (whole) pass.flush(tw, r0, st);
+        else pass.flush_partials(tw, r0, partials);
       }
-      if (rq.amax_bits || rq.sat) publish_epilogue_stats(rq, st, seen, lane);
+      if (whole && (rq.amax_bits || rq.sat)) publish_epilogue_stats(rq, st, seen, lane);
     } else {
 #pragma unroll 1
       for (int r0 = 0; r0 < BM; r0 += PASS) {
@@ -825,7 +848,8 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(
     // Lane l holds row m = l & 15 of each 16x16 block (the A operand went
     // second) and columns n = 4(l >> 4) .. +3.  MXFP8 carries its scales in
     // the instruction: no per-tensor factor.
-    const float sc = MX ? 1.0f : sinv_a[0] * sinv_b[0];
+    float sc = MX ? 1.0f : sinv_a[0] * sinv_b[0];
+    if constexpr (EPI) sc = rq.split > 1 ? 1.0f : sc;
     write_tile_checked([&](int r_lo, int r_hi, auto& tw, auto mask) {
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
@@ -992,7 +1016,8 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(
     // second) and columns n = 8g + 4(l >> 5) + 0..3 in registers 4g..4g+3.
     // kAccumMxExact: the result is acc * 2^(R_a - 127) * 2^(R_b - 127), in
     // that order (each step exact unless the result leaves fp32's range).
-    const float sc = MXE ? 1.0f : sinv_a[0] * sinv_b[0];
+    float sc = MXE ? 1.0f : sinv_a[0] * sinv_b[0];
+    if constexpr (EPI) sc = rq.split > 1 ? 1.0f : sc;
     const float* fac = reinterpret_cast<const float*>(refs + 512);
     write_tile_checked([&](int r_lo, int r_hi, auto& tw, auto mask) {
 #pragma unroll

@@ -116,10 +116,10 @@ hipError_t launch_gated_backward(const void* dh, int xtype, const uint16_t* gu, 
 
 hipError_t launch_gemm_fused(const uint8_t* A, int fa, const uint8_t* B, int fb, int64_t M, int64_t N, int64_t K,
                              const float* sinv_a, const float* sinv_b, const EpiArgs& epi, int accum,
-                             hipStream_t stream);
+                             void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 hipError_t launch_gemm_gated(const uint8_t* A, int fa, const uint8_t* B, int fb, int64_t M, int64_t F, int64_t K,
                              const float* sinv_a, const float* sinv_b, const EpiArgs& epi, int accum,
-                             hipStream_t stream);
+                             void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 }  // namespace fp8mi

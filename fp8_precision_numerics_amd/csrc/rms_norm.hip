@@ -13,15 +13,15 @@
 //
 // HBM-bound: the forward reads x (and the residual) once and writes the sum and
 // the codes once, because a row stays in registers between the sum of squares
-// and the encode.  A row belongs to TPR lanes (a wavefront for rows up to 2048
-// values, so that its sum takes shuffles only; a workgroup of 256 or 512 beyond),
-// VPT groups of eight consecutive values ("octets") each.  The grid walks the
+// and the encode.  A row of up to 1024 values belongs to a wavefront (its sum takes
+// shuffles only), one of up to 16384 to a workgroup just large enough for two groups
+// of eight consecutive values ("octets") a thread.  The grid walks the
 // rows, so the weight is loaded once per workgroup and the gradient's dweight
 // stays in registers: one fp32 partial row per workgroup goes to the workspace,
 // and a second kernel adds them in a fixed order.  Rows too long for the
 // registers are read twice (the second time mostly from the caches).
 // Sums of squares and of products are fp32: per lane over its octets, then across
-// lanes, so a sum of N terms is rounded about N / TPR + log2(TPR) times deep.
+// lanes, so a term of a row of up to 16384 values passes through at most about 40 roundings.
 #include "device_common.hpp"
 #include "launch.hpp"
 #include "stats.hpp"
@@ -78,20 +78,21 @@ struct Octet {
   }
 };
 
-// Sum over the TPR lanes of a row; every lane gets it.  More than a wavefront:
-// through LDS, in two buffers used in turn, so that one barrier a row is enough
-// (a wave that is a row ahead writes the other buffer).
-template <int TPR>
-__device__ __forceinline__ float row_sum(float v, float (*buf)[TPR / 64 > 0 ? TPR / 64 : 1], int turn) {
+// Sum over the lanes of a row; every lane gets it.  WG: the row is the whole
+// workgroup's: through LDS, in two buffers used in turn, so that one barrier a row
+// is enough (a wave that is a row ahead writes the other buffer).  Otherwise it is
+// one wave's.
+constexpr int kMaxWaves = 16;
+template <bool WG>
+__device__ __forceinline__ float row_sum(float v, float (*buf)[kMaxWaves], int turn) {
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
-  if constexpr (TPR > 64) {
-    constexpr int W = TPR / 64;
+  if constexpr (WG) {
+    const int waves = blockDim.x >> 6;
     if ((threadIdx.x & 63) == 0) buf[turn & 1][threadIdx.x >> 6] = v;
     __syncthreads();
     v = buf[turn & 1][0];
-#pragma unroll
-    for (int w = 1; w < W; ++w) v += buf[turn & 1][w];
+    for (int w = 1; w < waves; ++w) v += buf[turn & 1][w];
   }
   return v;
 }
@@ -146,17 +147,18 @@ __device__ __forceinline__ void norm_encode(const NormArgs& a, const Octet<XT>& 
     if (valid && (o & 15) == 0) a.scale_inv[row * ((octets + 15) / 16) + (o >> 4)] = si;
   }
   if (valid) {
-    const uint2 c = encode8<FMT, KIND == kNormStats>(y, scale, st);
+    const uint2 c = encode8<FMT>(y, scale, KIND == kNormStats, KIND == kNormStats && a.sat, st);
     *reinterpret_cast<uint2*>(a.q + row * a.cols + o * 8) = c;
   }
 }
 
-template <int XT, int FMT, int KIND, int TPR, int VPT, int NT>
-__global__ __launch_bounds__(NT) void rmsnorm_kernel(NormArgs a) {
-  constexpr int RPB = NT / TPR;  // rows side by side in a workgroup
-  static_assert(TPR == 64 || TPR == NT, "the barrier of a row's sum needs the whole workgroup on one row");
-  __shared__ float buf[2][TPR / 64];
-  const int t = threadIdx.x % TPR;
+// WG: a row per workgroup, whose size fits the row; otherwise a row per wavefront, four
+// side by side.
+template <int XT, int FMT, int KIND, bool WG, int VPT>
+__global__ __launch_bounds__(WG ? 1024 : 256) void rmsnorm_kernel(NormArgs a) {
+  __shared__ float buf[2][kMaxWaves];
+  const int TPR = WG ? blockDim.x : 64, RPB = WG ? 1 : 4;
+  const int t = WG ? threadIdx.x : threadIdx.x & 63;
   const int64_t octets = a.cols / 8;
   const float scale = KIND == kNormBlocks ? 1.0f : *a.scale;
   const float inv_n = 1.0f / (float)a.cols;
@@ -168,7 +170,7 @@ __global__ __launch_bounds__(NT) void rmsnorm_kernel(NormArgs a) {
   }
   LaneStats st;
   int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; row < a.rows; row += (int64_t)gridDim.x * RPB) {
+  for (int64_t row = (int64_t)blockIdx.x * RPB + (WG ? 0 : threadIdx.x >> 6); row < a.rows; row += (int64_t)gridDim.x * RPB) {
     const int64_t base = row * octets;
     Octet<XT> h[VPT];
 #pragma unroll
@@ -202,7 +204,7 @@ __global__ __launch_bounds__(NT) void rmsnorm_kernel(NormArgs a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(f[e], f[e], ss);
     }
-    ss = row_sum<TPR>(ss, buf, turn++);
+    ss = row_sum<WG>(ss, buf, turn++);
     const float r = 1.0f / __builtin_sqrtf(ss * inv_n + a.eps);
     if (a.rstd && t == 0) a.rstd[row] = r;
 #pragma unroll
@@ -211,7 +213,7 @@ __global__ __launch_bounds__(NT) void rmsnorm_kernel(NormArgs a) {
       norm_encode<XT, FMT, KIND>(a, h[v], wt[v], r, scale, row, o, octets, o < octets, st);
     }
   }
-  if constexpr (KIND == kNormStats) block_finish<NT / 64>(st.amax(), wave_sum_u32(st.sat), a.amax_bits, a.sat, a.partials);
+  if constexpr (KIND == kNormStats) block_finish(st.amax(), wave_sum_u32(st.sat), a.amax_bits, a.sat, a.partials);
 }
 
 // Rows of any length: a workgroup per row, two passes over it.  The second pass
@@ -219,7 +221,7 @@ __global__ __launch_bounds__(NT) void rmsnorm_kernel(NormArgs a) {
 // since x or the residual may be the buffer that the sum has overwritten.
 template <int XT, int FMT, int KIND, int NT>
 __global__ __launch_bounds__(NT) void rmsnorm_long_kernel(NormArgs a) {
-  __shared__ float buf[2][NT / 64];
+  __shared__ float buf[2][kMaxWaves];
   const int t = threadIdx.x;
   const int64_t octets = a.cols / 8;
   const float scale = KIND == kNormBlocks ? 1.0f : *a.scale;
@@ -252,7 +254,7 @@ __global__ __launch_bounds__(NT) void rmsnorm_long_kernel(NormArgs a) {
       for (int e = 0; e < 8; ++e) part = __builtin_fmaf(f[e], f[e], part);
       ss += part;
     }
-    ss = row_sum<NT>(ss, buf, turn++);
+    ss = row_sum<true>(ss, buf, turn++);
     const float r = 1.0f / __builtin_sqrtf(ss / (float)a.cols + a.eps);
     if (a.rstd && t == 0) a.rstd[row] = r;
     // whole workgroup passes, so that the 16 lanes of a block meet in its shuffles
@@ -269,7 +271,7 @@ __global__ __launch_bounds__(NT) void rmsnorm_long_kernel(NormArgs a) {
       norm_encode<XT, FMT, KIND>(a, h, wt, r, scale, row, o, octets, o < octets, st);
     }
   }
-  if constexpr (KIND == kNormStats) block_finish<NT / 64>(st.amax(), wave_sum_u32(st.sat), a.amax_bits, a.sat, a.partials);
+  if constexpr (KIND == kNormStats) block_finish(st.amax(), wave_sum_u32(st.sat), a.amax_bits, a.sat, a.partials);
 }
 
 // ---------------------------------------------------------------------------
@@ -286,12 +288,11 @@ struct NormBackArgs {
   int64_t rows, cols;
 };
 
-template <int XT, int TPR, int VPT, int NT>
-__global__ __launch_bounds__(NT) void rmsnorm_backward_kernel(NormBackArgs a) {
-  constexpr int RPB = NT / TPR;
-  static_assert(TPR == 64 || TPR == NT, "the barrier of a row's sum needs the whole workgroup on one row");
-  __shared__ float buf[2][TPR / 64];
-  const int t = threadIdx.x % TPR;
+template <int XT, bool WG, int VPT>
+__global__ __launch_bounds__(WG ? 1024 : 256) void rmsnorm_backward_kernel(NormBackArgs a) {
+  __shared__ float buf[2][kMaxWaves];
+  const int TPR = WG ? blockDim.x : 64, RPB = WG ? 1 : 4;
+  const int t = WG ? threadIdx.x : threadIdx.x & 63;
   const int64_t octets = a.cols / 8;
   const float inv_n = 1.0f / (float)a.cols;
   float w[VPT][8], dw[VPT][8];
@@ -305,7 +306,7 @@ __global__ __launch_bounds__(NT) void rmsnorm_backward_kernel(NormBackArgs a) {
     for (int e = 0; e < 8; ++e) dw[v][e] = 0.0f;
   }
   int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; row < a.rows; row += (int64_t)gridDim.x * RPB) {
+  for (int64_t row = (int64_t)blockIdx.x * RPB + (WG ? 0 : threadIdx.x >> 6); row < a.rows; row += (int64_t)gridDim.x * RPB) {
     const int64_t base = row * octets;
     Octet<XT> dy[VPT], h[VPT], dr[VPT];
     const float r = a.rstd[row];
@@ -332,7 +333,7 @@ __global__ __launch_bounds__(NT) void rmsnorm_backward_kernel(NormBackArgs a) {
         dw[v][e] = __builtin_fmaf(d[e], f[e] * r, dw[v][e]);
       }
     }
-    gh = row_sum<TPR>(gh, buf, turn++);
+    gh = row_sum<WG>(gh, buf, turn++);
     const float k = gh * inv_n * r * r;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
@@ -349,22 +350,22 @@ __global__ __launch_bounds__(NT) void rmsnorm_backward_kernel(NormBackArgs a) {
     }
   }
   if (!a.partials) return;
-  if constexpr (RPB > 1) {
+  if constexpr (!WG) {
     // the rows side by side add up in LDS, in a fixed order
-    __shared__ float sum[RPB][TPR * VPT * 8];
-    float* mine = sum[threadIdx.x / TPR];
+    __shared__ float sum[4][64 * VPT * 8];
+    float* mine = sum[threadIdx.x >> 6];
 #pragma unroll
     for (int v = 0; v < VPT; ++v)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) mine[(v * 8 + e) * TPR + t] = dw[v][e];
+      for (int e = 0; e < 8; ++e) mine[(v * 8 + e) * 64 + t] = dw[v][e];
     __syncthreads();
-    if (threadIdx.x >= TPR) return;
+    if (threadIdx.x >= 64) return;
 #pragma unroll
     for (int v = 0; v < VPT; ++v)
 #pragma unroll
       for (int e = 0; e < 8; ++e)
 #pragma unroll
-        for (int g = 1; g < RPB; ++g) dw[v][e] += sum[g][(v * 8 + e) * TPR + t];
+        for (int g = 1; g < 4; ++g) dw[v][e] += sum[g][(v * 8 + e) * 64 + t];
   }
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
@@ -379,7 +380,7 @@ __global__ __launch_bounds__(NT) void rmsnorm_backward_kernel(NormBackArgs a) {
 // row (each lane its own columns, so no two lanes meet at an address).
 template <int XT, int NT>
 __global__ __launch_bounds__(NT) void rmsnorm_backward_long_kernel(NormBackArgs a) {
-  __shared__ float buf[2][NT / 64];
+  __shared__ float buf[2][kMaxWaves];
   const int t = threadIdx.x;
   const int64_t octets = a.cols / 8;
   float* part = a.partials ? a.partials + (int64_t)blockIdx.x * a.cols : nullptr;
@@ -402,7 +403,7 @@ __global__ __launch_bounds__(NT) void rmsnorm_backward_long_kernel(NormBackArgs 
       for (int e = 0; e < 8; ++e) acc = __builtin_fmaf(d[e] * w[e], f[e], acc);
       gh += acc;
     }
-    gh = row_sum<NT>(gh, buf, turn++);
+    gh = row_sum<true>(gh, buf, turn++);
     const float k = gh / (float)a.cols * r * r;
     for (int64_t o = t; o < octets; o += NT) {
       Octet<XT> dy, h, wt, dr, out;
@@ -452,22 +453,23 @@ int row_groups(int64_t rows, int rpb, int per_cu, int64_t slots) {
   return g < 1 ? 1 : (int)g;
 }
 
-template <int XT, int FMT, int KIND, int TPR, int VPT, int NT>
-int norm_go(const NormArgs& a, int64_t slots, hipStream_t st) {
-  const int g = row_groups(a.rows, NT / TPR, 2048 / NT, slots);
-  hipLaunchKernelGGL((rmsnorm_kernel<XT, FMT, KIND, TPR, VPT, NT>), dim3((unsigned)g), dim3(NT), 0, st, a);
-  return g;
-}
+// Threads of a workgroup that holds a row in two octets a thread.
+int row_threads(int64_t octets) { return (int)((octets + 127) / 128 * 64); }
 
 template <int XT, int FMT, int KIND>
 int norm_run(const NormArgs& a, int64_t slots, hipStream_t st) {
   const int64_t o = a.cols / 8;
-  if (o <= 64) return norm_go<XT, FMT, KIND, 64, 1, 256>(a, slots, st);
-  if (o <= 128) return norm_go<XT, FMT, KIND, 64, 2, 256>(a, slots, st);
-  if (o <= 256) return norm_go<XT, FMT, KIND, 64, 4, 256>(a, slots, st);
-  if (o <= 512) return norm_go<XT, FMT, KIND, 256, 2, 256>(a, slots, st);
-  if (o <= 1024) return norm_go<XT, FMT, KIND, 256, 4, 256>(a, slots, st);
-  if (o <= 2048) return norm_go<XT, FMT, KIND, 512, 4, 512>(a, slots, st);
+  if (o <= 128) {
+    const int g = row_groups(a.rows, 4, 8, slots);
+    if (o <= 64) hipLaunchKernelGGL((rmsnorm_kernel<XT, FMT, KIND, false, 1>), dim3((unsigned)g), dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((rmsnorm_kernel<XT, FMT, KIND, false, 2>), dim3((unsigned)g), dim3(256), 0, st, a);
+    return g;
+  }
+  if (o <= 2048) {
+    const int nt = row_threads(o), g = row_groups(a.rows, 1, 2048 / nt, slots);
+    hipLaunchKernelGGL((rmsnorm_kernel<XT, FMT, KIND, true, 2>), dim3((unsigned)g), dim3(nt), 0, st, a);
+    return g;
+  }
   const int g = row_groups(a.rows, 1, 2, slots);
   hipLaunchKernelGGL((rmsnorm_long_kernel<XT, FMT, KIND, 1024>), dim3((unsigned)g), dim3(1024), 0, st, a);
   return g;
@@ -486,22 +488,20 @@ int norm_launch(const NormArgs& a, int xtype, int fmt, int kind, int64_t slots, 
   return fmt == kE4M3 ? norm_kind<kF32, kE4M3>(a, kind, slots, st) : norm_kind<kF32, kE5M2>(a, kind, slots, st);
 }
 
-template <int XT, int TPR, int VPT, int NT>
-int norm_back_go(const NormBackArgs& a, int64_t slots, hipStream_t st) {
-  const int g = row_groups(a.rows, NT / TPR, 1024 / NT, slots);
-  hipLaunchKernelGGL((rmsnorm_backward_kernel<XT, TPR, VPT, NT>), dim3((unsigned)g), dim3(NT), 0, st, a);
-  return g;
-}
-
 template <int XT>
 int norm_back_run(const NormBackArgs& a, int64_t slots, hipStream_t st) {
   const int64_t o = a.cols / 8;
-  if (o <= 64) return norm_back_go<XT, 64, 1, 256>(a, slots, st);
-  if (o <= 128) return norm_back_go<XT, 64, 2, 256>(a, slots, st);
-  if (o <= 256) return norm_back_go<XT, 256, 1, 256>(a, slots, st);
-  if (o <= 512) return norm_back_go<XT, 256, 2, 256>(a, slots, st);
-  if (o <= 1024) return norm_back_go<XT, 512, 2, 512>(a, slots, st);
-  if (o <= 2048) return norm_back_go<XT, 1024, 2, 1024>(a, slots, st);
+  if (o <= 128) {
+    const int g = row_groups(a.rows, 4, 4, slots);
+    if (o <= 64) hipLaunchKernelGGL((rmsnorm_backward_kernel<XT, false, 1>), dim3((unsigned)g), dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((rmsnorm_backward_kernel<XT, false, 2>), dim3((unsigned)g), dim3(256), 0, st, a);
+    return g;
+  }
+  if (o <= 2048) {
+    const int nt = row_threads(o), g = row_groups(a.rows, 1, 1024 / nt, slots);
+    hipLaunchKernelGGL((rmsnorm_backward_kernel<XT, true, 2>), dim3((unsigned)g), dim3(nt), 0, st, a);
+    return g;
+  }
   const int g = row_groups(a.rows, 1, 1, slots);
   hipLaunchKernelGGL((rmsnorm_backward_long_kernel<XT, 1024>), dim3((unsigned)g), dim3(1024), 0, st, a);
   return g;

@@ -15,13 +15,13 @@ namespace fp8mi {
 // reduce_partials_kernel) or device-scope atomics on the outputs.  The atomics
 // on one address are serialised across the chip (about 4 ns each on MI355X,
 // ~4 us for a 512-workgroup grid); the partials cost one tiny extra kernel.
-template <int WAVES>
+template <int MAX_WAVES = 16>
 __device__ __forceinline__ void block_finish(uint32_t amx, uint32_t wave_cnt, uint32_t* amax_bits,
                                              unsigned long long* sat, uint4* partials) {
-  __shared__ uint32_t s_max[WAVES];
-  __shared__ uint32_t s_cnt[WAVES];
+  __shared__ uint32_t s_max[MAX_WAVES];
+  __shared__ uint32_t s_cnt[MAX_WAVES];
   amx = wave_max_u32(amx);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;  // at most MAX_WAVES of them
   if (lane == 0) {
     s_max[wave] = amx;
     s_cnt[wave] = wave_cnt;
@@ -30,8 +30,8 @@ __device__ __forceinline__ void block_finish(uint32_t amx, uint32_t wave_cnt, ui
   if (threadIdx.x == 0) {
     uint32_t m = s_max[0];
     unsigned long long c = s_cnt[0];
-#pragma unroll
-    for (int w = 1; w < WAVES; ++w) {
+    const int waves = MAX_WAVES < (int)(blockDim.x >> 6) ? MAX_WAVES : (int)(blockDim.x >> 6);
+    for (int w = 1; w < waves; ++w) {
       m = m > s_max[w] ? m : s_max[w];
       c += s_cnt[w];
     }
@@ -57,14 +57,14 @@ struct LaneStats {
   }
 };
 
-// Codes of eight values y times `scale` (byte i of the pair = value i).  STATS:
-// also folds |y| and the count of |y * scale| > max into `st`.
-template <int FMT, bool STATS>
-__device__ __forceinline__ uint2 encode8(const float* y, float scale, LaneStats& st) {
+// Codes of eight values y times `scale` (byte i of the pair = value i); |y| and the
+// count of |y * scale| > max are folded into `st` where asked for.
+template <int FMT>
+__device__ __forceinline__ uint2 encode8(const float* y, float scale, bool amax, bool sat, LaneStats& st) {
   float p[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) p[e] = y[e] * scale;
-  if constexpr (STATS) {
+  if (sat) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) st.sat += __builtin_fabsf(p[e]) > Fp8Traits<FMT>::max_value ? 1u : 0u;
   }
@@ -75,14 +75,15 @@ __device__ __forceinline__ uint2 encode8(const float* y, float scale, LaneStats&
   if (__builtin_expect(t == t, 1)) {
     c.x = encode4_finite<FMT>(p[0], p[1], p[2], p[3]);
     c.y = encode4_finite<FMT>(p[4], p[5], p[6], p[7]);
-    if constexpr (STATS) {
+    if (amax) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) st.maxf = __builtin_fmaxf(st.maxf, __builtin_fabsf(y[e]));
+      for (int e = 0; e < 8; e += 2)
+        st.maxf = __builtin_fmaxf(__builtin_fmaxf(__builtin_fabsf(y[e]), __builtin_fabsf(y[e + 1])), st.maxf);
     }
   } else {
     c.x = encode4<FMT>(p[0], p[1], p[2], p[3]);
     c.y = encode4<FMT>(p[4], p[5], p[6], p[7]);
-    if constexpr (STATS) {
+    if (amax) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const uint32_t m = f2u(y[e]) & 0x7FFFFFFFu;

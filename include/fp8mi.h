@@ -495,7 +495,7 @@ FP8MI_API int fp8_rmsnorm_backward(const void* dy, const void* h, const float* r
  * out_scale  device, 1 fp32, needed for FP8 outputs.
  * gu         device, [M x 2F] bf16, receives g and u (what the gradient needs), or NULL.
  * amax, sat  device, of the unscaled h / of h * out_scale, overwritten, or NULL; FP8 outputs only.
- * accum      fp8mi_accum, as for fp8_gemm.  Products of at most 64 rows use the exact
+ * accum      fp8mi_accum, as for fp8_gemm.  Products of at most 16 rows use the exact
  *            arithmetic in both modes.
  * workspace  device scratch or NULL: products of few tiles are split along K over
  *            it where that pays.
@@ -541,7 +541,7 @@ FP8MI_API int fp8_gemm_fused(const uint8_t* A, int fa, const uint8_t* B, int fb,
  * workspace  device scratch, needed with dbias (at least one fp32 row of N values, else
  *            FP8MI_ERR_WORKSPACE; more rows let more workgroups run); the statistics
  *            take what is left of it.
- * One of q, q_t, dbias, amax, sat is needed.  N must be a multiple of 16; dy, z, q and
+ * One of q, q_t, dbias, amax, sat is needed.  N must be a multiple of 16, N <= 2^25; dy, z, q and
  * q_t 16-B aligned.  The sums' order is fixed, as fp8_rmsnorm_backward's.
  */
 FP8MI_API int fp8_act_backward(const void* dy, int xtype, const uint16_t* z, int act, int64_t M, int64_t N, int fmt,
@@ -556,7 +556,7 @@ FP8MI_API int fp8_act_backward(const void* dy, int xtype, const uint16_t* z, int
  * dh         device, [M x F] of xtype.
  * gu         device, [M x 2F] bf16, from the forward.
  * q, q_t     device, [M x 2F] and [2F x M] uint8, or NULL.
- * The other arguments and the rules are fp8_act_backward's, F in the place of N.
+ * The other arguments and the rules are fp8_act_backward's, F in the place of N (2F <= 2^25).
  */
 FP8MI_API int fp8_gated_backward(const void* dh, int xtype, const uint16_t* gu, int act, int64_t M, int64_t F, int fmt,
                        const float* scale, uint8_t* q, uint8_t* q_t, float* amax, unsigned long long* sat,
