@@ -167,28 +167,29 @@ __global__ __launch_bounds__(kNT, 4) void act_backward_kernel(BackArgs a) {
   if constexpr (STATS) block_finish<kNT / 64>(st.amax(), wave_sum_u32(st.sat), a.amax_bits, a.sat, a.stat_slots);
 }
 
-// out[n] = sum over the rows of partials [count x cols]: 16 columns a workgroup,
-// 16 lanes down the rows of each, then a tree in LDS.
-__global__ __launch_bounds__(256) void column_sums_kernel(const float* __restrict__ partials, int count, int64_t cols,
-                                                          float* __restrict__ out) {
-  __shared__ float buf[16][17];
+// out[n] = sum over the rows of partials [count x cols]: 16 columns a workgroup, 64
+// lanes down the rows of each, then a tree in LDS.
+constexpr int kSumLanes = 64;
+__global__ __launch_bounds__(16 * kSumLanes) void column_sums_kernel(const float* __restrict__ partials, int count,
+                                                                    int64_t cols, float* __restrict__ out) {
+  __shared__ float buf[kSumLanes][17];
   const int cx = threadIdx.x & 15, ry = threadIdx.x >> 4;
   const int64_t c = (int64_t)blockIdx.x * 16 + cx;
   float v = 0.0f;
   if (c < cols) {
     int r = ry;
-    for (; r + 112 < count; r += 128) {
+    for (; r + 7 * kSumLanes < count; r += 8 * kSumLanes) {
       float p[8];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) p[u] = partials[(int64_t)(r + 16 * u) * cols + c];
+      for (int u = 0; u < 8; ++u) p[u] = partials[(int64_t)(r + u * kSumLanes) * cols + c];
       v += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
     }
-    for (; r < count; r += 16) v += partials[(int64_t)r * cols + c];
+    for (; r < count; r += kSumLanes) v += partials[(int64_t)r * cols + c];
   }
   buf[ry][cx] = v;
   __syncthreads();
 #pragma unroll
-  for (int half = 8; half > 0; half >>= 1) {
+  for (int half = kSumLanes / 2; half > 0; half >>= 1) {
     if (ry < half) buf[ry][cx] += buf[ry + half][cx];
     __syncthreads();
   }
@@ -258,7 +259,7 @@ hipError_t back_launch(BackArgs a, int xtype, int fmt, int act, float* dbias, fl
 
 hipError_t launch_column_sums(const float* partials, int count, int64_t cols, float* out, hipStream_t stream) {
   if (cols == 0) return hipSuccess;
-  hipLaunchKernelGGL(column_sums_kernel, dim3((unsigned)((cols + 15) / 16)), dim3(256), 0, stream, partials, count,
+  hipLaunchKernelGGL(column_sums_kernel, dim3((unsigned)((cols + 15) / 16)), dim3(16 * kSumLanes), 0, stream, partials, count,
                      cols, out);
   return hipGetLastError();
 }

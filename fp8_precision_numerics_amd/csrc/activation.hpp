@@ -20,18 +20,21 @@ namespace fp8mi {
 enum : int { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3 };
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kGeluA = 0.044715f;
-constexpr float kGelu2C = 1.5957691216057308f;  // 2 sqrt(2/pi)
+constexpr double kGelu2C = 1.5957691216057308, kGeluA = 0.044715;  // 2 sqrt(2/pi)
+// -2u log2(e) = z (kGeluK1 + kGeluK3 z^2)
+constexpr float kGeluK1 = (float)(-1.4426950408889634 * kGelu2C);
+constexpr float kGeluK3 = (float)(-1.4426950408889634 * kGelu2C * kGeluA);
 
-__device__ __forceinline__ float logistic(float x) {
-  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * x));
+// 1 / (1 + 2^x)
+__device__ __forceinline__ float inv_one_plus_exp2(float x) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x));
 }
 
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
   if constexpr (ACT == kActRelu) return z > 0.0f ? z : (z == z ? 0.0f : z);  // NaN stays NaN
-  else if constexpr (ACT == kActSilu) return z * logistic(z);
-  else if constexpr (ACT == kActGelu) return z * logistic(kGelu2C * (z + kGeluA * z * z * z));
+  else if constexpr (ACT == kActSilu) return z * inv_one_plus_exp2(-kLog2e * z);
+  else if constexpr (ACT == kActGelu) return z * inv_one_plus_exp2(z * __builtin_fmaf(z * z, kGeluK3, kGeluK1));
   else return z;
 }
 
@@ -46,14 +49,14 @@ __device__ __forceinline__ void act_value_slope(float z, float* value, float* sl
     *value = z > 0.0f ? z : (z == z ? 0.0f : z);
     *slope = z > 0.0f ? 1.0f : 0.0f;
   } else if constexpr (ACT == kActSilu) {
-    const float s = logistic(z), v = z * s;
+    const float s = inv_one_plus_exp2(-kLog2e * z), v = z * s;
     *value = v;
     *slope = s + v * (1.0f - s);
   } else if constexpr (ACT == kActGelu) {
     const float c = __builtin_amdgcn_fmed3f(z, -20.0f, 20.0f), c2 = c * c;
-    const float s = logistic(kGelu2C * (c + kGeluA * c2 * c)), v = z * s;
+    const float s = inv_one_plus_exp2(c * __builtin_fmaf(c2, kGeluK3, kGeluK1)), v = z * s;
     *value = v;
-    *slope = s + v * (1.0f - s) * (kGelu2C * (1.0f + 3.0f * kGeluA * c2));
+    *slope = s + v * (1.0f - s) * __builtin_fmaf(c2, (float)(3.0 * kGeluA * kGelu2C), (float)kGelu2C);
   } else {
     *value = z;
     *slope = 1.0f;

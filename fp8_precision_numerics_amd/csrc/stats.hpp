@@ -38,57 +38,48 @@ __device__ __forceinline__ void block_finish(uint32_t amx, uint32_t wave_cnt, ui
     if (partials) {
       partials[blockIdx.x] = make_uint4(m, 0u, (uint32_t)c, (uint32_t)(c >> 32));
     } else {
-      if (amax_bits) atomicMax(amax_bits, m);
+      // The output only grows, so an older value of it is a safe bound: the atomic is
+      // skipped where it would change nothing.
+      if (amax_bits && m > __hip_atomic_load(amax_bits, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT))
+        atomicMax(amax_bits, m);
       if (sat && c) atomicAdd(sat, c);
     }
   }
 }
 
 // One lane's running amax and saturation count over the values it encodes.
-// The common case (no NaN among the scaled values) takes the short encoder and a
-// float maximum; otherwise the full rule and bit-pattern maxima (NaN above Inf).
 struct LaneStats {
-  float maxf = 0.0f;
-  uint32_t max_bits = 0u;
+  float max = 0.0f;  // IEEE maximum of |y|: a NaN stays
   uint32_t sat = 0u;
-  __device__ __forceinline__ uint32_t amax() const {
-    const uint32_t m = f2u(maxf);  // non-negative floats order as their bit patterns
-    return m > max_bits ? m : max_bits;
-  }
+  // Non-negative floats order as their bit patterns, NaN above Inf.
+  __device__ __forceinline__ uint32_t amax() const { return f2u(max) & 0x7FFFFFFFu; }
 };
 
-// Codes of eight values y times `scale` (byte i of the pair = value i); |y| and the
+// Codes of eight values y times `scale` (byte i of the pair = value i); max |y| and the
 // count of |y * scale| > max are folded into `st` where asked for.
+// The eight magnitudes' maximum (V_MAXIMUM3_F32, which keeps a NaN) decides the way:
+// rounding is monotone, so where fp32(max |y| * scale) <= max no product saturates and
+// none is NaN, and the conversion instruction alone is the rule.
 template <int FMT>
 __device__ __forceinline__ uint2 encode8(const float* y, float scale, bool amax, bool sat, LaneStats& st) {
+  float m = __builtin_elementwise_maximum(__builtin_fabsf(y[0]), __builtin_fabsf(y[1]));
+#pragma unroll
+  for (int e = 2; e < 8; e += 2)
+    m = __builtin_elementwise_maximum(__builtin_elementwise_maximum(__builtin_fabsf(y[e]), __builtin_fabsf(y[e + 1])), m);
+  if (amax) st.max = __builtin_elementwise_maximum(st.max, m);
   float p[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) p[e] = y[e] * scale;
-  if (sat) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) st.sat += __builtin_fabsf(p[e]) > Fp8Traits<FMT>::max_value ? 1u : 0u;
-  }
-  // A NaN among the products shows in their sum (as do opposite infinities,
-  // which then only take the longer way to the same codes).
-  const float t = ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
   uint2 c;
-  if (__builtin_expect(t == t, 1)) {
-    c.x = encode4_finite<FMT>(p[0], p[1], p[2], p[3]);
-    c.y = encode4_finite<FMT>(p[4], p[5], p[6], p[7]);
-    if (amax) {
-#pragma unroll
-      for (int e = 0; e < 8; e += 2)
-        st.maxf = __builtin_fmaxf(__builtin_fmaxf(__builtin_fabsf(y[e]), __builtin_fabsf(y[e + 1])), st.maxf);
-    }
+  if (__builtin_expect(__builtin_fabsf(m * scale) <= Fp8Traits<FMT>::max_value, 1)) {
+    c.x = cvt_pk<FMT, true>(p[2], p[3], cvt_pk<FMT, false>(p[0], p[1], 0u));
+    c.y = cvt_pk<FMT, true>(p[6], p[7], cvt_pk<FMT, false>(p[4], p[5], 0u));
   } else {
     c.x = encode4<FMT>(p[0], p[1], p[2], p[3]);
     c.y = encode4<FMT>(p[4], p[5], p[6], p[7]);
-    if (amax) {
+    if (sat) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t m = f2u(y[e]) & 0x7FFFFFFFu;
-        st.max_bits = m > st.max_bits ? m : st.max_bits;
-      }
+      for (int e = 0; e < 8; ++e) st.sat += __builtin_fabsf(p[e]) > Fp8Traits<FMT>::max_value ? 1u : 0u;
     }
   }
   return c;

@@ -1,0 +1,117 @@
+"""One gated feed-forward block on FP8 operands: residual addition and norm, gate
+and up projections with activation and product, down projection with the
+residual added; forward and backward under the HYBRID delayed-scaling recipe.
+
+    s = x + residual                 the residual stream after the block before
+    n = rms_norm(s) * weight         codes (E4M3)
+    h = act(n Wg^T) * (n Wu^T)       codes (E4M3), both projections in one GEMM
+    y = h Wd^T + s                   bf16
+
+"4.2 Hopper I — Transformer Engine·FP8", §4.2.3 and §4.2.6: forward operands are
+E4M3, gradients E5M2; §4.2.4: each tensor has its own delayed scale, and a GEMM's
+restore is combined with the next stage's scale, so the activations between the
+three products only ever exist as codes.
+
+The class only sequences libfp8mi's kernels and owns the buffers, as Fp8Linear.
+Any number of tokens runs forward (one token: the few-row kernels); the backward
+needs a multiple of 16, the K granule of its weight-gradient GEMMs.
+"""
+
+from __future__ import annotations
+
+import torch
+
+from . import _binding as _b
+from .state import DelayedScalingState, Recipe
+
+# Scratch of one block: split products' partial sums, the norm's and the
+# activation gradients' column sums, the statistics.
+WORKSPACE_BYTES = 64 << 20
+
+
+class Fp8FeedForward:
+    """Buffers and delayed-scaling states of one block: x, residual and y
+    [tokens x hidden] bf16, w_gate_up [2 ffn x hidden] (the gate's rows, then the
+    up projection's) and w_down [hidden x ffn] bf16, weight [hidden] bf16."""
+
+    def __init__(self, tokens: int, hidden: int, ffn: int, act: str = "silu", eps: float = 1e-5,
+                 recipe: Recipe = Recipe(), accum: str = "exact", device="cuda"):
+        if recipe.fmt_fwd != "e4m3" or recipe.fmt_bwd != "e5m2":
+            raise ValueError("Fp8FeedForward implements the HYBRID recipe (E4M3 forward, E5M2 backward)")
+        if act not in _b.ACTIVATIONS:
+            raise ValueError(f"unknown activation {act!r}")
+        dev = torch.device(device)
+        self.shape, self.act, self.eps, self.accum = (tokens, hidden, ffn), act, eps, accum
+
+        def state(fmt):
+            return DelayedScalingState(fmt, recipe.history_len, device=dev)
+
+        fwd, bwd = recipe.fmt_fwd, recipe.fmt_bwd
+        self.state_n, self.state_gu, self.state_h, self.state_d = state(fwd), state(fwd), state(fwd), state(fwd)
+        self.state_dy, self.state_dgu = state(bwd), state(bwd)
+        u8, bf = dict(dtype=torch.uint8, device=dev), dict(dtype=torch.bfloat16, device=dev)
+        T, H, F = tokens, hidden, ffn
+        self.sum, self.rstd = torch.empty((T, H), **bf), torch.empty(T, dtype=torch.float32, device=dev)
+        self.qn, self.qh, self.gu = torch.empty((T, H), **u8), torch.empty((T, F), **u8), torch.empty((T, 2 * F), **bf)
+        self.qw_gu, self.qw_d = torch.empty((2 * F, H), **u8), torch.empty((H, F), **u8)
+        self.qdy, self.qdy_t = torch.empty((T, H), **u8), torch.empty((H, T), **u8)
+        self.dh, self.dn = torch.empty((T, F), **bf), torch.empty((T, H), **bf)
+        self.qdgu, self.qdgu_t = torch.empty((T, 2 * F), **u8), torch.empty((2 * F, T), **u8)
+        self.workspace = torch.empty(WORKSPACE_BYTES, **u8)
+
+    def _check(self, t, shape, name):
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
+
+    def quantize_weights(self, w_gate_up, w_down, stream=None):
+        """Cast the weights with their current scales: once a training step, or once
+        before serving."""
+        T, H, F = self.shape
+        self._check(w_gate_up, (2 * F, H), "w_gate_up")
+        self._check(w_down, (H, F), "w_down")
+        self.state_gu.quantize(w_gate_up, q=self.qw_gu, stream=stream)
+        self.state_d.quantize(w_down, q=self.qw_d, stream=stream)
+
+    def forward(self, x, residual, weight, y, train=True, stream=None):
+        """y = down(act(gate(n)) * up(n)) + s, with the weights' codes as they are.
+        residual may be None (s = x).  train: keep what backward needs."""
+        T, H, F = self.shape
+        self._check(x, (T, H), "x")
+        self._check(y, (T, H), "y")
+        n, h, ws = self.state_n, self.state_h, self.workspace
+        _b.fp8_rmsnorm_quantize(x, weight, self.eps, n.fmt, n.scale, self.qn, residual=residual,
+                                sum_out=None if residual is None else self.sum, rstd=self.rstd if train else None,
+                                amax=n.amax, workspace=ws, stream=stream)
+        self._s = x if residual is None else self.sum
+        _b.fp8_gemm_gated(self.qn, n.fmt, self.qw_gu, self.state_gu.fmt, n.scale_inv, self.state_gu.scale_inv,
+                          self.act, self.qh, gu=self.gu if train else None, out_fmt=h.fmt, out_scale=h.scale,
+                          amax=h.amax, accum=self.accum, workspace=ws, stream=stream)
+        _b.fp8_gemm_fused(self.qh, h.fmt, self.qw_d, self.state_d.fmt, h.scale_inv, self.state_d.scale_inv, y,
+                          residual=self._s, accum=self.accum, workspace=ws, stream=stream)
+
+    def backward(self, dy, weight, dx, dweight, dw_gate_up, dw_down, stream=None):
+        """Gradients of the last forward(train=True): dx [tokens x hidden] bf16 (of x, hence of
+        the residual too), dweight fp32 [hidden], dw_gate_up and dw_down (fp32 or bf16)."""
+        T, H, F = self.shape
+        if T % 16:
+            raise ValueError(f"backward needs a multiple of 16 tokens, got {T}")
+        self._check(dy, (T, H), "dy")
+        self._check(dw_gate_up, (2 * F, H), "dw_gate_up")
+        self._check(dw_down, (H, F), "dw_down")
+        sy, sg, ws = self.state_dy, self.state_dgu, self.workspace
+        kw = dict(accum=self.accum, b_trans=True, stream=stream)
+        _b.fp8_act_backward(dy, None, "none", sy.fmt, sy.scale, q=self.qdy, q_t=self.qdy_t, amax=sy.amax, workspace=ws,
+                            stream=stream)
+        _b.fp8_gemm(self.qdy, sy.fmt, self.qw_d, self.state_d.fmt, sy.scale_inv, self.state_d.scale_inv, self.dh, **kw)
+        _b.fp8_gemm(self.qdy_t, sy.fmt, self.qh, self.state_h.fmt, sy.scale_inv, self.state_h.scale_inv, dw_down, **kw)
+        _b.fp8_gated_backward(self.dh, self.gu, self.act, sg.fmt, sg.scale, q=self.qdgu, q_t=self.qdgu_t, amax=sg.amax,
+                              workspace=ws, stream=stream)
+        _b.fp8_gemm(self.qdgu, sg.fmt, self.qw_gu, self.state_gu.fmt, sg.scale_inv, self.state_gu.scale_inv, self.dn, **kw)
+        _b.fp8_gemm(self.qdgu_t, sg.fmt, self.qn, self.state_n.fmt, sg.scale_inv, self.state_n.scale_inv, dw_gate_up, **kw)
+        _b.fp8_rmsnorm_backward(self.dn, self._s, self.rstd, weight, dx, dweight=dweight, dresidual=dy, workspace=ws,
+                                stream=stream)
+
+    def update(self, stream=None):
+        """Push each tensor's amax into its history and set the next step's scales."""
+        for st in (self.state_n, self.state_gu, self.state_h, self.state_d, self.state_dy, self.state_dgu):
+            st.update(stream=stream)

@@ -15,6 +15,8 @@ gemm     dequantised GEMM in fp64, exact integer dot products, the error
          bound, and the fine-grained grouped GEMM.
 linear   one FP8 linear-layer step (forward, data and weight gradients)
          under the HYBRID recipe with delayed scaling.
+feed_forward  the norm, activations and gated product around the GEMMs, with
+         their gradients, in fp64.
 
 Sources (the pages this follows)
 --------------------------------
@@ -32,4 +34,4 @@ Sources (the pages this follows)
 Parity status per function is listed in each module's header.
 """
 
-from . import codec, scaling, gemm, linear  # noqa: F401
+from . import codec, scaling, gemm, linear, feed_forward  # noqa: F401
