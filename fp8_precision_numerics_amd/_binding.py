@@ -192,6 +192,71 @@ def _call(name, status):
         raise Fp8Error(name, status)
 
 
+# Marshalling for the calls whose smallest sizes run for a few microseconds: each
+# property is read once, and the device is switched only where the operands are on
+# another one.
+_FLOATS = (torch.float32, torch.bfloat16)
+
+# The current stream's handle and device without building the Python objects
+# around them (about 2 us of a small call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_FUNCTIONS = {}
+
+
+def _dev_of(t, name):
+    """Index of the GPU that t is on."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    return t.get_device()
+
+
+def _ptr(t, name, dtype, shape, dev):
+    """Address of a contiguous operand of that type, shape and device (None: not given)."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and (shape is None or t.shape == shape):
+        return t.data_ptr()
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _scalar(t, name, dev, dtype=torch.float32):
+    if t is None:
+        return None
+    if t.numel() != 1:
+        raise ValueError(f"{name} must have 1 element, got {t.numel()}")
+    return _ptr(t, name, dtype, None, dev)
+
+
+def _space(workspace, dev):
+    """(address, bytes) of an optional workspace."""
+    if workspace is None:
+        return None, 0
+    return _ptr(workspace, "workspace", torch.uint8, None, dev), workspace.numel()
+
+
+def _launch(name, dev, stream, *args):
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return _launch(name, dev, stream, *args)
+    if stream is None:
+        handle = _raw_stream(dev)
+    else:
+        handle = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    fn = _FUNCTIONS.get(name)
+    if fn is None:
+        fn = _FUNCTIONS[name] = getattr(load_library(), name)
+    status = fn(*args, handle)
+    if status != 0:
+        raise Fp8Error(name, status)
+
+
 # ---------------------------------------------------------------------------
 # entry points
 # ---------------------------------------------------------------------------
@@ -296,22 +361,19 @@ def fp8_gemm(a, fa, b, fb, sinv_a, sinv_b, c, accum="exact", b_trans=False, stre
     accum: "exact" (every product exact, fp32 sums) or "mfma_fp8" (native FP8
     matrix cores; see include/fp8mi.h for their arithmetic).
     """
-    lib = load_library()
-    dev = a.device
-    _check(a, "a", torch.uint8, None, dev)
-    _check(b, "b", torch.uint8, None, dev)
-    _check(sinv_a, "sinv_a", torch.float32, 1, dev)
-    _check(sinv_b, "sinv_b", torch.float32, 1, dev)
-    _check(c, "c", (torch.float32, torch.bfloat16), None, dev)
+    dev = _dev_of(a, "a")
+    pa, pb = _ptr(a, "a", torch.uint8, None, dev), _ptr(b, "b", torch.uint8, None, dev)
+    if c.dtype not in _FLOATS:
+        raise TypeError(f"c must be {_FLOATS}, got {c.dtype}")
+    pc = _ptr(c, "c", c.dtype, None, dev)
     M, K = a.shape
     K2, N = b.shape if b_trans else (b.shape[1], b.shape[0])
     if K2 != K or tuple(c.shape) != (M, N):
         raise ValueError(f"shape mismatch: a {tuple(a.shape)}, b {tuple(b.shape)} (b_trans={bool(b_trans)}), "
                          f"c {tuple(c.shape)}")
-    ctype = F32 if c.dtype == torch.float32 else BF16
-    with torch.cuda.device(dev):
-        _call("fp8_gemm", lib.fp8_gemm(_p(a), _fmt(fa), _p(b), _fmt(fb), 1 if b_trans else 0, M, N, K, _p(sinv_a),
-                                       _p(sinv_b), _p(c), ctype, _accum(accum), _stream(stream)))
+    _launch("fp8_gemm", dev, stream, pa, _fmt(fa), pb, _fmt(fb), 1 if b_trans else 0, M, N, K,
+            _scalar(sinv_a, "sinv_a", dev), _scalar(sinv_b, "sinv_b", dev), pc,
+            F32 if c.dtype == torch.float32 else BF16, _accum(accum))
 
 
 def fp8_gemm_requant(a, fa, b, fb, sinv_a, sinv_b, out_fmt, out_scale, cq, amax=None, sat=None, accum="exact",
@@ -455,78 +517,13 @@ def fp8_grouped_gemm(a, sinv_a, b, sinv_b, m_offsets, c, accum="exact", stream=N
 
 
 # ---------------------------------------------------------------------------
-# feed-forward operators.  Their smallest calls run for a few microseconds, so
-# the checks read each property once and the device is switched only where the
-# operands are on another one.
+# feed-forward operators
 # ---------------------------------------------------------------------------
-_FLOATS = (torch.float32, torch.bfloat16)
-
-
 def _act(a) -> int:
     try:
         return ACTIVATIONS[a]
     except KeyError:
         raise ValueError(f"unknown activation {a!r}") from None
-
-
-# The current stream's handle and device without building the Python objects
-# around them (about 2 us of a small call).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
-_FUNCTIONS = {}
-
-
-def _dev_of(t, name):
-    """Index of the GPU that t is on."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor")
-    return t.get_device()
-
-
-def _ptr(t, name, dtype, shape, dev):
-    """Address of a contiguous operand of that type, shape and device (None: not given)."""
-    if t is None:
-        return None
-    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and (shape is None or t.shape == shape):
-        return t.data_ptr()
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
-    raise ValueError(f"{name} must be contiguous")
-
-
-def _scalar(t, name, dev, dtype=torch.float32):
-    if t is None:
-        return None
-    if t.numel() != 1:
-        raise ValueError(f"{name} must have 1 element, got {t.numel()}")
-    return _ptr(t, name, dtype, None, dev)
-
-
-def _space(workspace, dev):
-    """(address, bytes) of an optional workspace."""
-    if workspace is None:
-        return None, 0
-    return _ptr(workspace, "workspace", torch.uint8, None, dev), workspace.numel()
-
-
-def _launch(name, dev, stream, *args):
-    if torch.cuda.current_device() != dev:
-        with torch.cuda.device(dev):
-            return _launch(name, dev, stream, *args)
-    if stream is None:
-        handle = _raw_stream(dev)
-    else:
-        handle = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-    fn = _FUNCTIONS.get(name)
-    if fn is None:
-        fn = _FUNCTIONS[name] = getattr(load_library(), name)
-    status = fn(*args, handle)
-    if status != 0:
-        raise Fp8Error(name, status)
 
 
 def _norm_operands(x, weight, residual, sum_out, q, rstd):

@@ -168,10 +168,41 @@ __global__ __launch_bounds__(kNT, 4) void act_backward_kernel(BackArgs a) {
 }
 
 // out[n] = sum over the rows of partials [count x cols]: 16 columns a workgroup, 64
-// lanes down the rows of each, then a tree in LDS.
+// lanes down the rows of each, then a tree in LDS.  With statistics' slots, one more
+// workgroup (the last) reduces those, which saves a launch (3 us of a small call).
 constexpr int kSumLanes = 64;
 __global__ __launch_bounds__(16 * kSumLanes) void column_sums_kernel(const float* __restrict__ partials, int count,
-                                                                    int64_t cols, float* __restrict__ out) {
+                                                                    int64_t cols, float* __restrict__ out,
+                                                                    const uint4* __restrict__ slots, int nslots,
+                                                                    uint32_t* amax_bits, unsigned long long* sat) {
+  if (slots && blockIdx.x == gridDim.x - 1) {
+    __shared__ uint32_t s_max[kSumLanes / 4];
+    __shared__ unsigned long long s_cnt[kSumLanes / 4];
+    uint32_t m = 0u;
+    unsigned long long c = 0ull;
+    for (int i = threadIdx.x; i < nslots; i += 16 * kSumLanes) {
+      const uint4 p = slots[i];
+      m = m > p.x ? m : p.x;
+      c += (unsigned long long)p.z | ((unsigned long long)p.w << 32);
+    }
+    m = wave_max_u32(m);
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) c += __shfl_xor(c, off, 64);
+    if ((threadIdx.x & 63) == 0) {
+      s_max[threadIdx.x >> 6] = m;
+      s_cnt[threadIdx.x >> 6] = c;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int w = 1; w < kSumLanes / 4; ++w) {
+        m = m > s_max[w] ? m : s_max[w];
+        c += s_cnt[w];
+      }
+      if (amax_bits) *amax_bits = m;
+      if (sat) *sat = c;
+    }
+    return;
+  }
   __shared__ float buf[kSumLanes][17];
   const int cx = threadIdx.x & 15, ry = threadIdx.x >> 4;
   const int64_t c = (int64_t)blockIdx.x * 16 + cx;
@@ -219,13 +250,14 @@ hipError_t back_launch(BackArgs a, int xtype, int fmt, int act, float* dbias, fl
   // As many walks a strip as fill the device with 8 workgroups a compute unit.
   int64_t walks = empty ? 0 : persistent_groups(8) / strips;
   if (!empty) walks = walks < 1 ? 1 : (walks > row_tiles ? row_tiles : walks);
-  // The workspace holds the bias gradient's partial rows, then the statistics' slots.
+  // The workspace holds the bias gradient's partial rows (a single one goes straight to
+  // dbias), then the statistics' slots.
   uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
   if (dbias && !empty) {
     const int64_t fit = (int64_t)(workspace_bytes / (a.N * sizeof(float)));  // >= 1: checked by the entry point
     if (walks > fit) walks = fit;
-    a.col_partials = reinterpret_cast<float*>(ws);
-    const size_t used = ((size_t)walks * a.N * sizeof(float) + 15) & ~size_t(15);
+    a.col_partials = walks == 1 ? dbias : reinterpret_cast<float*>(ws);
+    const size_t used = walks == 1 ? 0 : ((size_t)walks * a.N * sizeof(float) + 15) & ~size_t(15);
     ws = used < workspace_bytes ? ws + used : nullptr;
     workspace_bytes = ws ? workspace_bytes - used : 0;
   }
@@ -245,22 +277,22 @@ hipError_t back_launch(BackArgs a, int xtype, int fmt, int act, float* dbias, fl
       else back_act<kF32, kE5M2, GATED>(a, act, stats, (unsigned)groups, st);
     }
   }
-  hipError_t e = hipGetLastError();
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (dbias) {
-    e = launch_column_sums(a.col_partials, (int)walks, a.N, dbias, st);
-    if (e != hipSuccess) return e;
-  }
+  if (dbias && walks != 1)
+    return launch_column_sums(a.col_partials, (int)walks, a.N, dbias, a.stat_slots, (int)groups, amax, a.sat, st);
   if (a.stat_slots) return launch_reduce_stats(a.stat_slots, (int)groups, amax, a.sat, st);
   return hipSuccess;
 }
 
 }  // namespace
 
-hipError_t launch_column_sums(const float* partials, int count, int64_t cols, float* out, hipStream_t stream) {
-  if (cols == 0) return hipSuccess;
-  hipLaunchKernelGGL(column_sums_kernel, dim3((unsigned)((cols + 15) / 16)), dim3(16 * kSumLanes), 0, stream, partials, count,
-                     cols, out);
+hipError_t launch_column_sums(const float* partials, int count, int64_t cols, float* out, const void* slots, int nslots,
+                              float* amax, unsigned long long* sat, hipStream_t stream) {
+  const unsigned groups = (unsigned)((cols + 15) / 16) + (slots ? 1u : 0u);
+  if (groups == 0) return hipSuccess;
+  hipLaunchKernelGGL(column_sums_kernel, dim3(groups), dim3(16 * kSumLanes), 0, stream, partials, count, cols, out,
+                     reinterpret_cast<const uint4*>(slots), nslots, reinterpret_cast<uint32_t*>(amax), sat);
   return hipGetLastError();
 }
 

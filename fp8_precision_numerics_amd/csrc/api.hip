@@ -403,7 +403,7 @@ int fp8_rmsnorm_backward(const void* dy, const void* h, const float* rstd, const
   if (rows * cols == 0 && (cols == 0 || !dweight)) return FP8MI_OK;
   if (rows != 0) {
     if (!dy || !h || !rstd || !weight || !dx) return FP8MI_ERR_NULL;
-    if (!aligned16(dy) || !aligned16(h) || !aligned16(weight) || !aligned16(dresidual) || !aligned16(dx))
+    if (!aligned16(dy) || !aligned16(h) || !aligned16(weight) || !aligned16(dresidual) || !aligned16(dx) || !aligned16(dweight))
       return FP8MI_ERR_ALIGN;
     if (dweight && !workspace) return FP8MI_ERR_NULL;
     if (dweight && workspace_bytes < (size_t)cols * sizeof(float)) return FP8MI_ERR_WORKSPACE;

@@ -181,14 +181,38 @@ __device__ __forceinline__ uint4 load_bf16x8(const uint16_t* p, bool vec, int le
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A wave's amax and count into the outputs (cleared beforehand): one device-scope
-// atomic per wave, skipped where the wave's maximum does not exceed `seen`, an
-// earlier value of the output, which only grows.
-__device__ __forceinline__ void publish_epilogue_stats(const EpiArgs& a, const LaneStats& st, uint32_t seen, int lane) {
+// A workgroup's amax and count into the outputs (cleared beforehand): the waves meet in
+// `scratch` (LDS, two words a wave, free of other use), then one device-scope atomic a
+// workgroup, skipped where it would change nothing (the outputs only grow).  One
+// atomic a wave, contended by every wave that finishes its tile at the same time, cost
+// 18 us (8192 x 4096 x 16384, FP8 cores: 397 against 379 us without the amax).
+// All threads of the workgroup call it.
+__device__ __forceinline__ void publish_epilogue_stats(const EpiArgs& a, const LaneStats& st, uint32_t* scratch) {
   const uint32_t m = wave_max_u32(st.amax()), cnt = wave_sum_u32(st.sat);
-  if (lane == 0) {
-    if (a.amax_bits && m > seen) atomicMax(a.amax_bits, m);
-    if (a.sat && cnt) atomicAdd(a.sat, (unsigned long long)cnt);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) {
+    scratch[2 * (threadIdx.x >> 6)] = m;
+    scratch[2 * (threadIdx.x >> 6) + 1] = cnt;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    uint32_t top = m;
+    unsigned long long total = cnt;
+    for (int w = 1; w < (int)(blockDim.x >> 6); ++w) {
+      top = scratch[2 * w] > top ? scratch[2 * w] : top;
+      total += scratch[2 * w + 1];
+    }
+    if (a.amax_bits && top > __hip_atomic_load(a.amax_bits, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT))
+      atomicMax(a.amax_bits, top);
+    if (a.sat && total) atomicAdd(a.sat, total);
+  }
+}
+
+// Clears the outputs that a later kernel's publish_epilogue_stats adds to.
+__device__ __forceinline__ void clear_epilogue_stats(const EpiArgs& a) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    if (a.amax_bits) *a.amax_bits = 0u;
+    if (a.sat) *a.sat = 0ull;
   }
 }
 

@@ -4,6 +4,7 @@
 #pragma once
 
 #include "gemm_kernel.hpp"
+#include "gemm_shape.hpp"
 
 namespace fp8mi {
 
@@ -30,17 +31,26 @@ inline hipError_t gemm_run(const uint8_t* A, const uint8_t* B, int64_t M, int64_
 // wavefronts of 128x128 (one per SIMD, accumulators in the AGPR half of the
 // register file) once the waves' priority window breaks their lockstep
 // (gemm_kernel.hpp): per-tensor 2-3 %, MXFP8 8 % (812 against 881 us).
-// FP8 path: 8 wavefronts (two per SIMD, 64x128 each).  Small problems:
-// 128x128 tiles of four 64x64 wavefronts.  BT: B stored [K x N] (read through
-// the LDS transpose path), same tiles.
+// FP8 path: 8 wavefronts (two per SIMD, 64x128 each).  Smaller problems: tiles of
+// 128x128 (four 64x64 wavefronts) or 64x128, whichever the estimate of
+// gemm_shape.hpp prefers (2048 x 4096 x 4096 exact: 56 us on 128x128 tiles, 76 us
+// on 256x256); MXFP8: 128x128.  Every shape sums an output's products in the same
+// order, so the bits do not depend on the choice.  BT: B stored [K x N] (read
+// through the LDS transpose path), same tiles.
 template <int FA, int FB, int OUT, int MODE, bool BT = false>
 inline hipError_t gemm_dispatch_shape(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, int64_t K,
                                       const float* sa, const float* sb, void* C, const RequantArgs& rq,
                                       hipStream_t st, const MxScales& mxs = MxScales{nullptr, nullptr}) {
-  if (M >= 1024 && N >= 1024) {
+  constexpr bool MXS = MODE == kAccumMx || MODE == kAccumMxExact;
+  int shape = M >= 1024 && N >= 1024 ? 0 : 1;
+  if constexpr (!MXS) shape = choose_tile(M, N, K, MODE, 0).shape;
+  if (shape == 0) {
     if constexpr (MODE == kAccumExact || MODE == kAccumMxExact)
       return gemm_run<256, 256, 2, 4, FA, FB, OUT, MODE, BT>(A, B, M, N, K, sa, sb, C, rq, st, mxs);
     else return gemm_run<256, 256, 4, 2, FA, FB, OUT, MODE, BT>(A, B, M, N, K, sa, sb, C, rq, st, mxs);
+  }
+  if constexpr (!MXS) {
+    if (shape == 2) return gemm_run<64, 128, 2, 2, FA, FB, OUT, MODE, BT>(A, B, M, N, K, sa, sb, C, rq, st, mxs);
   }
   return gemm_run<128, 128, 2, 2, FA, FB, OUT, MODE, BT>(A, B, M, N, K, sa, sb, C, rq, st, mxs);
 }

@@ -179,7 +179,7 @@ __global__ __launch_bounds__(64 * kWavesFew) void gemm_few_rows_kernel(const uin
       epilogue8<GATED>(epi, v[0], v[NB - 1], bias, res, m, n, N, vec, left, scale, st);
     }
   }
-  if (epi.amax_bits || epi.sat) publish_epilogue_stats(epi, st, 0u, threadIdx.x & 63);
+  if (epi.amax_bits || epi.sat) publish_epilogue_stats(epi, st, reinterpret_cast<uint32_t*>(red));
 }
 
 template <int FA, int FB, bool GATED>

@@ -717,8 +717,6 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(
       const bool whole = rq.split <= 1;
       float* partials = rq.partials + (whole ? 0 : (int64_t)part * M * (GATED ? 2 * (int64_t)N : (int64_t)N));
       LaneStats st;
-      const uint32_t seen =
-          whole && rq.amax_bits ? __hip_atomic_load(rq.amax_bits, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0u;
 #pragma unroll 1
       for (int r0 = 0; r0 < BM; r0 += PASS) {
         pass.prefetch(r0);
@@ -728,7 +726,10 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(
         if (whole) pass.flush(tw, r0, st);
         else pass.flush_partials(tw, r0, partials);
       }
-      if (whole && (rq.amax_bits || rq.sat)) publish_epilogue_stats(rq, st, seen, lane);
+      if (rq.amax_bits || rq.sat) {
+        if (whole) publish_epilogue_stats(rq, st, reinterpret_cast<uint32_t*>(smem));
+        else clear_epilogue_stats(rq);  // for the kernel that finishes the split product
+      }
     } else {
 #pragma unroll 1
       for (int r0 = 0; r0 < BM; r0 += PASS) {

@@ -90,8 +90,10 @@ hipError_t launch_clear_stats(float* amax, unsigned long long* sat, hipStream_t 
 hipError_t launch_reduce_stats(const void* partials, int count, float* amax, unsigned long long* sat,
                                hipStream_t stream);
 
-// out[n] = sum of column n of partials [count x cols], in a fixed order.
-hipError_t launch_column_sums(const float* partials, int count, int64_t cols, float* out, hipStream_t stream);
+// out[n] = sum of column n of partials [count x cols], in a fixed order; `slots` (may
+// be null): launch_reduce_stats in the same launch.
+hipError_t launch_column_sums(const float* partials, int count, int64_t cols, float* out, const void* slots, int nslots,
+                              float* amax, unsigned long long* sat, hipStream_t stream);
 
 hipError_t launch_rmsnorm_quantize(const void* x, const void* residual, const void* weight, int xtype, int64_t rows,
                                    int64_t cols, float eps, int fmt, const float* scale, void* sum_out, uint8_t* q,

@@ -506,25 +506,22 @@ int norm_launch(const NormArgs& a, int xtype, int fmt, int kind, int64_t slots, 
   return fmt == kE4M3 ? norm_kind<kF32, kE4M3>(a, kind, slots, st) : norm_kind<kF32, kE5M2>(a, kind, slots, st);
 }
 
+// Workgroups of the gradient's kernel: up to 1024 threads a compute unit for rows of a
+// wavefront; two workgroups for rows up to 8192 (4096: 46.1 us against 52.1 with four,
+// whose partials cost more than they gain), one beyond.
+int norm_back_groups(int64_t rows, int64_t octets, int64_t slots) {
+  if (octets <= 128) return row_groups(rows, 4, 4, slots);
+  return row_groups(rows, 1, octets <= 1024 ? 2 : 1, slots);
+}
+
 template <int XT>
-int norm_back_run(const NormBackArgs& a, int64_t slots, hipStream_t st) {
+void norm_back_run(const NormBackArgs& a, int g, hipStream_t st) {
   const int64_t o = a.cols / 8;
-  if (o <= 128) {
-    const int g = row_groups(a.rows, 4, 4, slots);
-    if (o <= 64) hipLaunchKernelGGL((rmsnorm_backward_kernel<XT, false, 1>), dim3((unsigned)g), dim3(256), 0, st, a);
-    else hipLaunchKernelGGL((rmsnorm_backward_kernel<XT, false, 2>), dim3((unsigned)g), dim3(256), 0, st, a);
-    return g;
-  }
-  if (o <= 2048) {
-    // Two workgroups a compute unit for rows up to 8192 (4096: 46.1 us against 52.1 with
-    // four, whose partials cost more than they gain), one beyond.
-    const int nt = row_threads(o), g = row_groups(a.rows, 1, nt <= 512 ? 2 : 1, slots);
-    hipLaunchKernelGGL((rmsnorm_backward_kernel<XT, true, 2>), dim3((unsigned)g), dim3(nt), 0, st, a);
-    return g;
-  }
-  const int g = row_groups(a.rows, 1, 1, slots);
-  hipLaunchKernelGGL((rmsnorm_backward_long_kernel<XT, 1024>), dim3((unsigned)g), dim3(1024), 0, st, a);
-  return g;
+  const dim3 grid((unsigned)g);
+  if (o <= 64) hipLaunchKernelGGL((rmsnorm_backward_kernel<XT, false, 1>), grid, dim3(256), 0, st, a);
+  else if (o <= 128) hipLaunchKernelGGL((rmsnorm_backward_kernel<XT, false, 2>), grid, dim3(256), 0, st, a);
+  else if (o <= 2048) hipLaunchKernelGGL((rmsnorm_backward_kernel<XT, true, 2>), grid, dim3(row_threads(o)), 0, st, a);
+  else hipLaunchKernelGGL((rmsnorm_backward_long_kernel<XT, 1024>), grid, dim3(1024), 0, st, a);
 }
 
 }  // namespace
@@ -559,16 +556,18 @@ hipError_t launch_rmsnorm_quantize_blockwise(const void* x, const void* residual
 hipError_t launch_rmsnorm_backward(const void* dy, const void* h, const float* rstd, const void* weight,
                                    const void* dres, int xtype, int64_t rows, int64_t cols, void* dx, float* dweight,
                                    void* workspace, size_t workspace_bytes, hipStream_t stream) {
-  float* partials = dweight ? reinterpret_cast<float*>(workspace) : nullptr;
   int g = 0;
+  float* partials = nullptr;
   if (rows * cols > 0) {
+    g = norm_back_groups(rows, cols / 8, dweight ? (int64_t)(workspace_bytes / (cols * sizeof(float))) : 0);
+    if (dweight) partials = g == 1 ? dweight : reinterpret_cast<float*>(workspace);  // a single partial row is the result
     const NormBackArgs a{dy, h, rstd, weight, dres, dx, partials, rows, cols};
-    const int64_t slots = partials ? (int64_t)(workspace_bytes / (cols * sizeof(float))) : 0;
-    g = xtype == kBF16 ? norm_back_run<kBF16>(a, slots, stream) : norm_back_run<kF32>(a, slots, stream);
+    if (xtype == kBF16) norm_back_run<kBF16>(a, g, stream);
+    else norm_back_run<kF32>(a, g, stream);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (dweight) return launch_column_sums(partials, g, cols, dweight, stream);
+  if (dweight && g != 1) return launch_column_sums(partials, g, cols, dweight, nullptr, 0, nullptr, nullptr, stream);
   return hipGetLastError();
 }
 

@@ -59,7 +59,7 @@ NORM_BACK = dict(dy=P, h=P, rstd=P, weight=P, dres=None, xtype=0, rows=4, cols=6
 @pytest.mark.parametrize("want,change", [
     (EDTYPE, dict(xtype=3)), (ESHAPE, dict(rows=-2)), (EALIGN, dict(cols=24)), (ENULL, dict(dy=None)), (ENULL, dict(h=None)),
     (ENULL, dict(rstd=None)), (ENULL, dict(weight=None)), (ENULL, dict(dx=None)), (EALIGN, dict(dy=P8)), (EALIGN, dict(h=P8)),
-    (EALIGN, dict(weight=P8)), (EALIGN, dict(dres=P8)), (EALIGN, dict(dx=P8)), (EALIGN, dict(ws=P8)), (ENULL, dict(ws=None, ws_bytes=0)),
+    (EALIGN, dict(weight=P8)), (EALIGN, dict(dres=P8)), (EALIGN, dict(dx=P8)), (EALIGN, dict(dweight=P8)), (EALIGN, dict(ws=P8)), (ENULL, dict(ws=None, ws_bytes=0)),
     (EWS, dict(ws_bytes=255)), (OK, dict(rows=0, dweight=None)), (OK, dict(cols=0))])
 def test_norm_backward_refusals(lib, want, change):
     assert call(lib.fp8_rmsnorm_backward, NORM_BACK, **change) == want
