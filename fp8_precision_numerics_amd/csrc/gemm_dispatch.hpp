@@ -8,7 +8,7 @@
 
 namespace fp8mi {
 
-template <int BM, int BN, int WM, int WN, int FA, int FB, int OUT, int MODE, bool BT>
+template <int BM, int BN, int WM, int WN, int FA, int FB, int OUT, int MODE, bool BT, int STAGES = 2>
 inline hipError_t gemm_run(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, int64_t K, const float* sa,
                            const float* sb, void* C, const RequantArgs& rq, hipStream_t st,
                            const MxScales& mxs = MxScales{nullptr, nullptr}) {
@@ -20,7 +20,7 @@ inline hipError_t gemm_run(const uint8_t* A, const uint8_t* B, int64_t M, int64_
   // for the exact kernel and 3.5 % for the FP8 one than bands of 16; bands of
   // 8 and 2 in between.
   const int group_m = 4;
-  hipLaunchKernelGGL((gemm_kernel<BM, BN, WM, WN, FA, FB, OUT, MODE, BT>), dim3((unsigned)(tiles_m * tiles_n)),
+  hipLaunchKernelGGL((gemm_kernel<BM, BN, WM, WN, FA, FB, OUT, MODE, BT, RequantArgs, STAGES>), dim3((unsigned)(tiles_m * tiles_n)),
                      dim3(64 * WM * WN), 0, st, A, B, (int)M, (int)N, (int)K, sa, sb, C, tiles_m, tiles_n, group_m,
                      rq, mxs);
   return hipGetLastError();
@@ -32,7 +32,7 @@ inline hipError_t gemm_run(const uint8_t* A, const uint8_t* B, int64_t M, int64_
 // register file) once the waves' priority window breaks their lockstep
 // (gemm_kernel.hpp): per-tensor 2-3 %, MXFP8 8 % (812 against 881 us).
 // FP8 path: 8 wavefronts (two per SIMD, 64x128 each).  Smaller problems: tiles of
-// 128x128 (four 64x64 wavefronts) or 64x128, whichever the estimate of
+// 128x128 (four 64x64 wavefronts) or 64x128 (with two or three stages), whichever the estimate of
 // gemm_shape.hpp prefers (2048 x 4096 x 4096 exact: 56 us on 128x128 tiles, 76 us
 // on 256x256); MXFP8: 128x128.  Every shape sums an output's products in the same
 // order, so the bits do not depend on the choice.  BT: B stored [K x N] (read
@@ -51,6 +51,7 @@ inline hipError_t gemm_dispatch_shape(const uint8_t* A, const uint8_t* B, int64_
   }
   if constexpr (!MXS) {
     if (shape == 2) return gemm_run<64, 128, 2, 2, FA, FB, OUT, MODE, BT>(A, B, M, N, K, sa, sb, C, rq, st, mxs);
+    if (shape == 3) return gemm_run<64, 128, 2, 2, FA, FB, OUT, MODE, BT, 3>(A, B, M, N, K, sa, sb, C, rq, st, mxs);
   }
   return gemm_run<128, 128, 2, 2, FA, FB, OUT, MODE, BT>(A, B, M, N, K, sa, sb, C, rq, st, mxs);
 }

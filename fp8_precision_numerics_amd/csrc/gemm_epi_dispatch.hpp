@@ -66,7 +66,7 @@ __global__ __launch_bounds__(256) void epilogue_partials_kernel(EpiArgs a, int64
 
 // `split` > 1: that many workgroups share a tile's K (no part is empty) over
 // epi.partials, and a second kernel finishes.
-template <int BM, int BN, int WM, int WN, int FA, int FB, int MODE, class EPI>
+template <int BM, int BN, int WM, int WN, int FA, int FB, int MODE, class EPI, int STAGES = 2>
 inline hipError_t epi_run(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, int64_t K, const float* sa,
                           const float* sb, EPI epi, int split, hipStream_t st) {
   constexpr bool GATED = std::is_same<EPI, GatedEpi>::value;
@@ -80,7 +80,7 @@ inline hipError_t epi_run(const uint8_t* A, const uint8_t* B, int64_t M, int64_t
     const hipError_t e = launch_clear_stats(reinterpret_cast<float*>(epi.amax_bits), epi.sat, st);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((gemm_kernel<BM, BN, WM, WN, FA, FB, kF32, MODE, false, EPI>),
+  hipLaunchKernelGGL((gemm_kernel<BM, BN, WM, WN, FA, FB, kF32, MODE, false, EPI, STAGES>),
                      dim3((unsigned)(tiles_m * tiles_n * epi.split)), dim3(64 * WM * WN), 0, st, A, B, (int)M, (int)N,
                      (int)K, sa, sb, (void*)nullptr, tiles_m, tiles_n, group_m, epi, MxScales{nullptr, nullptr});
   if (epi.split > 1) {
@@ -102,7 +102,8 @@ inline hipError_t epi_shape(const uint8_t* A, const uint8_t* B, int64_t M, int64
     else return epi_run<256, 256, 4, 2, FA, FB, MODE, EPI>(A, B, M, N, K, sa, sb, epi, c.split, st);
   }
   if (c.shape == 1) return epi_run<128, 128, 2, 2, FA, FB, MODE, EPI>(A, B, M, N, K, sa, sb, epi, c.split, st);
-  return epi_run<64, 128, 2, 2, FA, FB, MODE, EPI>(A, B, M, N, K, sa, sb, epi, c.split, st);
+  if (c.shape == 2) return epi_run<64, 128, 2, 2, FA, FB, MODE, EPI>(A, B, M, N, K, sa, sb, epi, c.split, st);
+  return epi_run<64, 128, 2, 2, FA, FB, MODE, EPI, 3>(A, B, M, N, K, sa, sb, epi, c.split, st);
 }
 
 template <int MODE, class EPI>

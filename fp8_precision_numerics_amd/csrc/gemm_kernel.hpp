@@ -308,6 +308,75 @@ __device__ __forceinline__ void run_main_loop(uint8_t* s0, uint8_t* s1, int nful
   wait_vmem();  // no load may still be writing the LDS when the epilogue reuses it
 }
 
+// The same with three stages: the loads of step kt + 2 are issued during step kt, so
+// they have two steps to arrive, and the end of a step waits only for those of step
+// kt + 1 (vector loads complete in order; a step issues LOADS of them a wave, and no
+// other vector memory operation runs in the loop).  For small tiles, whose steps are
+// shorter than a round trip to memory.  The stages rotate as run-time pointers: one
+// copy of the step serves all three.
+template <int LOADS, class Issue, class Ragged, class Frags, class Compute, class Hint>
+__device__ __forceinline__ void run_main_loop_deep(uint8_t* smem, int stage_bytes, int nfull, int nk, bool ragged_k,
+                                                   Issue& issue_direct, Ragged& stage_ragged, Frags& load_frags,
+                                                   Compute& compute, Hint& interleave) {
+  uint8_t* cur = smem;
+  uint8_t* nxt = smem + stage_bytes;
+  uint8_t* pre = smem + 2 * stage_bytes;
+  auto rotate = [&]() {
+    uint8_t* t = cur;
+    cur = nxt;
+    nxt = pre;
+    pre = t;
+  };
+  auto no_dma = [](int) {};
+  if (nfull > 0) {
+    for (int g = 0; g < kDmaGroups; ++g) issue_direct(cur, 0, g);
+    if (nfull > 1) {
+      for (int g = 0; g < kDmaGroups; ++g) issue_direct(nxt, 1, g);
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS) : "memory");
+    } else {
+      wait_vmem();
+    }
+    __builtin_amdgcn_s_barrier();
+    load_frags(cur);
+  }
+  int kt = 0;
+#pragma unroll 1
+  for (; kt + 2 < nfull; ++kt) {
+    compute(cur, [&](int g) { issue_direct(pre, kt + 2, g); });
+    interleave();
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LOADS) : "memory");
+    __builtin_amdgcn_s_barrier();
+    load_frags(nxt);
+    rotate();
+  }
+  // The last two full steps issue no loads; the ragged step, if any, is staged during
+  // the last of them (in the stage that it will rotate to, free by then).
+#pragma unroll 1
+  for (; kt < nfull; ++kt) {
+    const bool last = kt + 1 == nfull;
+    if (last && ragged_k) stage_ragged(nfull, (int)((nxt - smem) / stage_bytes));
+    compute(cur, no_dma);
+    interleave();
+    __builtin_amdgcn_sched_barrier(0);
+    wait_loads_and_barrier();
+    if (!last) load_frags(nxt);
+    rotate();
+  }
+  if (kt < nk) {
+    if (nfull == 0) {
+      stage_ragged(0, 0);
+      wait_vmem();
+    }
+    __syncthreads();
+    load_frags(cur);
+    compute(cur, no_dma);
+    interleave();
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  wait_vmem();
+}
+
 // Epilogue: the scaled output tile goes through LDS (free once the K loop is
 // done) so that global stores are whole contiguous rows: each lane stores 16
 // bytes, consecutive lanes consecutive addresses.  Storing straight from the
@@ -564,7 +633,9 @@ __device__ __forceinline__ uint2 lds_read_tr8(const uint8_t* p) {
 // ARGS: RequantArgs, or (epilogue.hpp) FusedEpi or GatedEpi, which replace the
 // output's writing by the feed-forward epilogues (OUT is then kF32, the type in
 // which the tile is staged, and C is unused).
-template <int BM, int BN, int WM, int WN, int FA, int FB, int OUT, int MODE, bool BT = false, class ARGS = RequantArgs>
+// STAGES: LDS buffers of the K loop, 2 or 3.
+template <int BM, int BN, int WM, int WN, int FA, int FB, int OUT, int MODE, bool BT = false, class ARGS = RequantArgs,
+          int STAGES = 2>
 __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, int M, int N, int K,
     const float* __restrict__ sinv_a, const float* __restrict__ sinv_b, void* __restrict__ C,
@@ -587,7 +658,7 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(
   constexpr int SLABS = (BM + BN) * kBK;
   constexpr int STAGE = SLABS + (MXS ? (BM + BN) * 4 : 0);
   static_assert(STAGE % 1024 == 0, "stages keep the slabs' 1 KiB alignment");
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * STAGE + (MXE ? kMxRefBytes : 0)];
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[STAGES * STAGE + (MXE ? kMxRefBytes : 0)];
 
   int tm, tn;
   int pid = blockIdx.x, part = 0;
@@ -646,6 +717,8 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(
     return lds_read_tr8(st + BM * kBK + bt_lds_offset<BN>(krow0 + jt, col0 + 8 * ht));
   };
 
+  constexpr int kLoads = SlabLoader<BM, BN, NW, BT, PAIR>::LQA + SlabLoader<BM, BN, NW, BT, PAIR>::LQB;
+  static_assert(STAGES == 2 || (STAGES == 3 && !MXS), "two or three stages; MXFP8 loads more a step");
   uint8_t* const s0 = smem;
   uint8_t* const s1 = smem + STAGE;
   int nfull = K / kBK;
@@ -709,7 +782,7 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(
   // `emit(r_lo, r_hi, writer)` puts this lane's outputs of rows [r_lo, r_hi).
   auto write_tile = [&](auto&& emit) {
     using TW = TileWriter<OUT, BM, BN, NT>;
-    constexpr int PASS = pass_rows<BM>(2 * STAGE, TW::ROWB);
+    constexpr int PASS = pass_rows<BM>(STAGES * STAGE, TW::ROWB);
     static_assert(PASS == BM || OUT == kF32 || OUT == kBF16, "FP8 tiles go out in one pass");
     TW tw{smem, PASS};
     if constexpr (EPI) {
@@ -844,7 +917,10 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(
         __builtin_amdgcn_sched_group_barrier(kSchedMfma, FM, 0);
       }
     };
-    run_main_loop(s0, s1, nfull, nk, ragged_k, issue_direct, stage_ragged, load_frags, compute, interleave);
+    if constexpr (STAGES == 3)
+      run_main_loop_deep<kLoads>(smem, STAGE, nfull, nk, ragged_k, issue_direct, stage_ragged, load_frags, compute, interleave);
+    else
+      run_main_loop(s0, s1, nfull, nk, ragged_k, issue_direct, stage_ragged, load_frags, compute, interleave);
 
     // Lane l holds row m = l & 15 of each 16x16 block (the A operand went
     // second) and columns n = 4(l >> 4) .. +3.  MXFP8 carries its scales in
@@ -1011,7 +1087,10 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(
       }
     };
     auto interleave = [&]() {};
-    run_main_loop(s0, s1, nfull, nk, ragged_k, issue_direct, stage_ragged, load_frags, compute, interleave, MXE);
+    if constexpr (STAGES == 3)
+      run_main_loop_deep<kLoads>(smem, STAGE, nfull, nk, ragged_k, issue_direct, stage_ragged, load_frags, compute, interleave);
+    else
+      run_main_loop(s0, s1, nfull, nk, ragged_k, issue_direct, stage_ragged, load_frags, compute, interleave, MXE);
 
     // Lane l holds row m = l & 31 of each 32x32 block (the A operand went
     // second) and columns n = 8g + 4(l >> 5) + 0..3 in registers 4g..4g+3.

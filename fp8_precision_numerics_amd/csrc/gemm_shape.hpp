@@ -6,25 +6,27 @@
 
 namespace fp8mi {
 
-// A compute unit holds one 256 x 256 tile, two of
-// 128 x 128 or three of 64 x 128; the larger ones need fewer operand bytes a
-// product, the smaller ones fill the chip with fewer rows and columns, and a split
-// fills it where even those are few (only with a workspace for the parts).  The choice is the least of an estimate in
-// microseconds, from step times (a K step of 128) measured on MI355X:
+// The larger tiles need fewer operand bytes a product; the smaller ones fill the chip
+// with fewer rows and columns, and a split of K fills it where even those are few (only
+// with a workspace for the parts).  64 x 128 tiles with three stages of loads (two
+// workgroups a compute unit instead of three) take a shorter step where few of them
+// share a compute unit.  The choice is the least of an estimate in microseconds, from
+// step times (a K step of 128) measured on MI355X:
 //
 //   L = the most workgroups that any compute unit gets, S = K steps of a part
 //   start + S max(alone, L each) + (split: second launch + traffic of the partials)
 //
 // `alone` is the step of a lone workgroup (latency-bound), `each` the step's share
 // of a busy compute unit.  At M x N x K the choices measured (exact mode, us; 256,
-// 128 and 64 stand for the three shapes, /s for the split):
+// 128, 64 and 64t stand for the shapes, t for three stages, /s for the split):
 //   8192 x 4096 x 16384   256: 715   128: 784   64: 876
-//   1003 x 16384 x 4096   256: 103   128: 115   64: 127
-//   2048 x 4096 x 4096    256: 84    128: 58    64: 67
-//   500 x 4096 x 16384    256/6: 74  128/4: 66  64/2: 70   64: 96
-//   64 x 4096 x 16384     64: 96     64/4: 34   64/8: 24   64/16: 30
+//   1003 x 16384 x 4096   256: 102   128: 115   64: 126   64t: 140
+//   2048 x 4096 x 4096    256: 77    128: 57    64: 66    64t: 70
+//   500 x 4096 x 16384    256/6: 73  128/4: 66  64/2: 70  64t/2: 72   64: 95
+//   64 x 4096 x 16384     64: 96     64/8: 24   64t: 69   64t/6: 23
+//   24 x 4096 x 16384     64/12: 22  64t/8: 20
 struct TileChoice {
-  int shape;  // 0: 256 x 256, 1: 128 x 128, 2: 64 x 128
+  int shape;  // 0: 256 x 256, 1: 128 x 128, 2: 64 x 128, 3: 64 x 128 in three stages
   int split;
 };
 
@@ -33,13 +35,15 @@ inline TileChoice choose_tile(int64_t M, int64_t brows, int64_t K, int mode, siz
     int bm, bn;
     double start, alone, each;
   };
-  static constexpr Cost kExact[3] = {{256, 256, 14.0, 2.4, 2.8}, {128, 128, 6.0, 0.90, 0.80}, {64, 128, 4.0, 0.73, 0.45}};
-  static constexpr Cost kFp8[3] = {{256, 256, 8.0, 1.25, 1.5}, {128, 128, 5.0, 0.90, 0.52}, {64, 128, 3.5, 0.73, 0.33}};
+  static constexpr Cost kExact[4] = {{256, 256, 14.0, 2.4, 2.8}, {128, 128, 6.0, 0.90, 0.80}, {64, 128, 4.0, 0.73, 0.45},
+                                     {64, 128, 4.0, 0.50, 0.53}};
+  static constexpr Cost kFp8[4] = {{256, 256, 8.0, 1.25, 1.5}, {128, 128, 5.0, 0.90, 0.52}, {64, 128, 3.5, 0.73, 0.35},
+                                   {64, 128, 3.5, 0.44, 0.38}};
   const Cost* costs = mode == kAccumMfma8 ? kFp8 : kExact;
   const int64_t cus = persistent_groups(1), steps = (K + kBK - 1) / kBK;
   TileChoice best{2, 1};
   double least = 1e300;
-  for (int i = 0; i < 3; ++i) {
+  for (int i = 0; i < 4; ++i) {
     const Cost& c = costs[i];
     const int64_t tiles = ((M + c.bm - 1) / c.bm) * ((brows + c.bn - 1) / c.bn);
     for (int split = 1; split <= 32 && split <= steps; split = split < 4 ? split + 1 : split + split / 2) {
