@@ -7,7 +7,9 @@
 //   GEMM takes as its K-contiguous operand), amax = max |d|, and for the first
 //   dbias_n = sum_m d.
 //
-// HBM-bound: one read of the inputs, one write of each orientation.  A workgroup
+// HBM-bound: one read of the inputs, one write of each orientation.  Measured on
+// MI355X: gated, 8192 x 2 x 16384, 233 us (1.34 GB, 5.8 TB/s); with bias gradient and
+// GELU, 4096 x 16384, 77 us (0.40 GB, 5.2 TB/s).  A workgroup
 // takes 128 x 128 tiles of d (gated: the gate's and the up projection's tile of
 // the same 128 x 128 of dh, so that dh is read once); codes go out row-major
 // straight from the registers and column-major through LDS with 4 x 4 byte
@@ -79,7 +81,7 @@ __global__ __launch_bounds__(kNT, 4) void act_backward_kernel(BackArgs a) {
     // Pass i covers rows row0 + 16 i + rr0.  Addresses: a uniform base per pass plus the
     // lane's 32-bit offset, the same for every pass.  Four passes' loads are issued
     // before the first is used, held as they were loaded: widened, they took 256
-    // registers and left one wave a SIMD (416 us against @US@ us for 8192 x 2 x 16384).
+    // registers and left one wave a SIMD (416 us against 233 us for 8192 x 2 x 16384).
     auto passes = [&](int i0, auto whole) {
       Raw8<XT> dy[4];
       Raw8<kBF16> z[4], u[GATED ? 4 : 1];
@@ -262,8 +264,9 @@ hipError_t back_launch(BackArgs a, int xtype, int fmt, int act, float* dbias, fl
     workspace_bytes = ws ? workspace_bytes - used : 0;
   }
   const int64_t groups = walks * strips;
-  if (stats && ws && workspace_bytes >= (size_t)groups * sizeof(uint4)) a.stat_slots = reinterpret_cast<uint4*>(ws);
-  if (stats && !a.stat_slots) {
+  const bool gather = stats && groups != 1;  // a single workgroup writes the statistics itself
+  if (gather && ws && workspace_bytes >= (size_t)groups * sizeof(uint4)) a.stat_slots = reinterpret_cast<uint4*>(ws);
+  if (gather && !a.stat_slots) {
     const hipError_t e = launch_clear_stats(amax, a.sat, st);
     if (e != hipSuccess) return e;
   }

@@ -224,7 +224,10 @@ __device__ __forceinline__ void clear_epilogue_stats(const EpiArgs& a) {
 // pass is staged.
 // The row loop is rolled on purpose: unrolled, the kernel had 85 KiB of code, each
 // instruction of the epilogue ran once a pass, and fetching them from memory cost
-// about 40 us a launch (2048 x 4096 x 4096: @ROLLED@).
+// about 40 us a launch (2048 x 4096 x 4096 exact on these tiles:
+// 105 us against 84).  The next row's values are read from LDS while the present row is
+// worked on (8192 x 2 x 16384 x 4096 exact: 1552 against 1474 us, a plain GEMM of that
+// size beside them 1511 and 1451).
 template <int BN, int NT, int PASS, int PAIR, class TW>
 struct EpiPass {
   static constexpr bool GATED = PAIR != 0;

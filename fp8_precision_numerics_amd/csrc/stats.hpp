@@ -37,6 +37,9 @@ __device__ __forceinline__ void block_finish(uint32_t amx, uint32_t wave_cnt, ui
     }
     if (partials) {
       partials[blockIdx.x] = make_uint4(m, 0u, (uint32_t)c, (uint32_t)(c >> 32));
+    } else if (gridDim.x == 1) {  // the only one: no clearing needed beforehand
+      if (amax_bits) *amax_bits = m;
+      if (sat) *sat = c;
     } else {
       // The output only grows, so an older value of it is a safe bound: the atomic is
       // skipped where it would change nothing.

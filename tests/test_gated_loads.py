@@ -86,3 +86,11 @@ def test_few_row_chunks_cover_k_once(chunks, split):
                 k = c + first
                 taken.append(k if k < chunks else k - chunks)
         assert sorted(taken) == list(range(chunks))
+
+
+@pytest.mark.parametrize("nfull", [1, 2, 7, 8, 32, 127])
+def test_turned_k_steps_are_each_taken_once(nfull):
+    for xcd in range(8):
+        turn = (xcd * nfull) >> 3
+        steps = [kt + turn - (nfull if kt + turn >= nfull else 0) for kt in range(nfull)]
+        assert sorted(steps) == list(range(nfull))
