@@ -201,6 +201,7 @@ _FLOATS = (torch.float32, torch.bfloat16)
 # around them (about 2 us of a small call).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _FUNCTIONS = {}
 
 
@@ -242,7 +243,7 @@ def _space(workspace, dev):
 
 
 def _launch(name, dev, stream, *args):
-    if torch.cuda.current_device() != dev:
+    if _current_device() != dev:
         with torch.cuda.device(dev):
             return _launch(name, dev, stream, *args)
     if stream is None:

@@ -14,10 +14,14 @@ namespace fp8mi {
 // step times (a K step of 128) measured on MI355X:
 //
 //   L = the most workgroups that any compute unit gets, S = K steps of a part
-//   start + S max(alone, L each) + (split: second launch + traffic of the partials)
+//   start + S max(alone, L each odd) + (split: second launch + traffic of the partials)
 //
-// `alone` is the step of a lone workgroup (latency-bound), `each` the step's share
-// of a busy compute unit.  At M x N x K the choices measured (exact mode, us; 256,
+// `alone` is the step of a lone workgroup (latency-bound), `each` the step's share of a
+// busy compute unit, `odd` its growth where K is no multiple of 128 and the 128 bytes
+// of a row and step lie in two cache lines (8192 x 4096 on the FP8 cores: 108 us at
+// K = 4096, 133 at 4112).  The constants are a least-squares fit to 100 products of
+// random and of round sizes; over them the choice is 4 % slower than the best shape
+// and split of each, 30 % at worst.  At M x N x K the choices measured (exact mode, us; 256,
 // 128, 64 and 64t stand for the shapes, t for three stages, /s for the split):
 //   8192 x 4096 x 16384   256: 715   128: 784   64: 876
 //   1003 x 16384 x 4096   256: 102   128: 115   64: 126   64t: 140
@@ -33,12 +37,16 @@ struct TileChoice {
 inline TileChoice choose_tile(int64_t M, int64_t brows, int64_t K, int mode, size_t workspace_bytes) {
   struct Cost {
     int bm, bn;
-    double start, alone, each;
+    double start, alone, each, odd;
   };
-  static constexpr Cost kExact[4] = {{256, 256, 14.0, 2.4, 2.8}, {128, 128, 6.0, 0.90, 0.80}, {64, 128, 4.0, 0.73, 0.45},
-                                     {64, 128, 4.0, 0.50, 0.53}};
-  static constexpr Cost kFp8[4] = {{256, 256, 8.0, 1.25, 1.5}, {128, 128, 5.0, 0.90, 0.52}, {64, 128, 3.5, 0.73, 0.35},
-                                   {64, 128, 3.5, 0.44, 0.38}};
+  static constexpr Cost kExact[4] = {{256, 256, 10.5, 2.13, 2.22, 1.04},
+                                     {128, 128, 6.9, 0.86, 0.72, 1.11},
+                                     {64, 128, 6.4, 0.60, 0.43, 1.20},
+                                     {64, 128, 6.6, 0.48, 0.49, 1.12}};
+  static constexpr Cost kFp8[4] = {{256, 256, 9.0, 1.00, 1.27, 1.23},
+                                   {128, 128, 6.3, 0.77, 0.50, 1.23},
+                                   {64, 128, 5.7, 0.60, 0.34, 1.32},
+                                   {64, 128, 5.9, 0.39, 0.35, 1.27}};
   const Cost* costs = mode == kAccumMfma8 ? kFp8 : kExact;
   const int64_t cus = persistent_groups(1), steps = (K + kBK - 1) / kBK;
   TileChoice best{2, 1};
@@ -50,9 +58,10 @@ inline TileChoice choose_tile(int64_t M, int64_t brows, int64_t K, int mode, siz
       const double traffic = (double)split * M * brows * 4.0;
       if (split > 1 && (traffic > (double)workspace_bytes || tiles * split > 4 * cus)) break;
       const int64_t load = (tiles * split + cus - 1) / cus;
-      const double step = c.alone > load * c.each ? c.alone : load * c.each;
+      const double busy = load * c.each * (K % kBK ? c.odd : 1.0);
+      const double step = c.alone > busy ? c.alone : busy;
       const double t = c.start + (double)((steps + split - 1) / split) * step +
-                       (split > 1 ? 4.0 + 2.0 * traffic / 5.0e6 : 0.0);
+                       (split > 1 ? 2.0 + 2.0 * traffic / 5.2e6 : 0.0);
       if (t < least) {
         least = t;
         best = TileChoice{i, split};
