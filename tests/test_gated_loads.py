@@ -94,3 +94,11 @@ def test_turned_k_steps_are_each_taken_once(nfull):
         turn = (xcd * nfull) >> 3
         steps = [kt + turn - (nfull if kt + turn >= nfull else 0) for kt in range(nfull)]
         assert sorted(steps) == list(range(nfull))
+
+
+@pytest.mark.parametrize("groups", [1, 7, 8, 9, 24, 1972, 2047])
+def test_strips_by_xcd_is_a_bijection(groups):
+    """The gradients' workgroup order where rows are no multiple of 128 bytes (act_backward.hip)."""
+    each, more = groups >> 3, groups & 7
+    places = [(b & 7) * each + min(b & 7, more) + (b >> 3) for b in range(groups)]
+    assert sorted(places) == list(range(groups))
