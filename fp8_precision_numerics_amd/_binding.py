@@ -1,4 +1,4 @@
-"""ctypes binding of libfp8mi (include/fp8mi.h): argument marshalling only.
+"""Binding of libfp8mi (include/fp8mi.h): argument marshalling only, with ctypes and csrc/marshal.cpp.
 
 Every function here takes torch tensors that already live on the GPU, turns
 them into raw device pointers, sizes and enum codes, and calls the C entry
@@ -29,8 +29,7 @@ ACCUM_EXACT, ACCUM_MFMA_FP8 = 0, 1
 FORMATS = {"e4m3": E4M3, "e5m2": E5M2, E4M3: E4M3, E5M2: E5M2}
 ACCUMS = {"exact": ACCUM_EXACT, "mfma_fp8": ACCUM_MFMA_FP8, ACCUM_EXACT: ACCUM_EXACT,
           ACCUM_MFMA_FP8: ACCUM_MFMA_FP8}
-ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
-OUT_E4M3, OUT_E5M2 = 2, 3  # output kinds of the fused GEMMs besides F32 and BF16
+ACTIVATIONS = ("none", "relu", "silu", "gelu")
 
 EXPORTED_SYMBOLS = ("fp8mi_status_string", "fp8mi_version", "fp8_quantize", "fp8_amax_update",
                     "fp8_gemm", "fp8_quantize_blockwise", "fp8_grouped_gemm", "fp8_gemm_requant",
@@ -192,70 +191,53 @@ def _call(name, status):
         raise Fp8Error(name, status)
 
 
-# Marshalling for the calls whose smallest sizes run for a few microseconds: each
-# property is read once, and the device is switched only where the operands are on
-# another one.
-_FLOATS = (torch.float32, torch.bfloat16)
-
+# The calls whose smallest sizes run for a few microseconds (fp8_gemm and the
+# feed-forward operators) are marshalled by the extension module of csrc/marshal.cpp.
+_MARSHALLED = ("fp8_gemm", "fp8_gemm_gated", "fp8_gemm_fused", "fp8_rmsnorm_quantize", "fp8_rmsnorm_quantize_blockwise",
+               "fp8_rmsnorm_backward", "fp8_act_backward", "fp8_gated_backward")
+_MODULE = None
 # The current stream's handle and device without building the Python objects
 # around them (about 2 us of a small call).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
-_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-_FUNCTIONS = {}
+_device_index = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _dev_of(t, name):
-    """Index of the GPU that t is on."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor")
-    return t.get_device()
+def _load_module():
+    """The marshalling module, bound to the library that load_library gives."""
+    global _MODULE
+    import importlib.util
+
+    lib = load_library()
+    path = os.path.join(_HERE, "lib", "_fp8mi_marshal.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"the marshalling module is not built ({path} missing); run __graft_entry__.build() "
+                           "or python -m fp8_precision_numerics_amd.build")
+    spec = importlib.util.spec_from_file_location("_fp8mi_marshal", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    module.bind(*[ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in _MARSHALLED])
+    _MODULE = module
+    return module
 
 
-def _ptr(t, name, dtype, shape, dev):
-    """Address of a contiguous operand of that type, shape and device (None: not given)."""
-    if t is None:
-        return None
-    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and (shape is None or t.shape == shape):
-        return t.data_ptr()
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
-    raise ValueError(f"{name} must be contiguous")
-
-
-def _scalar(t, name, dev, dtype=torch.float32):
-    if t is None:
-        return None
-    if t.numel() != 1:
-        raise ValueError(f"{name} must have 1 element, got {t.numel()}")
-    return _ptr(t, name, dtype, None, dev)
-
-
-def _space(workspace, dev):
-    """(address, bytes) of an optional workspace."""
-    if workspace is None:
-        return None, 0
-    return _ptr(workspace, "workspace", torch.uint8, None, dev), workspace.numel()
-
-
-def _launch(name, dev, stream, *args):
-    if _current_device() != dev:
-        with torch.cuda.device(dev):
-            return _launch(name, dev, stream, *args)
+def _where(stream):
+    """(current device, handle of the stream to use on it).  Without a GPU the operands' own check answers."""
+    try:
+        index = _device_index()
+    except (RuntimeError, AssertionError):
+        return -1, 0
     if stream is None:
-        handle = _raw_stream(dev)
-    else:
-        handle = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-    fn = _FUNCTIONS.get(name)
-    if fn is None:
-        fn = _FUNCTIONS[name] = getattr(load_library(), name)
-    status = fn(*args, handle)
-    if status != 0:
-        raise Fp8Error(name, status)
+        return index, _raw_stream(index)
+    return index, stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _settle(status, entry, *args):
+    """What a marshalled call's non-zero answer asks for: an error, or the same call on its operands' device."""
+    if status < 0:
+        raise Fp8Error(entry.__name__, status)
+    with torch.cuda.device(status - 1):
+        return entry(*args)
 
 
 # ---------------------------------------------------------------------------
@@ -362,19 +344,10 @@ def fp8_gemm(a, fa, b, fb, sinv_a, sinv_b, c, accum="exact", b_trans=False, stre
     accum: "exact" (every product exact, fp32 sums) or "mfma_fp8" (native FP8
     matrix cores; see include/fp8mi.h for their arithmetic).
     """
-    dev = _dev_of(a, "a")
-    pa, pb = _ptr(a, "a", torch.uint8, None, dev), _ptr(b, "b", torch.uint8, None, dev)
-    if c.dtype not in _FLOATS:
-        raise TypeError(f"c must be {_FLOATS}, got {c.dtype}")
-    pc = _ptr(c, "c", c.dtype, None, dev)
-    M, K = a.shape
-    K2, N = b.shape if b_trans else (b.shape[1], b.shape[0])
-    if K2 != K or tuple(c.shape) != (M, N):
-        raise ValueError(f"shape mismatch: a {tuple(a.shape)}, b {tuple(b.shape)} (b_trans={bool(b_trans)}), "
-                         f"c {tuple(c.shape)}")
-    _launch("fp8_gemm", dev, stream, pa, _fmt(fa), pb, _fmt(fb), 1 if b_trans else 0, M, N, K,
-            _scalar(sinv_a, "sinv_a", dev), _scalar(sinv_b, "sinv_b", dev), pc,
-            F32 if c.dtype == torch.float32 else BF16, _accum(accum))
+    index, handle = _where(stream)
+    status = (_MODULE or _load_module()).gemm(index, handle, a, fa, b, fb, sinv_a, sinv_b, c, accum, b_trans)
+    if status:
+        _settle(status, fp8_gemm, a, fa, b, fb, sinv_a, sinv_b, c, accum, b_trans, stream)
 
 
 def fp8_gemm_requant(a, fa, b, fb, sinv_a, sinv_b, out_fmt, out_scale, cq, amax=None, sat=None, accum="exact",
@@ -520,25 +493,6 @@ def fp8_grouped_gemm(a, sinv_a, b, sinv_b, m_offsets, c, accum="exact", stream=N
 # ---------------------------------------------------------------------------
 # feed-forward operators
 # ---------------------------------------------------------------------------
-def _act(a) -> int:
-    try:
-        return ACTIVATIONS[a]
-    except KeyError:
-        raise ValueError(f"unknown activation {a!r}") from None
-
-
-def _norm_operands(x, weight, residual, sum_out, q, rstd):
-    dev = _dev_of(x, "x")
-    if x.dim() != 2 or x.dtype not in _FLOATS:
-        raise ValueError("x must be a [rows x cols] float32 or bfloat16 tensor")
-    shape, t = x.shape, x.dtype
-    rows, cols = shape
-    return (dev, rows, cols, BF16 if t is torch.bfloat16 else F32, _ptr(x, "x", t, None, dev),
-            _ptr(residual, "residual", t, shape, dev), _ptr(weight, "weight", t, (cols,), dev),
-            _ptr(sum_out, "sum_out", t, shape, dev), _ptr(q, "q", torch.uint8, shape, dev),
-            _ptr(rstd, "rstd", torch.float32, (rows,), dev))
-
-
 def fp8_rmsnorm_quantize(x, weight, eps, fmt, scale, q, residual=None, sum_out=None, rstd=None, amax=None, sat=None,
                          workspace=None, stream=None) -> None:
     """q = FP8 codes of fp32(norm(h) * weight * scale), h = x + residual rounded to x's type.
@@ -547,51 +501,33 @@ def fp8_rmsnorm_quantize(x, weight, eps, fmt, scale, q, residual=None, sum_out=N
     weight: [cols] of the same type; scale: fp32[1]; q: uint8 [rows x cols]; rstd: fp32 [rows];
     amax / sat: fp32[1] / int64[1], overwritten; workspace: optional uint8 scratch for the statistics.
     cols must be a multiple of 16."""
-    dev, rows, cols, xtype, px, pr, pw, ps, pq, prs = _norm_operands(x, weight, residual, sum_out, q, rstd)
-    ws, ws_bytes = _space(workspace, dev)
-    _launch("fp8_rmsnorm_quantize", dev, stream, px, pr, pw, xtype, rows, cols, eps, _fmt(fmt),
-            _scalar(scale, "scale", dev), ps, pq, prs, _scalar(amax, "amax", dev), _scalar(sat, "sat", dev, torch.int64),
-            ws, ws_bytes)
+    index, handle = _where(stream)
+    status = (_MODULE or _load_module()).norm(index, handle, x, weight, eps, fmt, scale, q, residual, sum_out, rstd,
+        amax, sat, workspace)
+    if status:
+        _settle(status, fp8_rmsnorm_quantize, x, weight, eps, fmt, scale, q, residual, sum_out, rstd, amax, sat,
+                workspace, stream)
 
 
 def fp8_rmsnorm_quantize_blockwise(x, weight, eps, fmt, q, scale_inv, residual=None, sum_out=None, rstd=None,
                                    stream=None) -> None:
     """fp8_rmsnorm_quantize with current scaling per 128 values of a row: scale_inv fp32 [rows x ceil(cols/128)]."""
-    dev, rows, cols, xtype, px, pr, pw, ps, pq, prs = _norm_operands(x, weight, residual, sum_out, q, rstd)
-    _launch("fp8_rmsnorm_quantize_blockwise", dev, stream, px, pr, pw, xtype, rows, cols, eps, _fmt(fmt), ps, pq,
-            _ptr(scale_inv, "scale_inv", torch.float32, (rows, (cols + 127) // 128), dev), prs)
+    index, handle = _where(stream)
+    status = (_MODULE or _load_module()).norm_blocks(index, handle, x, weight, eps, fmt, q, scale_inv, residual,
+        sum_out, rstd)
+    if status:
+        _settle(status, fp8_rmsnorm_quantize_blockwise, x, weight, eps, fmt, q, scale_inv, residual, sum_out, rstd,
+                stream)
 
 
 def fp8_rmsnorm_backward(dy, h, rstd, weight, dx, dweight=None, dresidual=None, workspace=None, stream=None) -> None:
     """Gradient of the norm: dx = that of h (plus dresidual), dweight fp32 [cols] (needs a workspace of at least
     one fp32 row).  dy, h, dresidual, dx: [rows x cols] of one type; rstd: the forward's."""
-    dev = _dev_of(dy, "dy")
-    if dy.dim() != 2 or dy.dtype not in _FLOATS:
-        raise ValueError("dy must be a [rows x cols] float32 or bfloat16 tensor")
-    shape, t = dy.shape, dy.dtype
-    rows, cols = shape
-    ws, ws_bytes = _space(workspace, dev)
-    _launch("fp8_rmsnorm_backward", dev, stream, _ptr(dy, "dy", t, None, dev), _ptr(h, "h", t, shape, dev),
-            _ptr(rstd, "rstd", torch.float32, (rows,), dev), _ptr(weight, "weight", t, (cols,), dev),
-            _ptr(dresidual, "dresidual", t, shape, dev), BF16 if t is torch.bfloat16 else F32, rows, cols,
-            _ptr(dx, "dx", t, shape, dev), _ptr(dweight, "dweight", torch.float32, (cols,), dev), ws, ws_bytes)
-
-
-def _output(y, name, out_fmt, shape, dev):
-    """(address, output kind) of a fused GEMM's output."""
-    if out_fmt is not None:
-        kind = OUT_E4M3 if _fmt(out_fmt) == E4M3 else OUT_E5M2
-        return _ptr(y, name, torch.uint8, shape, dev), kind
-    if y.dtype not in _FLOATS:
-        raise TypeError(f"{name} must be float32 or bfloat16, or have an out_fmt, got {y.dtype}")
-    return _ptr(y, name, y.dtype, shape, dev), BF16 if y.dtype is torch.bfloat16 else F32
-
-
-def _codes(a, b):
-    dev = _dev_of(a, "a")
-    if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1]:
-        raise ValueError(f"shape mismatch: a {tuple(a.shape)}, b {tuple(b.shape)}")
-    return dev, a.shape[0], b.shape[0], a.shape[1], _ptr(a, "a", torch.uint8, None, dev), _ptr(b, "b", torch.uint8, None, dev)
+    index, handle = _where(stream)
+    status = (_MODULE or _load_module()).norm_back(index, handle, dy, h, rstd, weight, dx, dweight, dresidual,
+        workspace)
+    if status:
+        _settle(status, fp8_rmsnorm_backward, dy, h, rstd, weight, dx, dweight, dresidual, workspace, stream)
 
 
 def fp8_gemm_gated(a, fa, b, fb, sinv_a, sinv_b, act, h, gu=None, out_fmt=None, out_scale=None, amax=None, sat=None,
@@ -599,58 +535,43 @@ def fp8_gemm_gated(a, fa, b, fb, sinv_a, sinv_b, act, h, gu=None, out_fmt=None, 
     """h [M x F] = act(g) * u with [g | u] = (A · Bᵀ) · sinv_a · sinv_b, b [2F x K] the gate's rows then the up
     projection's.  h: fp32 or bf16, or uint8 codes with out_fmt and out_scale (then amax / sat of h may be had);
     gu: bf16 [M x 2F] or None, receives g and u; act: "none", "relu", "silu" or "gelu"; accum as for fp8_gemm."""
-    dev, M, rows, K, pa, pb = _codes(a, b)
-    if rows & 1:
-        raise ValueError(f"b must hold gate and up rows, got {rows} rows")
-    F = rows // 2
-    ph, kind = _output(h, "h", out_fmt, (M, F), dev)
-    ws, ws_bytes = _space(workspace, dev)
-    _launch("fp8_gemm_gated", dev, stream, pa, _fmt(fa), pb, _fmt(fb), M, F, K, _scalar(sinv_a, "sinv_a", dev),
-            _scalar(sinv_b, "sinv_b", dev), _act(act), ph, kind, _scalar(out_scale, "out_scale", dev),
-            _ptr(gu, "gu", torch.bfloat16, (M, rows), dev), _scalar(amax, "amax", dev),
-            _scalar(sat, "sat", dev, torch.int64), _accum(accum), ws, ws_bytes)
+    index, handle = _where(stream)
+    status = (_MODULE or _load_module()).gated(index, handle, a, fa, b, fb, sinv_a, sinv_b, act, h, gu, out_fmt,
+        out_scale, amax, sat, accum, workspace)
+    if status:
+        _settle(status, fp8_gemm_gated, a, fa, b, fb, sinv_a, sinv_b, act, h, gu, out_fmt, out_scale, amax, sat,
+                accum, workspace, stream)
 
 
 def fp8_gemm_fused(a, fa, b, fb, sinv_a, sinv_b, y, bias=None, act="none", residual=None, z=None, out_fmt=None,
                    out_scale=None, amax=None, sat=None, accum="exact", workspace=None, stream=None) -> None:
     """y [M x N] = act(z) + residual, z = (A · Bᵀ) · sinv_a · sinv_b + bias.  bias bf16 [N], residual bf16 [M x N]
     (it may be y), z: bf16 [M x N] or None, receives z; y, amax and sat as h's of fp8_gemm_gated."""
-    dev, M, N, K, pa, pb = _codes(a, b)
-    py, kind = _output(y, "y", out_fmt, (M, N), dev)
-    ws, ws_bytes = _space(workspace, dev)
-    _launch("fp8_gemm_fused", dev, stream, pa, _fmt(fa), pb, _fmt(fb), M, N, K, _scalar(sinv_a, "sinv_a", dev),
-            _scalar(sinv_b, "sinv_b", dev), _ptr(bias, "bias", torch.bfloat16, (N,), dev), _act(act),
-            _ptr(residual, "residual", torch.bfloat16, (M, N), dev), py, kind, _scalar(out_scale, "out_scale", dev),
-            _ptr(z, "z", torch.bfloat16, (M, N), dev), _scalar(amax, "amax", dev),
-            _scalar(sat, "sat", dev, torch.int64), _accum(accum), ws, ws_bytes)
-
-
-def _gradient(dy, name):
-    dev = _dev_of(dy, name)
-    if dy.dim() != 2 or dy.dtype not in _FLOATS:
-        raise ValueError(f"{name} must be a 2-d float32 or bfloat16 tensor")
-    return dev, dy.shape[0], dy.shape[1], BF16 if dy.dtype is torch.bfloat16 else F32, _ptr(dy, name, dy.dtype, None, dev)
+    index, handle = _where(stream)
+    status = (_MODULE or _load_module()).fused(index, handle, a, fa, b, fb, sinv_a, sinv_b, y, bias, act, residual, z,
+        out_fmt, out_scale, amax, sat, accum, workspace)
+    if status:
+        _settle(status, fp8_gemm_fused, a, fa, b, fb, sinv_a, sinv_b, y, bias, act, residual, z, out_fmt, out_scale,
+                amax, sat, accum, workspace, stream)
 
 
 def fp8_act_backward(dy, z, act, fmt, scale, q=None, q_t=None, dbias=None, amax=None, sat=None, workspace=None,
                      stream=None) -> None:
     """d = dy · act'(z) cast to FP8: codes q [M x N] and / or q_t [N x M], dbias fp32 [N] = column sums of d (needs a
     workspace of at least one fp32 row), amax and sat of d.  z: bf16 [M x N], the forward's (None with act "none")."""
-    dev, M, N, xtype, pd = _gradient(dy, "dy")
-    ws, ws_bytes = _space(workspace, dev)
-    _launch("fp8_act_backward", dev, stream, pd, xtype, _ptr(z, "z", torch.bfloat16, (M, N), dev), _act(act), M, N,
-            _fmt(fmt), _scalar(scale, "scale", dev), _ptr(q, "q", torch.uint8, (M, N), dev),
-            _ptr(q_t, "q_t", torch.uint8, (N, M), dev), _ptr(dbias, "dbias", torch.float32, (N,), dev),
-            _scalar(amax, "amax", dev), _scalar(sat, "sat", dev, torch.int64), ws, ws_bytes)
+    index, handle = _where(stream)
+    status = (_MODULE or _load_module()).act_back(index, handle, dy, z, act, fmt, scale, q, q_t, dbias, amax, sat,
+        workspace)
+    if status:
+        _settle(status, fp8_act_backward, dy, z, act, fmt, scale, q, q_t, dbias, amax, sat, workspace, stream)
 
 
 def fp8_gated_backward(dh, gu, act, fmt, scale, q=None, q_t=None, amax=None, sat=None, workspace=None,
                        stream=None) -> None:
     """d = [dh · u · act'(g) | dh · act(g)] cast to FP8: codes q [M x 2F] and / or q_t [2F x M], amax and sat of d.
     gu: bf16 [M x 2F], the forward's."""
-    dev, M, F, xtype, pd = _gradient(dh, "dh")
-    ws, ws_bytes = _space(workspace, dev)
-    _launch("fp8_gated_backward", dev, stream, pd, xtype, _ptr(gu, "gu", torch.bfloat16, (M, 2 * F), dev), _act(act),
-            M, F, _fmt(fmt), _scalar(scale, "scale", dev), _ptr(q, "q", torch.uint8, (M, 2 * F), dev),
-            _ptr(q_t, "q_t", torch.uint8, (2 * F, M), dev), _scalar(amax, "amax", dev),
-            _scalar(sat, "sat", dev, torch.int64), ws, ws_bytes)
+    index, handle = _where(stream)
+    status = (_MODULE or _load_module()).gated_back(index, handle, dh, gu, act, fmt, scale, q, q_t, amax, sat,
+        workspace)
+    if status:
+        _settle(status, fp8_gated_backward, dh, gu, act, fmt, scale, q, q_t, amax, sat, workspace, stream)

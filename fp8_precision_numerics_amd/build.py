@@ -1,4 +1,5 @@
-"""Build libfp8mi.so (the HIP/CDNA4 kernels and the C ABI) in-tree for gfx950.
+"""Build libfp8mi.so (the HIP/CDNA4 kernels and the C ABI) in-tree for gfx950, and the
+Python extension module that marshals tensors into it (host code).
 
     python -m fp8_precision_numerics_amd.build        # or: from ... import build_library
 
@@ -28,6 +29,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIBDIR = os.path.join(PKG, "lib")
 LIBPATH = os.path.join(LIBDIR, "libfp8mi.so")
+MARSHALPATH = os.path.join(LIBDIR, "_fp8mi_marshal.so")
 BUILDDIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["api.hip", "quantize.hip", "amax_update.hip", "gemm.hip", "gemm_requant.hip", "grouped_gemm.hip", "allreduce.hip", "mx.hip", "rms_norm.hip", "act_backward.hip",
@@ -68,13 +70,38 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def build_marshal(verbose: bool = False) -> str:
+    """Compile the Python extension module that marshals tensors (host code only); returns its path."""
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    os.makedirs(LIBDIR, exist_ok=True)
+    tmp = MARSHALPATH + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-I", os.path.join(root, "include"), "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "marshal.cpp"), "-o", tmp,
+           "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"marshal.cpp failed:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, MARSHALPATH)
+    return MARSHALPATH
+
+
 def build_library(verbose: bool = False, jobs: int | None = None) -> str:
-    """Compile every HIP source and link libfp8mi.so; returns the library path."""
+    """Compile every HIP source and link libfp8mi.so, and the marshalling module beside it; returns the library path."""
     os.makedirs(BUILDDIR, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
     jobs = jobs or min(len(SOURCES), max(1, (os.cpu_count() or 2)))
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
+        marshal = ex.submit(build_marshal, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+        marshal.result()
     tmp = LIBPATH + ".tmp"
     cmd = [_hipcc(), "-shared", "-fPIC", f"--offload-arch={ARCH}", *objs, "-o", tmp]
     if verbose:
