@@ -64,13 +64,14 @@ class Fp8FeedForward:
             raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
 
     def quantize_weights(self, w_gate_up, w_down, stream=None):
-        """Cast the weights with their current scales: once a training step, or once
-        before serving."""
+        """Cast the weights with their current scales and set the scales of the next cast: once a
+        training step, or once before serving.  The products take the inverse of the scale that
+        the codes were cast with (scale_inv_used)."""
         T, H, F = self.shape
         self._check(w_gate_up, (2 * F, H), "w_gate_up")
         self._check(w_down, (H, F), "w_down")
-        self.state_gu.quantize(w_gate_up, q=self.qw_gu, stream=stream)
-        self.state_d.quantize(w_down, q=self.qw_d, stream=stream)
+        self.state_gu.quantize_update(w_gate_up, q=self.qw_gu, stream=stream)
+        self.state_d.quantize_update(w_down, q=self.qw_d, stream=stream)
 
     def forward(self, x, residual, weight, y, train=True, stream=None):
         """y = down(act(gate(n)) * up(n)) + s, with the weights' codes as they are.
@@ -83,10 +84,10 @@ class Fp8FeedForward:
                                 sum_out=None if residual is None else self.sum, rstd=self.rstd if train else None,
                                 amax=n.amax, workspace=ws, stream=stream)
         self._s = x if residual is None else self.sum
-        _b.fp8_gemm_gated(self.qn, n.fmt, self.qw_gu, self.state_gu.fmt, n.scale_inv, self.state_gu.scale_inv,
+        _b.fp8_gemm_gated(self.qn, n.fmt, self.qw_gu, self.state_gu.fmt, n.scale_inv, self.state_gu.scale_inv_used,
                           self.act, self.qh, gu=self.gu if train else None, out_fmt=h.fmt, out_scale=h.scale,
                           amax=h.amax, accum=self.accum, workspace=ws, stream=stream)
-        _b.fp8_gemm_fused(self.qh, h.fmt, self.qw_d, self.state_d.fmt, h.scale_inv, self.state_d.scale_inv, y,
+        _b.fp8_gemm_fused(self.qh, h.fmt, self.qw_d, self.state_d.fmt, h.scale_inv, self.state_d.scale_inv_used, y,
                           residual=self._s, accum=self.accum, workspace=ws, stream=stream)
 
     def backward(self, dy, weight, dx, dweight, dw_gate_up, dw_down, stream=None):
@@ -102,16 +103,19 @@ class Fp8FeedForward:
         kw = dict(accum=self.accum, b_trans=True, stream=stream)
         _b.fp8_act_backward(dy, None, "none", sy.fmt, sy.scale, q=self.qdy, q_t=self.qdy_t, amax=sy.amax, workspace=ws,
                             stream=stream)
-        _b.fp8_gemm(self.qdy, sy.fmt, self.qw_d, self.state_d.fmt, sy.scale_inv, self.state_d.scale_inv, self.dh, **kw)
+        _b.fp8_gemm(self.qdy, sy.fmt, self.qw_d, self.state_d.fmt, sy.scale_inv, self.state_d.scale_inv_used, self.dh,
+                    **kw)
         _b.fp8_gemm(self.qdy_t, sy.fmt, self.qh, self.state_h.fmt, sy.scale_inv, self.state_h.scale_inv, dw_down, **kw)
         _b.fp8_gated_backward(self.dh, self.gu, self.act, sg.fmt, sg.scale, q=self.qdgu, q_t=self.qdgu_t, amax=sg.amax,
                               workspace=ws, stream=stream)
-        _b.fp8_gemm(self.qdgu, sg.fmt, self.qw_gu, self.state_gu.fmt, sg.scale_inv, self.state_gu.scale_inv, self.dn, **kw)
+        _b.fp8_gemm(self.qdgu, sg.fmt, self.qw_gu, self.state_gu.fmt, sg.scale_inv, self.state_gu.scale_inv_used,
+                    self.dn, **kw)
         _b.fp8_gemm(self.qdgu_t, sg.fmt, self.qn, self.state_n.fmt, sg.scale_inv, self.state_n.scale_inv, dw_gate_up, **kw)
         _b.fp8_rmsnorm_backward(self.dn, self._s, self.rstd, weight, dx, dweight=dweight, dresidual=dy, workspace=ws,
                                 stream=stream)
 
     def update(self, stream=None):
-        """Push each tensor's amax into its history and set the next step's scales."""
-        for st in (self.state_n, self.state_gu, self.state_h, self.state_d, self.state_dy, self.state_dgu):
+        """Push the activations' and gradients' amaxes into their histories and set the next step's
+        scales.  The weights' are stepped where they are cast, so their codes outlive any number of updates."""
+        for st in (self.state_n, self.state_h, self.state_dy, self.state_dgu):
             st.update(stream=stream)

@@ -1,0 +1,64 @@
+"""What Fp8FeedForward keeps between its calls, on the GPU (tests/test_feed_forward_state.py follows the same orders
+of calls on the CPU).  Tolerance of a forward: four E4M3 casts, each off by at most half a step, 2^-4 relative
+(rms 2^-4 / sqrt(3) and less): sqrt(4 * 2^-8 / 3) = 0.073 of the branch in the 2-norm, and bf16's half step, 2^-8,
+of its sum with the residual stream."""
+
+import numpy as np
+import pytest
+import torch
+
+import fp8_precision_numerics_amd as fm
+from gpu_helpers import announce, device
+from oracle import feed_forward as ff
+
+pytestmark = pytest.mark.gpu
+T, H, F = 64, 256, 400
+
+
+def randn(seed, *shape, std=1.0):
+    return torch.from_numpy(np.random.default_rng(seed).normal(0, std, shape).astype(np.float32)).bfloat16().to(device())
+
+
+def inputs(seed=0):
+    return dict(x=randn(seed + 1, T, H), residual=randn(seed + 2, T, H), weight=(randn(seed + 3, H, std=0.1) + 1).bfloat16(),
+                w_gu=randn(seed + 4, 2 * F, H, std=0.25), w_d=randn(seed + 5, H, F, std=0.25), dy=randn(seed + 6, T, H))
+
+
+def block(accum="exact"):
+    return fm.Fp8FeedForward(T, H, F, accum=accum, device=device())
+
+
+def forward(ffn, d, train=True, y=None):
+    y = torch.empty(T, H, dtype=torch.bfloat16, device=device()) if y is None else y
+    ffn.forward(d["x"], d["residual"], d["weight"], y, train=train)
+    return y
+
+
+def backward(ffn, d):
+    o = dict(dx=torch.empty(T, H, dtype=torch.bfloat16, device=device()), dweight=torch.empty(H, device=device()),
+             dw_gu=torch.empty(2 * F, H, device=device()), dw_d=torch.empty(H, F, device=device()))
+    ffn.backward(d["dy"], d["weight"], o["dx"], o["dweight"], o["dw_gu"], o["dw_d"])
+    return o
+
+
+def check_forward(y, d):
+    s = d["x"].float() if d["residual"] is None else (d["x"].float() + d["residual"].float()).bfloat16().float()
+    s = s.double().cpu().numpy()
+    w = {k: d[k].double().cpu().numpy() for k in ("weight", "w_gu", "w_d")}
+    n, _ = ff.rms_norm(s, w["weight"], 1e-5)
+    branch = ff.gated(n @ w["w_gu"][:F].T, n @ w["w_gu"][F:].T, "silu") @ w["w_d"].T
+    off = np.linalg.norm(y.double().cpu().numpy() - s - branch)
+    assert off <= 0.073 * np.linalg.norm(branch) + 2.0 ** -8 * np.linalg.norm(s + branch), off / np.linalg.norm(branch)
+
+
+@pytest.mark.parametrize("accum", ["exact", "mfma_fp8"])
+def test_weights_cast_once_serve_any_number_of_updates(accum):
+    """The codes of the weights keep the scale they were cast with, whatever update() makes of the next one."""
+    announce(f"weights cast once {accum}")
+    ffn, d = block(accum), inputs()
+    ffn.quantize_weights(d["w_gu"], d["w_d"])
+    forward(ffn, d)                                    # h saturates at the first step's scale of 1
+    for _ in range(3):
+        ffn.update()
+        check_forward(forward(ffn, d), d)
+        backward(ffn, d)
