@@ -52,6 +52,9 @@ class Fp8FeedForward:
         u8, bf = dict(dtype=torch.uint8, device=dev), dict(dtype=torch.bfloat16, device=dev)
         T, H, F = tokens, hidden, ffn
         self.sum, self.rstd = torch.empty((T, H), **bf), torch.empty(T, dtype=torch.float32, device=dev)
+        # forward(train=False) has its own, so that what a backward takes stays as it is
+        self.sum_infer = torch.empty((T, H), **bf)
+        self.qn_infer, self.qh_infer = torch.empty((T, H), **u8), torch.empty((T, F), **u8)
         self.qn, self.qh, self.gu = torch.empty((T, H), **u8), torch.empty((T, F), **u8), torch.empty((T, 2 * F), **bf)
         self.qw_gu, self.qw_d = torch.empty((2 * F, H), **u8), torch.empty((H, F), **u8)
         self.qdy, self.qdy_t = torch.empty((T, H), **u8), torch.empty((H, T), **u8)
@@ -75,20 +78,28 @@ class Fp8FeedForward:
 
     def forward(self, x, residual, weight, y, train=True, stream=None):
         """y = down(act(gate(n)) * up(n)) + s, with the weights' codes as they are.
-        residual may be None (s = x).  train: keep what backward needs."""
+        residual may be None (s = x).
+
+        train: keep what backward needs, and the amaxes that update() takes.  Without it the
+        call changes nothing that a backward or an update() sees, so it may come between a
+        training forward and those; the scales that serving needs are settled by a few training
+        forwards, each with an update()."""
         T, H, F = self.shape
         self._check(x, (T, H), "x")
         self._check(y, (T, H), "y")
         n, h, ws = self.state_n, self.state_h, self.workspace
-        _b.fp8_rmsnorm_quantize(x, weight, self.eps, n.fmt, n.scale, self.qn, residual=residual,
-                                sum_out=None if residual is None else self.sum, rstd=self.rstd if train else None,
-                                amax=n.amax, workspace=ws, stream=stream)
-        self._s = x if residual is None else self.sum
-        _b.fp8_gemm_gated(self.qn, n.fmt, self.qw_gu, self.state_gu.fmt, n.scale_inv, self.state_gu.scale_inv_used,
-                          self.act, self.qh, gu=self.gu if train else None, out_fmt=h.fmt, out_scale=h.scale,
-                          amax=h.amax, accum=self.accum, workspace=ws, stream=stream)
-        _b.fp8_gemm_fused(self.qh, h.fmt, self.qw_d, self.state_d.fmt, h.scale_inv, self.state_d.scale_inv_used, y,
-                          residual=self._s, accum=self.accum, workspace=ws, stream=stream)
+        total, qn, qh = (self.sum, self.qn, self.qh) if train else (self.sum_infer, self.qn_infer, self.qh_infer)
+        _b.fp8_rmsnorm_quantize(x, weight, self.eps, n.fmt, n.scale, qn, residual=residual,
+                                sum_out=None if residual is None else total, rstd=self.rstd if train else None,
+                                amax=n.amax if train else None, workspace=ws, stream=stream)
+        s = x if residual is None else total
+        if train:
+            self._s = s
+        _b.fp8_gemm_gated(qn, n.fmt, self.qw_gu, self.state_gu.fmt, n.scale_inv, self.state_gu.scale_inv_used,
+                          self.act, qh, gu=self.gu if train else None, out_fmt=h.fmt, out_scale=h.scale,
+                          amax=h.amax if train else None, accum=self.accum, workspace=ws, stream=stream)
+        _b.fp8_gemm_fused(qh, h.fmt, self.qw_d, self.state_d.fmt, h.scale_inv, self.state_d.scale_inv_used, y,
+                          residual=s, accum=self.accum, workspace=ws, stream=stream)
 
     def backward(self, dy, weight, dx, dweight, dw_gate_up, dw_down, stream=None):
         """Gradients of the last forward(train=True): dx [tokens x hidden] bf16 (of x, hence of

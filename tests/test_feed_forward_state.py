@@ -184,3 +184,26 @@ def test_weights_recast_every_step_step_their_history_once():
         scale = float(448.0 / top_of(w.float()))
         assert torch.equal(ffn.state_gu.history[:step + 1], torch.stack([top_of((d["w_gu"].float() * (k + 1)).bfloat16().float())[0] for k in range(step + 1)]))
         assert not ffn.state_gu.history[step + 1:].any()
+
+
+@pytest.mark.parametrize("with_residual", [True, False])
+def test_inference_leaves_a_training_step_as_it_is(with_residual):
+    """forward(train=False) between a training forward and its backward and update: the gradients are those of the
+    training batch, bit for bit, and the next scales come from its amaxes."""
+    d, other = inputs(), inputs(50)
+    if not with_residual:
+        d["residual"] = None
+    out = []
+    for between in (False, True):
+        ffn = block()
+        ffn.quantize_weights(d["w_gu"], d["w_d"])
+        for _ in range(2):
+            y = forward(ffn, d)
+            if between:
+                assert torch.equal(forward(ffn, d, train=False), y)
+                forward(ffn, other, train=False)
+            o = backward(ffn, d)
+            ffn.update()
+        out.append(dict(o, y=y, **{k: getattr(ffn, k).history.clone() for k in ("state_n", "state_h", "state_dy", "state_dgu")}))
+    for k in out[0]:
+        assert torch.equal(out[0][k], out[1][k]), k

@@ -62,3 +62,28 @@ def test_weights_cast_once_serve_any_number_of_updates(accum):
         ffn.update()
         check_forward(forward(ffn, d), d)
         backward(ffn, d)
+
+
+@pytest.mark.parametrize("accum", ["exact", "mfma_fp8"])
+@pytest.mark.parametrize("with_residual", [True, False])
+def test_inference_leaves_a_training_step_as_it_is(with_residual, accum):
+    """forward(train=False) between a training forward and its backward and update: the gradients are those of the
+    training batch, bit for bit, and the next scales come from its amaxes."""
+    announce(f"inference between residual={with_residual} {accum}")
+    d, other = inputs(), inputs(50)
+    if not with_residual:
+        d["residual"] = None
+    out = []
+    for between in (False, True):
+        ffn = block(accum)
+        ffn.quantize_weights(d["w_gu"], d["w_d"])
+        for _ in range(2):
+            y = forward(ffn, d)
+            if between:
+                assert torch.equal(forward(ffn, d, train=False), y)
+                forward(ffn, other, train=False)
+            o = backward(ffn, d)
+            ffn.update()
+        out.append(dict(o, y=y, **{k: getattr(ffn, k).history.clone() for k in ("state_n", "state_h", "state_dy", "state_dgu")}))
+    for k in out[0]:
+        assert torch.equal(out[0][k], out[1][k]), k
