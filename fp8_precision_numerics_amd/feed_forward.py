@@ -29,6 +29,17 @@ from .state import DelayedScalingState, Recipe
 WORKSPACE_BYTES = 64 << 20
 
 
+def _overlap(a, b):
+    """Whether two contiguous tensors share memory."""
+    return (a.data_ptr() < b.data_ptr() + b.numel() * b.element_size()
+            and b.data_ptr() < a.data_ptr() + a.numel() * a.element_size())
+
+
+def _version(t):
+    """torch's count of the in-place changes of a tensor (inference tensors have none)."""
+    return None if t.is_inference() else t._version
+
+
 class Fp8FeedForward:
     """Buffers and delayed-scaling states of one block: x, residual and y
     [tokens x hidden] bf16, w_gate_up [2 ffn x hidden] (the gate's rows, then the
@@ -78,7 +89,8 @@ class Fp8FeedForward:
 
     def forward(self, x, residual, weight, y, train=True, stream=None):
         """y = down(act(gate(n)) * up(n)) + s, with the weights' codes as they are.
-        residual may be None (s = x).
+        residual may be None (s = x); backward then reads x itself, which must stay as it is
+        until then: y may not share its memory, and a change that torch counts is an error there.
 
         train: keep what backward needs, and the amaxes that update() takes.  Without it the
         call changes nothing that a backward or an update() sees, so it may come between a
@@ -87,6 +99,8 @@ class Fp8FeedForward:
         T, H, F = self.shape
         self._check(x, (T, H), "x")
         self._check(y, (T, H), "y")
+        if train and residual is None and _overlap(x, y):
+            raise ValueError("y shares memory with x, which backward needs (residual=None)")
         n, h, ws = self.state_n, self.state_h, self.workspace
         total, qn, qh = (self.sum, self.qn, self.qh) if train else (self.sum_infer, self.qn_infer, self.qh_infer)
         _b.fp8_rmsnorm_quantize(x, weight, self.eps, n.fmt, n.scale, qn, residual=residual,
@@ -94,7 +108,7 @@ class Fp8FeedForward:
                                 amax=n.amax if train else None, workspace=ws, stream=stream)
         s = x if residual is None else total
         if train:
-            self._s = s
+            self._s, self._s_version = s, _version(s)
         _b.fp8_gemm_gated(qn, n.fmt, self.qw_gu, self.state_gu.fmt, n.scale_inv, self.state_gu.scale_inv_used,
                           self.act, qh, gu=self.gu if train else None, out_fmt=h.fmt, out_scale=h.scale,
                           amax=h.amax if train else None, accum=self.accum, workspace=ws, stream=stream)
@@ -110,6 +124,8 @@ class Fp8FeedForward:
         self._check(dy, (T, H), "dy")
         self._check(dw_gate_up, (2 * F, H), "dw_gate_up")
         self._check(dw_down, (H, F), "dw_down")
+        if _version(self._s) != self._s_version:
+            raise RuntimeError("x was changed after the forward (residual=None), and backward needs it as it was")
         sy, sg, ws = self.state_dy, self.state_dgu, self.workspace
         kw = dict(accum=self.accum, b_trans=True, stream=stream)
         _b.fp8_act_backward(dy, None, "none", sy.fmt, sy.scale, q=self.qdy, q_t=self.qdy_t, amax=sy.amax, workspace=ws,

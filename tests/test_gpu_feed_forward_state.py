@@ -87,3 +87,36 @@ def test_inference_leaves_a_training_step_as_it_is(with_residual, accum):
         out.append(dict(o, y=y, **{k: getattr(ffn, k).history.clone() for k in ("state_n", "state_h", "state_dy", "state_dgu")}))
     for k in out[0]:
         assert torch.equal(out[0][k], out[1][k]), k
+
+
+def test_without_a_residual_x_is_kept_or_the_call_refused():
+    """With residual=None backward reads the caller's x: an output over it is refused where backward will follow, a
+    change in between is an error, and untouched the step is that of a residual of zeros."""
+    d = inputs()
+    zeros = dict(d, residual=torch.zeros_like(d["x"]))
+    out = []
+    for e in (zeros, dict(d, residual=None)):
+        ffn = block()
+        ffn.quantize_weights(e["w_gu"], e["w_d"])
+        out.append(dict(y=forward(ffn, e), **backward(ffn, e)))
+    for k in out[0]:
+        assert torch.equal(out[0][k], out[1][k]), k
+    d["residual"] = None
+    x, y = d["x"].clone(), out[1]["y"]
+    store = torch.empty(2 * T * H, dtype=torch.bfloat16, device=device())
+    part, over = store[:T * H].view(T, H), store[T * H // 2:3 * T * H // 2].view(T, H)   # they share half their memory
+    part.copy_(x)
+    for given, into in ((d["x"], d["x"]), (part, over)):
+        with pytest.raises(ValueError, match="memory"):
+            forward(ffn, dict(d, x=given), y=into)
+        assert torch.equal(given, x)                                                       # refused before anything ran
+    assert torch.equal(forward(ffn, d, train=False, y=d["x"]), y) and torch.equal(d["x"], y)   # inference: in place
+    d["x"] = x
+    forward(ffn, d)
+    x.mul_(2)
+    with pytest.raises(RuntimeError, match="changed"):
+        backward(ffn, d)
+    with torch.inference_mode():                       # tensors without a count of their changes
+        e = dict(d, x=x.clone())
+        forward(ffn, e)
+        backward(ffn, e)
