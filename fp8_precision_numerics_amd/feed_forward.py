@@ -72,6 +72,7 @@ class Fp8FeedForward:
         self.dh, self.dn = torch.empty((T, F), **bf), torch.empty((T, H), **bf)
         self.qdgu, self.qdgu_t = torch.empty((T, 2 * F), **u8), torch.empty((2 * F, T), **u8)
         self.workspace = torch.empty(WORKSPACE_BYTES, **u8)
+        self._kept = False  # the buffers and scales are those of one training forward
 
     def _check(self, t, shape, name):
         if tuple(t.shape) != shape:
@@ -84,6 +85,7 @@ class Fp8FeedForward:
         T, H, F = self.shape
         self._check(w_gate_up, (2 * F, H), "w_gate_up")
         self._check(w_down, (H, F), "w_down")
+        self._kept = False
         self.state_gu.quantize_update(w_gate_up, q=self.qw_gu, stream=stream)
         self.state_d.quantize_update(w_down, q=self.qw_d, stream=stream)
 
@@ -101,6 +103,8 @@ class Fp8FeedForward:
         self._check(y, (T, H), "y")
         if train and residual is None and _overlap(x, y):
             raise ValueError("y shares memory with x, which backward needs (residual=None)")
+        if train:
+            self._kept = False
         n, h, ws = self.state_n, self.state_h, self.workspace
         total, qn, qh = (self.sum, self.qn, self.qh) if train else (self.sum_infer, self.qn_infer, self.qh_infer)
         _b.fp8_rmsnorm_quantize(x, weight, self.eps, n.fmt, n.scale, qn, residual=residual,
@@ -114,9 +118,12 @@ class Fp8FeedForward:
                           amax=h.amax if train else None, accum=self.accum, workspace=ws, stream=stream)
         _b.fp8_gemm_fused(qh, h.fmt, self.qw_d, self.state_d.fmt, h.scale_inv, self.state_d.scale_inv_used, y,
                           residual=s, accum=self.accum, workspace=ws, stream=stream)
+        if train:
+            self._kept = True
 
     def backward(self, dy, weight, dx, dweight, dw_gate_up, dw_down, stream=None):
-        """Gradients of the last forward(train=True): dx [tokens x hidden] bf16 (of x, hence of
+        """Gradients of the last forward(train=True), as often as wanted until the weights are cast
+        again or update() sets new scales: dx [tokens x hidden] bf16 (of x, hence of
         the residual too), dweight fp32 [hidden], dw_gate_up and dw_down (fp32 or bf16)."""
         T, H, F = self.shape
         if T % 16:
@@ -124,6 +131,8 @@ class Fp8FeedForward:
         self._check(dy, (T, H), "dy")
         self._check(dw_gate_up, (2 * F, H), "dw_gate_up")
         self._check(dw_down, (H, F), "dw_down")
+        if not self._kept:
+            raise RuntimeError("backward needs a training forward, with no quantize_weights or update since")
         if _version(self._s) != self._s_version:
             raise RuntimeError("x was changed after the forward (residual=None), and backward needs it as it was")
         sy, sg, ws = self.state_dy, self.state_dgu, self.workspace
@@ -144,5 +153,6 @@ class Fp8FeedForward:
     def update(self, stream=None):
         """Push the activations' and gradients' amaxes into their histories and set the next step's
         scales.  The weights' are stepped where they are cast, so their codes outlive any number of updates."""
+        self._kept = False
         for st in (self.state_n, self.state_h, self.state_dy, self.state_dgu):
             st.update(stream=stream)

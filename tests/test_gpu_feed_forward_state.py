@@ -120,3 +120,30 @@ def test_without_a_residual_x_is_kept_or_the_call_refused():
         e = dict(d, x=x.clone())
         forward(ffn, e)
         backward(ffn, e)
+
+
+def test_calls_out_of_order_are_errors():
+    """A backward needs a training forward whose codes still have their scales and weights."""
+    ffn, d = block(), inputs()
+    ffn.quantize_weights(d["w_gu"], d["w_d"])
+    with pytest.raises(RuntimeError, match="training forward"):
+        backward(ffn, d)
+    forward(ffn, d, train=False)
+    with pytest.raises(RuntimeError, match="training forward"):
+        backward(ffn, d)
+    for between in (ffn.update, lambda: ffn.quantize_weights(d["w_gu"], d["w_d"])):
+        forward(ffn, d)
+        first, again = backward(ffn, d), backward(ffn, d)          # any number of gradients of one forward
+        for k in first:
+            assert torch.equal(first[k], again[k]), k
+        between()
+        with pytest.raises(RuntimeError, match="training forward"):
+            backward(ffn, d)
+    forward(ffn, d)
+    with pytest.raises(ValueError, match="y must be"):
+        forward(ffn, d, y=torch.empty(T, 2 * H, dtype=torch.bfloat16))
+    backward(ffn, d)                                               # refused before anything was written: still whole
+    with pytest.raises(Exception):                                 # refused by the norm, halfway
+        forward(ffn, dict(d, weight=d["weight"][:5]))
+    with pytest.raises(RuntimeError, match="training forward"):
+        backward(ffn, d)
