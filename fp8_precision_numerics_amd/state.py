@@ -73,7 +73,7 @@ class DelayedScalingState:
     def snapshot(self) -> dict:
         """Host copies of every buffer (synchronises)."""
         return {k: getattr(self, k).detach().cpu().clone()
-                for k in ("history", "head", "scale", "scale_inv", "status", "amax", "sat")}
+                for k in ("history", "head", "scale", "scale_inv", "status", "amax", "sat", "scale_inv_used")}
 
     def restore(self, snap: dict) -> None:
         for k, v in snap.items():

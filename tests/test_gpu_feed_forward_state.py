@@ -147,3 +147,20 @@ def test_calls_out_of_order_are_errors():
         forward(ffn, dict(d, weight=d["weight"][:5]))
     with pytest.raises(RuntimeError, match="training forward"):
         backward(ffn, d)
+
+
+def test_a_block_restored_from_codes_and_snapshots_goes_on_as_it_was():
+    """A weight state's snapshot carries the inverse scale that the codes were cast with, so codes and snapshots put
+    into another block give the same bits, without another cast."""
+    ffn, d = block(), inputs()
+    for _ in range(2):
+        ffn.quantize_weights(d["w_gu"], d["w_d"])
+        forward(ffn, d)
+        ffn.update()
+    ffn.quantize_weights((d["w_gu"].float() * 3).bfloat16(), d["w_d"])      # the scale it sets differs from the one it used
+    y, other = forward(ffn, d, train=False), block()
+    for name in ("state_n", "state_gu", "state_h", "state_d"):
+        getattr(other, name).restore(getattr(ffn, name).snapshot())
+    other.qw_gu.copy_(ffn.qw_gu)
+    other.qw_d.copy_(ffn.qw_d)
+    assert torch.equal(forward(other, d, train=False), y)
