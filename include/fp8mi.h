@@ -436,8 +436,9 @@ typedef enum { FP8MI_OUT_F32 = 0, FP8MI_OUT_BF16 = 1, FP8MI_OUT_E4M3 = 2, FP8MI_
  * q            device, [rows x cols] uint8.
  * rstd         device, [rows] fp32, receives r (what the gradient needs); or NULL.
  * amax, sat    device, 1 fp32 / 1 uint64, overwritten, or NULL.
- * workspace    device scratch or NULL: with it the statistics are gathered in up
- *              to workspace_bytes / 16 slots, without it with atomics.
+ * workspace    device scratch or NULL: where it has 16 bytes for every workgroup
+ *              (32 KiB always do on 256 compute units) the statistics are gathered
+ *              there, otherwise with atomics.
  * cols must be a multiple of 16; x, residual, weight, sum_out and q 16-B aligned;
  * eps >= 0.  rows * cols may be 0 (then amax = 0 and sat = 0).
  */
