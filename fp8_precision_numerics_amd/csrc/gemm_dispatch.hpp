@@ -5,6 +5,7 @@
 
 #include "gemm_kernel.hpp"
 #include "gemm_shape.hpp"
+#include "launch.hpp"
 
 namespace fp8mi {
 
@@ -43,7 +44,7 @@ inline hipError_t gemm_dispatch_shape(const uint8_t* A, const uint8_t* B, int64_
                                       hipStream_t st, const MxScales& mxs = MxScales{nullptr, nullptr}) {
   constexpr bool MXS = MODE == kAccumMx || MODE == kAccumMxExact;
   int shape = M >= 1024 && N >= 1024 ? 0 : 1;
-  if constexpr (!MXS) shape = choose_tile(M, N, K, MODE, 0).shape;
+  if constexpr (!MXS) shape = choose_tile(M, N, K, MODE == kAccumMfma8, 0, persistent_groups(1)).shape;
   if (shape == 0) {
     if constexpr (MODE == kAccumExact || MODE == kAccumMxExact)
       return gemm_run<256, 256, 2, 4, FA, FB, OUT, MODE, BT>(A, B, M, N, K, sa, sb, C, rq, st, mxs);

@@ -5,6 +5,7 @@
 
 #include "gemm_kernel.hpp"
 #include "gemm_shape.hpp"
+#include "launch.hpp"
 
 namespace fp8mi {
 
@@ -95,7 +96,7 @@ template <int FA, int FB, int MODE, class EPI>
 inline hipError_t epi_shape(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, int64_t K, const float* sa,
                             const float* sb, const EPI& epi, size_t workspace_bytes, hipStream_t st) {
   constexpr int64_t W = std::is_same<EPI, GatedEpi>::value ? 2 : 1;  // B rows per output column
-  const TileChoice c = choose_tile(M, W * N, K, MODE, workspace_bytes);
+  const TileChoice c = choose_tile(M, W * N, K, MODE == kAccumMfma8, workspace_bytes, persistent_groups(1));
   if (c.shape == 0) {
     // 8 wavefronts either way, arranged as the plain GEMM's of that mode
     if constexpr (MODE == kAccumExact) return epi_run<256, 256, 2, 4, FA, FB, MODE, EPI>(A, B, M, N, K, sa, sb, epi, c.split, st);

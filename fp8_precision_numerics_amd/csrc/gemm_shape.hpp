@@ -1,10 +1,13 @@
-// Tile shape and split of K of the dense GEMMs, by an estimate of their time.
+// Tile shape and split of K of the dense GEMMs, by an estimate of their time.  Plain
+// host C++, so that a test can ask for the choice without a device.
 #pragma once
 
-#include "gemm_tile.hpp"
-#include "launch.hpp"
+#include <cstddef>
+#include <cstdint>
 
 namespace fp8mi {
+
+constexpr int kShapeStep = 128;  // K bytes of a main-loop step
 
 // The larger tiles need fewer operand bytes a product; the smaller ones fill the chip
 // with fewer rows and columns, and a split of K fills it where even those are few (only
@@ -34,7 +37,9 @@ struct TileChoice {
   int split;
 };
 
-inline TileChoice choose_tile(int64_t M, int64_t brows, int64_t K, int mode, size_t workspace_bytes) {
+// `brows`: rows of B; `cus`: compute units of the device.
+inline TileChoice choose_tile(int64_t M, int64_t brows, int64_t K, bool fp8_cores, size_t workspace_bytes,
+                              int64_t cus) {
   struct Cost {
     int bm, bn;
     double start, alone, each, odd;
@@ -47,8 +52,8 @@ inline TileChoice choose_tile(int64_t M, int64_t brows, int64_t K, int mode, siz
                                    {128, 128, 6.3, 0.77, 0.50, 1.23},
                                    {64, 128, 5.7, 0.60, 0.34, 1.32},
                                    {64, 128, 5.9, 0.39, 0.35, 1.27}};
-  const Cost* costs = mode == kAccumMfma8 ? kFp8 : kExact;
-  const int64_t cus = persistent_groups(1), steps = (K + kBK - 1) / kBK;
+  const Cost* costs = fp8_cores ? kFp8 : kExact;
+  const int64_t steps = (K + kShapeStep - 1) / kShapeStep;
   TileChoice best{2, 1};
   double least = 1e300;
   for (int i = 0; i < 4; ++i) {
@@ -58,7 +63,7 @@ inline TileChoice choose_tile(int64_t M, int64_t brows, int64_t K, int mode, siz
       const double traffic = (double)split * M * brows * 4.0;
       if (split > 1 && (traffic > (double)workspace_bytes || tiles * split > 4 * cus)) break;
       const int64_t load = (tiles * split + cus - 1) / cus;
-      const double busy = load * c.each * (K % kBK ? c.odd : 1.0);
+      const double busy = load * c.each * (K % kShapeStep ? c.odd : 1.0);
       const double step = c.alone > busy ? c.alone : busy;
       const double t = c.start + (double)((steps + split - 1) / split) * step +
                        (split > 1 ? 2.0 + 2.0 * traffic / 5.2e6 : 0.0);
