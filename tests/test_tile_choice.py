@@ -59,3 +59,24 @@ def test_every_shape_is_tested_in_every_layout():
 def test_the_step_is_the_kernels(lib):
     with open(os.path.join(CSRC, "gemm_tile.hpp")) as f:
         assert f"constexpr int kBK = {lib.step()};" in f.read()
+
+
+@pytest.mark.parametrize("case", tile_cases.EPILOGUE)
+@pytest.mark.parametrize("fp8_cores", [0, 1])
+def test_products_with_an_epilogue_select_their_tiles(lib, case, fp8_cores):
+    assert choice(lib, *case, fp8_cores, tile_cases.WORKSPACE) == tile_cases.EPILOGUE[case][fp8_cores]
+
+
+def test_every_shape_is_tested_whole_and_split():
+    for fp8_cores in (0, 1):
+        seen = {(shape, split > 1) for shape, split in (v[fp8_cores] for v in tile_cases.EPILOGUE.values())}
+        assert {(0, False), (0, True), (1, False), (1, True), (2, True), (3, True)} <= seen
+
+
+@pytest.mark.parametrize("fp8_cores", [0, 1])
+def test_a_split_fits_its_workspace_and_leaves_no_part_empty(lib, fp8_cores):
+    for m, brows, k in list(tile_cases.EPILOGUE) + [(17, 16, 16), (64, 4096, 16384), (24, 4096, 16384), (500, 4096, 16384)]:
+        for workspace in (0, 15, m * brows * 4, 2 * m * brows * 4 - 1, 2 * m * brows * 4, 5 * m * brows * 4, 1 << 30):
+            shape, split = choice(lib, m, brows, k, fp8_cores, workspace)
+            assert 0 <= shape <= 3 and 1 <= split <= max(1, -(-k // 128))
+            assert split == 1 or split * m * brows * 4 <= workspace
