@@ -24,14 +24,15 @@ constexpr int kShapeStep = 128;  // K bytes of a main-loop step
 // of a row and step lie in two cache lines (8192 x 4096 on the FP8 cores: 108 us at
 // K = 4096, 133 at 4112).  The constants are a least-squares fit to 100 products of
 // random and of round sizes; over them the choice is 4 % slower than the best shape
-// and split of each, 30 % at worst.  At M x N x K the choices measured (exact mode, us; 256,
-// 128, 64 and 64t stand for the shapes, t for three stages, /s for the split):
-//   8192 x 4096 x 16384   256: 715   128: 784   64: 876
-//   1003 x 16384 x 4096   256: 102   128: 115   64: 126   64t: 140
-//   2048 x 4096 x 4096    256: 77    128: 57    64: 66    64t: 70
-//   500 x 4096 x 16384    256/6: 73  128/4: 66  64/2: 70  64t/2: 72   64: 95
-//   64 x 4096 x 16384     64: 96     64/8: 24   64t: 69   64t/6: 23
-//   24 x 4096 x 16384     64/12: 22  64t/8: 20
+// and split of each, 30 % at worst.  Measured for some M x N x K (exact mode, cold weights, us; 256, 128, 64
+// and 64t stand for the shapes, t for three stages, /s for the best split tried, * for the choice
+// with a workspace of 64 MiB):
+//   8192 x 4096 x 16384   256*: 718   128: 777    64: 876     64t: 963
+//   1003 x 16384 x 4096   256*: 99    128: 109    64: 122     64t: 138
+//   2048 x 4096 x 4096    256/2: 75   128*: 56    64: 66      64t: 70
+//   500 x 4096 x 16384    256/6: 73   128/4*: 65  64/3: 68    64t/2: 70
+//   64 x 4096 x 16384                             64/13: 24   64t/6*: 23
+//   24 x 4096 x 16384                             64/13*: 21  64t/6: 21
 struct TileChoice {
   int shape;  // 0: 256 x 256, 1: 128 x 128, 2: 64 x 128, 3: 64 x 128 in three stages
   int split;

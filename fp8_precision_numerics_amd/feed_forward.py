@@ -137,6 +137,8 @@ class Fp8FeedForward:
             raise RuntimeError("x was changed after the forward (residual=None), and backward needs it as it was")
         sy, sg, ws = self.state_dy, self.state_dgu, self.workspace
         kw = dict(accum=self.accum, b_trans=True, stream=stream)
+        # The cast of fp8_quantize with the same bits: 512 x 4096 7.7 us a call against 15.5, 8192 x 4096 31 against 28,
+        # 8192 x 16384 93 against 111.
         _b.fp8_act_backward(dy, None, "none", sy.fmt, sy.scale, q=self.qdy, q_t=self.qdy_t, amax=sy.amax, workspace=ws,
                             stream=stream)
         _b.fp8_gemm(self.qdy, sy.fmt, self.qw_d, self.state_d.fmt, sy.scale_inv, self.state_d.scale_inv_used, self.dh,
