@@ -51,22 +51,30 @@ PEAK_BY_ACCUM = {"exact": PEAK_BF16_TFLOPS, "mfma_fp8": PEAK_FP8_TFLOPS}
 
 # HBM traffic per launch of the FC1 GEMM from two counter runs (FETCH_SIZE, WRITE_SIZE), each scaled by what
 # the same counter reads for a 256 MiB device copy (profiles/gemm_fc1_8192x16384x4096_hbm_traffic.md).  Valid
-# only for the kernel sources they were taken on: GEMM_SOURCES hashed in order must give GEMM_TRAFFIC_SHA256.
-GEMM_SOURCES = ("gemm.hip", "gemm_dispatch.hpp", "gemm_kernel.hpp", "gemm_tile.hpp", "device_common.hpp")
-GEMM_TRAFFIC_SHA256 = "2a8df5447029215bb2bf6d580f5b78871c0b499c58e48f090d1eb685663bfed5"
-GEMM_TRAFFIC = {"exact": {"read_bytes": 805546341, "write_bytes": 268523191},
-                "mfma_fp8": {"read_bytes": 805601577, "write_bytes": 268710760}}
+# only for the code they were taken on: gemm_sources_sha256() must give GEMM_TRAFFIC_SHA256.
+GEMM_SOURCES = ("gemm.hip", "gemm_dispatch.hpp", "gemm_kernel.hpp", "gemm_shape.hpp", "gemm_tile.hpp", "epilogue.hpp",
+                "activation.hpp", "stats.hpp", "launch.hpp", "device_common.hpp")
+GEMM_TRAFFIC_SHA256 = "509228d07443d0897f382fefef26856958f5fc11cbb27231c26663dd0b774313"
+GEMM_TRAFFIC = {"exact": {"read_bytes": 805583767, "write_bytes": 268531917},
+                "mfma_fp8": {"read_bytes": 805659536, "write_bytes": 268702925}}
 
 
-def gemm_traffic(accum):
-    """Counter-measured HBM bytes per launch, or None once the GEMM sources differ from the measured ones."""
+def gemm_sources_sha256(folder=os.path.join(ROOT, "fp8_precision_numerics_amd", "csrc")):
+    """Hash of the GEMM's sources in order, without comments and white space at the ends of lines."""
     import hashlib
+    import re
 
     h = hashlib.sha256()
     for name in GEMM_SOURCES:
-        with open(os.path.join(ROOT, "fp8_precision_numerics_amd", "csrc", name), "rb") as f:
-            h.update(f.read())
-    if h.hexdigest() != GEMM_TRAFFIC_SHA256:
+        with open(os.path.join(folder, name)) as f:
+            code = [re.sub(r"//.*", "", line).rstrip() for line in f]
+        h.update("\n".join(line for line in code if line).encode() + b"\n")
+    return h.hexdigest()
+
+
+def gemm_traffic(accum):
+    """Counter-measured HBM bytes per launch, or None once the GEMM's code differs from the measured one."""
+    if gemm_sources_sha256() != GEMM_TRAFFIC_SHA256:
         return None
     t = GEMM_TRAFFIC[accum]
     return t["read_bytes"] + t["write_bytes"]
