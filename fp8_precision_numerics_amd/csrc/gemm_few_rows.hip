@@ -13,8 +13,8 @@
 // of B are often a power of two apart, and with every wave of the chip at the same
 // K their reads fell on few of the memory's channels.  Measured on MI355X, cold
 // weights: gated 2 x 16384 x 4096, 8 rows, 24.0 us (5.6 TB/s) against 28.5 us
-// without the turn; 4096 x 16384 16.1 against 19.3 us; a plain read of the same
-// bytes takes 21.5 and 11.4 us.  Waves: a split that gives the chip about 2048
+// without the turn; 4096 x 16384 16.1 against 19.3 us (14.9 us in a run of its own); a plain
+// read of the same bytes takes 21.5 and 11.4 us.  Waves: a split that gives the chip about 2048
 // waves (8 a compute unit) is best; with 1 wave a tile 41.3 us, with 8 33.3 us,
 // with 2 28.2 us (gated shape, before the turn).
 //
