@@ -19,6 +19,8 @@ needs a multiple of 16, the K granule of its weight-gradient GEMMs.
 
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import _binding as _b
@@ -29,21 +31,24 @@ from .state import DelayedScalingState, Recipe
 WORKSPACE_BYTES = 64 << 20
 
 
-def _overlap(a, b):
-    """Whether two contiguous tensors share memory."""
-    return (a.data_ptr() < b.data_ptr() + b.numel() * b.element_size()
-            and b.data_ptr() < a.data_ptr() + a.numel() * a.element_size())
+def _straddle(a, b):
+    """Whether two contiguous tensors share memory without beginning at the same address."""
+    p, q = a.data_ptr(), b.data_ptr()
+    return p != q and p < q + b.numel() * b.element_size() and q < p + a.numel() * a.element_size()
 
 
-def _version(t):
-    """torch's count of the in-place changes of a tensor (inference tensors have none)."""
-    return None if t.is_inference() else t._version
+def _on(stream):
+    """Context in which torch works on what a `stream` argument names."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
 
 
 class Fp8FeedForward:
     """Buffers and delayed-scaling states of one block: x, residual and y
     [tokens x hidden] bf16, w_gate_up [2 ffn x hidden] (the gate's rows, then the
-    up projection's) and w_down [hidden x ffn] bf16, weight [hidden] bf16."""
+    up projection's) and w_down [hidden x ffn] bf16, weight [hidden] bf16.  The calls share one
+    workspace and the scales: on several streams, the caller puts them in order."""
 
     def __init__(self, tokens: int, hidden: int, ffn: int, act: str = "silu", eps: float = 1e-5,
                  recipe: Recipe = Recipe(), accum: str = "exact", device="cuda"):
@@ -91,8 +96,7 @@ class Fp8FeedForward:
 
     def forward(self, x, residual, weight, y, train=True, stream=None):
         """y = down(act(gate(n)) * up(n)) + s, with the weights' codes as they are.
-        residual may be None (s = x); backward then reads x itself, which must stay as it is
-        until then: y may not share its memory, and a change that torch counts is an error there.
+        residual may be None (s = x; a training forward keeps a copy).  y may be x or the residual.
 
         train: keep what backward needs, and the amaxes that update() takes.  Without it the
         call changes nothing that a backward or an update() sees, so it may come between a
@@ -101,8 +105,8 @@ class Fp8FeedForward:
         T, H, F = self.shape
         self._check(x, (T, H), "x")
         self._check(y, (T, H), "y")
-        if train and residual is None and _overlap(x, y):
-            raise ValueError("y shares memory with x, which backward needs (residual=None)")
+        if residual is None and _straddle(x, y):
+            raise ValueError("y shares part of its memory with x, which is the residual (residual=None)")
         if train:
             self._kept = False
         n, h, ws = self.state_n, self.state_h, self.workspace
@@ -110,9 +114,10 @@ class Fp8FeedForward:
         _b.fp8_rmsnorm_quantize(x, weight, self.eps, n.fmt, n.scale, qn, residual=residual,
                                 sum_out=None if residual is None else total, rstd=self.rstd if train else None,
                                 amax=n.amax if train else None, workspace=ws, stream=stream)
+        if train and residual is None:
+            with _on(stream):
+                total.copy_(x)
         s = x if residual is None else total
-        if train:
-            self._s, self._s_version = s, _version(s)
         _b.fp8_gemm_gated(qn, n.fmt, self.qw_gu, self.state_gu.fmt, n.scale_inv, self.state_gu.scale_inv_used,
                           self.act, qh, gu=self.gu if train else None, out_fmt=h.fmt, out_scale=h.scale,
                           amax=h.amax if train else None, accum=self.accum, workspace=ws, stream=stream)
@@ -133,8 +138,6 @@ class Fp8FeedForward:
         self._check(dw_down, (H, F), "dw_down")
         if not self._kept:
             raise RuntimeError("backward needs a training forward, with no quantize_weights or update since")
-        if _version(self._s) != self._s_version:
-            raise RuntimeError("x was changed after the forward (residual=None), and backward needs it as it was")
         sy, sg, ws = self.state_dy, self.state_dgu, self.workspace
         kw = dict(accum=self.accum, b_trans=True, stream=stream)
         # The cast of fp8_quantize with the same bits: 512 x 4096 7.7 us a call against 15.5, 8192 x 4096 31 against 28,
@@ -149,7 +152,7 @@ class Fp8FeedForward:
         _b.fp8_gemm(self.qdgu, sg.fmt, self.qw_gu, self.state_gu.fmt, sg.scale_inv, self.state_gu.scale_inv_used,
                     self.dn, **kw)
         _b.fp8_gemm(self.qdgu_t, sg.fmt, self.qn, self.state_n.fmt, sg.scale_inv, self.state_n.scale_inv, dw_gate_up, **kw)
-        _b.fp8_rmsnorm_backward(self.dn, self._s, self.rstd, weight, dx, dweight=dweight, dresidual=dy, workspace=ws,
+        _b.fp8_rmsnorm_backward(self.dn, self.sum, self.rstd, weight, dx, dweight=dweight, dresidual=dy, workspace=ws,
                                 stream=stream)
 
     def update(self, stream=None):
