@@ -216,6 +216,7 @@ def test_norm_special_rows(cols, blocks):
 # gated and fused products
 # ---------------------------------------------------------------------------
 # few-row kernel (<= 16), the three tile shapes, K split over the workspace (256 x 64 x 8192 and the like), ragged everything
+# (beyond 16 rows these select 64 x 128 tiles, in two or three stages; test_gpu_tile_epilogues.py has the larger tiles, whole and split)
 GEMM_SHAPES = [(1, 16, 16), (1, 48, 4096), (3, 40, 144), (16, 136, 1040), (16, 2064, 528), (17, 33, 272), (64, 64, 8192), (65, 200, 400),
                (130, 72, 4112), (200, 131, 144), (300, 300, 1040), (1100, 700, 272)]
 

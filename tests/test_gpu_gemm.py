@@ -57,6 +57,8 @@ def check_within_bound(c_gpu, qa, fa, qb, fb, sa, sb, out, bound=None):
 # The last three take the 256x256-tile path (M, N >= 1024) with edge tiles in
 # both M and N; (1100, 1030, 400) and (1024, 1040, 144) also end on a ragged K
 # step (K % 128 != 0), which that path stages through registers.
+# (As the tile shape was chosen when these sizes were picked. By the estimate that chooses it now they all take 64 x 128
+# tiles; tile_cases.py has the sizes that select each shape.)
 SHAPES = [(64, 64, 128), (1, 1, 16), (300, 260, 272), (257, 513, 144), (128, 2048, 256), (1100, 1030, 384),
           (1100, 1030, 400), (1024, 1040, 144)]
 
@@ -145,6 +147,8 @@ def test_permutation_selects_columns_exactly(fa, fb, accum):
 
 # B handed over as [K x N] (N a multiple of 16): small tiles, the 256x256 path
 # with edge tiles, ragged last K steps (400, 144, 272) and a long K.
+# (As the tile shape was chosen when these sizes were picked. By the estimate that chooses it now they all take 64 x 128
+# tiles; tile_cases.py has the sizes that select each shape.)
 BT_SHAPES = [(64, 64, 128), (16, 16, 16), (300, 272, 272), (257, 528, 144), (128, 2048, 256),
              (1100, 1040, 400), (1024, 1040, 144), (1030, 1024, 4096)]
 

@@ -31,6 +31,8 @@ def _rows_of_codes(values, K, dev):
     return t
 
 
+# (The tile shapes named here are those that were chosen when the sizes were picked. Now both take 64 x 128 tiles;
+# test_gpu_tile_shapes.py has the larger ones at this K.)
 @pytest.mark.parametrize("accum", ["exact", "mfma_fp8"])
 @pytest.mark.parametrize("M,N", [(64, 48), (1024, 1040)])      # 128x128 tiles; 256x256 tiles with a ragged N
 def test_dense_gemm_at_the_largest_k(M, N, accum):

@@ -46,6 +46,8 @@ def _run_both(qa, fa, qbT, fb, sa, sb, out_fmt, s_out, accum):
 
 # (1100, 1030, 400) and (1024, 1040, 144): the 256x256-tile path with edge
 # tiles and a ragged last K step.
+# (As the tile shape was chosen when these sizes were picked. By the estimate that chooses it now they all take 64 x 128
+# tiles; tile_cases.py has the sizes that select each shape.)
 SHAPES = [(64, 64, 128), (1, 1, 16), (300, 260, 272), (257, 513, 144), (1100, 1030, 384), (1024, 1040, 256),
           (1100, 1030, 400), (1024, 1040, 144)]
 
