@@ -21,6 +21,7 @@ __all__ = ["E4M3", "E5M2", "F32", "BF16", "ACCUM_EXACT", "ACCUM_MFMA_FP8", "QUAN
            "fp8_quantize_mx", "fp8_gemm_mx", "mx_scale_ld", "mx_scale_pos", "fp8_quantize_update",
            "fp8_quantize_update_noalloc", "fp8_rmsnorm_quantize", "fp8_rmsnorm_quantize_blockwise",
            "fp8_rmsnorm_backward", "fp8_gemm_gated", "fp8_gemm_fused", "fp8_act_backward", "fp8_gated_backward",
+           "fp8_layernorm_quantize", "fp8_layernorm_backward",
            "EXPORTED_SYMBOLS"]
 
 E4M3, E5M2 = 0, 1
@@ -36,7 +37,7 @@ EXPORTED_SYMBOLS = ("fp8mi_status_string", "fp8mi_version", "fp8_quantize", "fp8
                     "fp8_shared_scale", "fp8_dequant_sum", "fp8_quantize_mx", "fp8_gemm_mx",
                     "fp8_quantize_update", "fp8_quantize_update_noalloc", "fp8_rmsnorm_quantize",
                     "fp8_rmsnorm_quantize_blockwise", "fp8_rmsnorm_backward", "fp8_gemm_gated", "fp8_gemm_fused",
-                    "fp8_act_backward", "fp8_gated_backward")
+                    "fp8_act_backward", "fp8_gated_backward", "fp8_layernorm_quantize", "fp8_layernorm_backward")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
@@ -112,8 +113,12 @@ def load_library():
                                    sz, vp]
     lib.fp8_act_backward.argtypes = [vp, ci, vp, ci, i64, i64, ci, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.fp8_gated_backward.argtypes = [vp, ci, vp, ci, i64, i64, ci, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.fp8_layernorm_quantize.argtypes = [vp, vp, vp, vp, ci, i64, i64, cf, cf, vp, ci, vp, vp, vp, vp, vp, vp, vp, vp,
+                                           sz, vp]
+    lib.fp8_layernorm_backward.argtypes = [vp, vp, vp, vp, vp, vp, ci, i64, i64, cf, vp, vp, vp, vp, vp, vp, sz, vp]
     for name in ("fp8_rmsnorm_quantize", "fp8_rmsnorm_quantize_blockwise", "fp8_rmsnorm_backward", "fp8_gemm_gated",
-                 "fp8_gemm_fused", "fp8_act_backward", "fp8_gated_backward"):
+                 "fp8_gemm_fused", "fp8_act_backward", "fp8_gated_backward", "fp8_layernorm_quantize",
+                 "fp8_layernorm_backward"):
         getattr(lib, name).restype = ci
     _LIB = lib
     return lib
@@ -192,9 +197,10 @@ def _call(name, status):
 
 
 # The calls whose smallest sizes run for a few microseconds (fp8_gemm and the
-# feed-forward operators) are marshalled by the extension module of csrc/marshal.cpp.
+# feed-forward operators, those at the ends of a model) are marshalled by the extension module of csrc/marshal.cpp.
 _MARSHALLED = ("fp8_gemm", "fp8_gemm_gated", "fp8_gemm_fused", "fp8_rmsnorm_quantize", "fp8_rmsnorm_quantize_blockwise",
-               "fp8_rmsnorm_backward", "fp8_act_backward", "fp8_gated_backward")
+               "fp8_rmsnorm_backward", "fp8_act_backward", "fp8_gated_backward", "fp8_layernorm_quantize",
+               "fp8_layernorm_backward")
 _MODULE = None
 # The current stream's handle and device without building the Python objects
 # around them (about 2 us of a small call).
@@ -575,3 +581,37 @@ def fp8_gated_backward(dh, gu, act, fmt, scale, q=None, q_t=None, amax=None, sat
         workspace)
     if status:
         _settle(status, fp8_gated_backward, dh, gu, act, fmt, scale, q, q_t, amax, sat, workspace, stream)
+
+
+# ---------------------------------------------------------------------------
+# operators at both ends of a model
+# ---------------------------------------------------------------------------
+def fp8_layernorm_quantize(x, weight, bias, eps, fmt, scale, q, residual=None, sum_out=None, mean=None, rstd=None,
+                           amax=None, sat=None, dropout=0.0, rng=None, workspace=None, stream=None) -> None:
+    """q = FP8 codes of fp32((norm(h) * weight + bias) * scale), h = drop(x) + residual rounded to x's type, the norm
+    with the row's mean taken out.
+
+    x, residual, sum_out: [rows x cols] fp32 or bf16 (sum_out receives h; it may be x or residual);
+    weight, bias: [cols] of the same type (bias may be None); scale: fp32[1]; q: uint8 [rows x cols];
+    mean, rstd: fp32 [rows]; amax / sat: fp32[1] / int64[1], overwritten; dropout: probability in [0, 1), in steps of
+    2^-16; rng: int64[2] on the GPU, {seed, offset} (include/fp8mi.h names the generator); workspace: optional uint8
+    scratch for the statistics.  cols must be a multiple of 16."""
+    index, handle = _where(stream)
+    status = (_MODULE or _load_module()).layer(index, handle, x, weight, bias, eps, fmt, scale, q, residual, sum_out,
+        mean, rstd, amax, sat, dropout, rng, workspace)
+    if status:
+        _settle(status, fp8_layernorm_quantize, x, weight, bias, eps, fmt, scale, q, residual, sum_out, mean, rstd,
+                amax, sat, dropout, rng, workspace, stream)
+
+
+def fp8_layernorm_backward(dy, h, mean, rstd, weight, dx, dweight=None, dbias=None, dresidual=None, dbranch=None,
+                           dropout=0.0, rng=None, workspace=None, stream=None) -> None:
+    """Gradient of the norm and of the dropped branch: dx = that of h (plus dresidual), dbranch = that of the forward's
+    x (with its dropout and rng), dweight and dbias fp32 [cols] (either needs a workspace of at least one fp32 row
+    each).  dy, h, dresidual, dx, dbranch: [rows x cols] of one type; mean, rstd: the forward's."""
+    index, handle = _where(stream)
+    status = (_MODULE or _load_module()).layer_back(index, handle, dy, h, mean, rstd, weight, dx, dweight, dbias,
+        dresidual, dbranch, dropout, rng, workspace)
+    if status:
+        _settle(status, fp8_layernorm_backward, dy, h, mean, rstd, weight, dx, dweight, dbias, dresidual, dbranch,
+                dropout, rng, workspace, stream)

@@ -20,6 +20,7 @@
 #include <type_traits>
 
 #include "activation.hpp"
+#include "column_sums.hpp"
 #include "launch.hpp"
 #include "stats.hpp"
 #include "transpose.hpp"
@@ -175,10 +176,8 @@ __global__ __launch_bounds__(kNT, 4) void act_backward_kernel(BackArgs a) {
   if constexpr (STATS) block_finish<kNT / 64>(st.amax(), wave_sum_u32(st.sat), a.amax_bits, a.sat, a.stat_slots);
 }
 
-// out[n] = sum over the rows of partials [count x cols]: 16 columns a workgroup, 64
-// lanes down the rows of each, then a tree in LDS.  With statistics' slots, one more
-// workgroup (the last) reduces those, which saves a launch (3 us of a small call).
-constexpr int kSumLanes = 64;
+// out[n] = sum over the rows of partials [count x cols] (column_sums.hpp).  With statistics'
+// slots, one more workgroup (the last) reduces those, which saves a launch (3 us of a small call).
 __global__ __launch_bounds__(16 * kSumLanes) void column_sums_kernel(const float* __restrict__ partials, int count,
                                                                     int64_t cols, float* __restrict__ out,
                                                                     const uint4* __restrict__ slots, int nslots,
@@ -211,28 +210,9 @@ __global__ __launch_bounds__(16 * kSumLanes) void column_sums_kernel(const float
     }
     return;
   }
-  __shared__ float buf[kSumLanes][17];
-  const int cx = threadIdx.x & 15, ry = threadIdx.x >> 4;
-  const int64_t c = (int64_t)blockIdx.x * 16 + cx;
-  float v = 0.0f;
-  if (c < cols) {
-    int r = ry;
-    for (; r + 7 * kSumLanes < count; r += 8 * kSumLanes) {
-      float p[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u) p[u] = partials[(int64_t)(r + u * kSumLanes) * cols + c];
-      v += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
-    }
-    for (; r < count; r += kSumLanes) v += partials[(int64_t)r * cols + c];
-  }
-  buf[ry][cx] = v;
-  __syncthreads();
-#pragma unroll
-  for (int half = kSumLanes / 2; half > 0; half >>= 1) {
-    if (ry < half) buf[ry][cx] += buf[ry + half][cx];
-    __syncthreads();
-  }
-  if (ry == 0 && c < cols) out[c] = buf[0][cx];
+  const int64_t c = (int64_t)blockIdx.x * 16 + (threadIdx.x & 15);
+  const float v = column_sum(partials, count, cols, c, c < cols);
+  if (threadIdx.x < 16 && c < cols) out[c] = v;
 }
 
 template <int XT, int FMT, int ACT, bool GATED>

@@ -5,27 +5,18 @@
 
 #include <atomic>
 
-#include "fp8mi.h"
+#include "api_common.hpp"
 #include "epilogue.hpp"
 #include "launch.hpp"
 
 namespace {
 
-constexpr int64_t kMaxDim = 0x7FFFFFFF;             // kernels index rows/cols with 32-bit ints
-constexpr int64_t kMaxGemmK = int64_t(1) << 23;     // 256 rows x K bytes of a tile slab in a 32-bit buffer offset
-constexpr int64_t kMaxGroupedK = int64_t(1) << 22;  // 512 rows x K bytes (the grouped kernels' widest slab)
-constexpr int64_t kMaxBufferBytes = 0x7FFFFFFF;     // any offset a buffer load carries in one 32-bit register
-constexpr int64_t kMaxBackCols = int64_t(1) << 25;  // 16 rows of d in a 32-bit byte offset (fp32)
-constexpr int64_t kMaxElems = (int64_t)1 << 40;     // sanity bound on any one tensor
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_device_ok[kMaxDevices];         // 0 unknown, 1 gfx950, -1 not usable
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool fmt_ok(int f) { return f == FP8MI_E4M3 || f == FP8MI_E5M2; }
-bool dtype_ok(int d) { return d == FP8MI_F32 || d == FP8MI_BF16; }
-bool accum_ok(int a) { return a == FP8MI_ACCUM_EXACT || a == FP8MI_ACCUM_MFMA_FP8; }
+}  // namespace
 
-bool act_ok(int a) { return a == FP8MI_ACT_NONE || a == FP8MI_ACT_RELU || a == FP8MI_ACT_SILU || a == FP8MI_ACT_GELU; }
+namespace fp8mi {
 
 int check_device() {
   int dev = -1;
@@ -52,15 +43,9 @@ int check_device() {
   return state == 1 ? FP8MI_OK : FP8MI_ERR_DEVICE;
 }
 
-int launched(hipError_t e) { return e == hipSuccess ? FP8MI_OK : FP8MI_ERR_LAUNCH; }
+}  // namespace fp8mi
 
-bool dims_ok(int64_t rows, int64_t cols) {
-  if (rows < 0 || cols < 0 || rows > kMaxElems || cols > kMaxElems) return false;
-  if (rows != 0 && cols > kMaxElems / rows) return false;
-  return true;
-}
-
-}  // namespace
+using namespace fp8mi;
 
 extern "C" {
 

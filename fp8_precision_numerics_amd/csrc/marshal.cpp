@@ -31,6 +31,8 @@ decltype(&fp8_rmsnorm_quantize_blockwise) p_norm_blocks;
 decltype(&fp8_rmsnorm_backward) p_norm_back;
 decltype(&fp8_act_backward) p_act_back;
 decltype(&fp8_gated_backward) p_gated_back;
+decltype(&fp8_layernorm_quantize) p_layer;
+decltype(&fp8_layernorm_backward) p_layer_back;
 
 // One call's operands: every tensor must be on the first one's device.
 class Call {
@@ -358,6 +360,61 @@ PyObject* gemm(PyObject* const* args, Py_ssize_t n) {
   return invoke(p_gemm, pa, fa, pb, fb, trans ? 1 : 0, M, N, K, sa, sb, pc, type, accum, c.stream);
 }
 
+// cur stream x weight bias eps fmt scale q residual sum_out mean rstd amax sat dropout rng workspace
+PyObject* layer(PyObject* const* args, Py_ssize_t n) {
+  Call c(args, n, 18);
+  const at::Tensor& x = c.first(2, "x", 2);
+  const int xt = float_type(x, "x", PyExc_ValueError);
+  const at::ScalarType t = x.scalar_type();
+  const int64_t rows = x.size(0), cols = x.size(1);
+  size_t bytes;
+  void* px = c.check(&x, "x", t, false, {});
+  void* pw = c.vec(3, "weight", t, cols);
+  void* pb = c.vec(4, "bias", t, cols);
+  const float eps = (float)c.number(5);
+  const int fmt = c.format(6);
+  float* scale = c.scalar(7, "scale");
+  void* q = c.mat(8, "q", at::kByte, rows, cols);
+  void* res = c.mat(9, "residual", t, rows, cols);
+  void* sum = c.mat(10, "sum_out", t, rows, cols);
+  void* mean = c.vec(11, "mean", at::kFloat, rows);
+  void* rstd = c.vec(12, "rstd", at::kFloat, rows);
+  float* amax = c.scalar(13, "amax");
+  unsigned long long* sat = c.count(14);
+  const float drop = (float)c.number(15);
+  void* rng = c.vec(16, "rng", at::kLong, 2);
+  void* ws = c.space(17, &bytes);
+  if (c.elsewhere()) return c.device();
+  return invoke(p_layer, px, res, pw, pb, xt, rows, cols, eps, drop, (const uint64_t*)rng, fmt, scale, sum, (uint8_t*)q,
+                                 (float*)mean, (float*)rstd, amax, sat, ws, bytes, c.stream);
+}
+
+// cur stream dy h mean rstd weight dx dweight dbias dresidual dbranch dropout rng workspace
+PyObject* layer_back(PyObject* const* args, Py_ssize_t n) {
+  Call c(args, n, 15);
+  const at::Tensor& dy = c.first(2, "dy", 2);
+  const int xt = float_type(dy, "dy", PyExc_ValueError);
+  const at::ScalarType t = dy.scalar_type();
+  const int64_t rows = dy.size(0), cols = dy.size(1);
+  size_t bytes;
+  void* pdy = c.check(&dy, "dy", t, false, {});
+  void* h = c.mat(3, "h", t, rows, cols);
+  void* mean = c.vec(4, "mean", at::kFloat, rows);
+  void* rstd = c.vec(5, "rstd", at::kFloat, rows);
+  void* w = c.vec(6, "weight", t, cols);
+  void* dx = c.mat(7, "dx", t, rows, cols);
+  void* dw = c.vec(8, "dweight", at::kFloat, cols);
+  void* db = c.vec(9, "dbias", at::kFloat, cols);
+  void* dres = c.mat(10, "dresidual", t, rows, cols);
+  void* branch = c.mat(11, "dbranch", t, rows, cols);
+  const float drop = (float)c.number(12);
+  void* rng = c.vec(13, "rng", at::kLong, 2);
+  void* ws = c.space(14, &bytes);
+  if (c.elsewhere()) return c.device();
+  return invoke(p_layer_back, pdy, h, (const float*)mean, (const float*)rstd, w, dres, xt, rows, cols, drop,
+                                      (const uint64_t*)rng, dx, branch, (float*)dw, (float*)db, ws, bytes, c.stream);
+}
+
 template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   try {
@@ -372,27 +429,23 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
 
 // Addresses of the entry points, in the order of the declarations above.
 PyObject* bind(PyObject* const* args, Py_ssize_t n) {
-  if (n != 8) raise(PyExc_TypeError, "%s", "eight addresses");
-  void* p[8];
-  for (int i = 0; i < 8; ++i) {
-    p[i] = PyLong_AsVoidPtr(args[i]);
+  void* const slots[] = {&p_gemm, &p_gated, &p_fused, &p_norm, &p_norm_blocks, &p_norm_back, &p_act_back, &p_gated_back,
+                         &p_layer, &p_layer_back};
+  constexpr Py_ssize_t count = sizeof(slots) / sizeof(slots[0]);
+  if (n != count) raise(PyExc_TypeError, "%s", "an address for every entry point");
+  for (Py_ssize_t i = 0; i < count; ++i) {
+    void* const p = PyLong_AsVoidPtr(args[i]);
     if (PyErr_Occurred()) throw Raised{};
+    std::memcpy(slots[i], &p, sizeof(void*));
   }
-  std::memcpy(&p_gemm, &p[0], sizeof(void*));
-  std::memcpy(&p_gated, &p[1], sizeof(void*));
-  std::memcpy(&p_fused, &p[2], sizeof(void*));
-  std::memcpy(&p_norm, &p[3], sizeof(void*));
-  std::memcpy(&p_norm_blocks, &p[4], sizeof(void*));
-  std::memcpy(&p_norm_back, &p[5], sizeof(void*));
-  std::memcpy(&p_act_back, &p[6], sizeof(void*));
-  std::memcpy(&p_gated_back, &p[7], sizeof(void*));
   Py_RETURN_NONE;
 }
 
 #define ENTRY(name, fn) {name, (PyCFunction)(void (*)(void))entry<fn>, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ENTRY("bind", bind), ENTRY("gemm", gemm), ENTRY("gated", gated), ENTRY("fused", fused),
                          ENTRY("norm", norm), ENTRY("norm_blocks", norm_blocks), ENTRY("norm_back", norm_back),
-                         ENTRY("act_back", act_back), ENTRY("gated_back", gated_back), {nullptr, nullptr, 0, nullptr}};
+                         ENTRY("act_back", act_back), ENTRY("gated_back", gated_back), ENTRY("layer", layer),
+                         ENTRY("layer_back", layer_back), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fp8mi_marshal", nullptr, -1, methods};
 
 }  // namespace

@@ -563,6 +563,69 @@ FP8MI_API int fp8_gated_backward(const void* dh, int xtype, const uint16_t* gu, 
                        const float* scale, uint8_t* q, uint8_t* q_t, float* amax, unsigned long long* sat,
                        void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * The operators at both ends of a model that is trained on these products: the norm
+ * with a mean, the loss over the vocabulary, the embedding.
+ *
+ * Dropout: value i of a tensor [rows x cols] is dropped (0) where a number of 16 bits,
+ * u_i, is below T = round(65536 * dropout), and multiplied with 65536 / (65536 - T)
+ * otherwise.  u_i is half-word i % 8 (word (i % 8) / 2, lower half first) of the 128
+ * bits that Philox4x32 with 10 rounds (Salmon, Moraes, Dror, Shaw, SC 2011) gives for the counter
+ * (g mod 2^32, g / 2^32, offset mod 2^32, offset / 2^32), g = i / 8, and the key (seed mod 2^32, seed / 2^32).
+ * No mask is stored: a backward call with the same rng draws the same values.
+ *   dropout  host, in [0, 1), T at most 65535 (else FP8MI_ERR_SHAPE); 0: none.
+ *   rng      device, 2 uint64 {seed, offset}, 8-B aligned; not read (may be NULL) where T is 0.
+ *            Calls that must not drop the same places take another offset (or seed);
+ *            being device memory, it may change between replays of a captured call.
+ */
+
+/*
+ * fp8_layernorm_quantize — dropout of a branch, residual addition, layer norm and the
+ * cast with a given (delayed) scale, in one pass over the row.
+ *
+ *   h = round_to_xtype(drop(x) + residual)
+ *   m = mean over the row of h,  r = 1 / sqrt(mean over the row of (h - m)^2 + eps)   (fp32 sums)
+ *   y = (h - m) * r * weight + bias             (fp32)
+ *   q = round_to_fp8(fp32(y * scale)), as fp8_quantize;  amax, sat as fp8_rmsnorm_quantize
+ *
+ * x, residual  device, [rows x cols] of xtype; residual may be NULL.
+ * weight, bias device, [cols] of xtype; bias may be NULL.
+ * sum_out      device, [rows x cols] of xtype, receives h; or NULL.  It may be x or
+ *              the residual itself (updated in place).
+ * mean, rstd   device, [rows] fp32, receive m and r (what the gradient needs); or NULL.
+ * The other arguments and the rules are fp8_rmsnorm_quantize's.
+ */
+FP8MI_API int fp8_layernorm_quantize(const void* x, const void* residual, const void* weight, const void* bias, int xtype,
+                           int64_t rows, int64_t cols, float eps, float dropout, const uint64_t* rng, int fmt,
+                           const float* scale, void* sum_out, uint8_t* q, float* mean, float* rstd, float* amax,
+                           unsigned long long* sat, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * fp8_layernorm_backward — gradient of y = (h - m) * r * weight + bias and of h = drop(x) + residual.
+ *
+ *   g = dy * weight,  a = (h - m) * r
+ *   dh = r * (g - mean over the row of g - a * mean over the row of (g * a)) + dresidual
+ *   dx = round_to_xtype(dh)                      (of h, hence of the residual)
+ *   dbranch = round_to_xtype(drop(dh))           (of the forward's x, with the forward's dropout and rng)
+ *   dweight[n] = sum over the rows of dy * a,  dbias[n] = sum over the rows of dy
+ *
+ * dy, h        device, [rows x cols] of xtype (h: the forward's sum_out, or its x).
+ * mean, rstd   device, [rows] fp32, from the forward.
+ * dresidual    as fp8_rmsnorm_backward's.
+ * dx           device, [rows x cols] of xtype.  It may be dy or dresidual itself.
+ * dbranch      device, [rows x cols] of xtype, or NULL; another buffer than dx, and dy or dresidual
+ *              only where dx is not that one.
+ * dweight, dbias  device, [cols] fp32, overwritten, or NULL.
+ * workspace    device scratch, needed with dweight or dbias: one fp32 row of cols values of each
+ *              that is asked for per workgroup (at least one, else FP8MI_ERR_WORKSPACE; up to 1024 are used).
+ *              The sums' order is fixed for a given device, shape and workspace size.
+ * cols must be a multiple of 16; all 16-B aligned.
+ */
+FP8MI_API int fp8_layernorm_backward(const void* dy, const void* h, const float* mean, const float* rstd, const void* weight,
+                           const void* dresidual, int xtype, int64_t rows, int64_t cols, float dropout,
+                           const uint64_t* rng, void* dx, void* dbranch, float* dweight, float* dbias, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

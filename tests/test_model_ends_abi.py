@@ -1,0 +1,74 @@
+"""Host-only checks of the entry points at both ends of a model: argument combinations the
+library refuses before touching a device (fake pointers, never dereferenced), and
+the binding's own refusals.  Nothing here can reach a kernel."""
+
+import ctypes
+
+import pytest
+import torch
+
+import fp8_precision_numerics_amd as fm
+from fp8_precision_numerics_amd import _binding as binding
+
+OK, ENULL, ESHAPE, EALIGN, EFMT, EDTYPE, EACCUM, EWS = 0, -1, -2, -3, -4, -5, -8, -10
+P, P8, P4 = ctypes.c_void_p(0x10000), ctypes.c_void_p(0x10008), ctypes.c_void_p(0x10004)   # 16-B, 8-B and 4-B aligned
+P2 = ctypes.c_void_p(0x20000)
+BIG = 1 << 41
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return fm.load_library()
+
+
+def call(fn, defaults, **changes):
+    args = dict(defaults, **changes)
+    assert args.keys() == defaults.keys()
+    return fn(*args.values())
+
+
+NORM = dict(x=P, residual=P, weight=P, bias=P, xtype=1, rows=4, cols=64, eps=1e-5, dropout=0.1, rng=P, fmt=0, scale=P, sum_out=P, q=P,
+            mean=None, rstd=None, amax=None, sat=None, ws=None, ws_bytes=0, stream=None)
+
+
+@pytest.mark.parametrize("want,change", [
+    (EDTYPE, dict(xtype=7)), (EFMT, dict(fmt=5)), (ESHAPE, dict(rows=-1)), (ESHAPE, dict(rows=BIG)), (ESHAPE, dict(cols=-16)),
+    (ESHAPE, dict(eps=-1.0)), (ESHAPE, dict(eps=float("nan"))), (EALIGN, dict(cols=72)), (ENULL, dict(x=None)), (ENULL, dict(weight=None)),
+    (ENULL, dict(q=None)), (ENULL, dict(scale=None)), (EALIGN, dict(x=P8)), (EALIGN, dict(residual=P8)), (EALIGN, dict(weight=P8)),
+    (EALIGN, dict(bias=P8)), (EALIGN, dict(sum_out=P8)), (EALIGN, dict(q=P8)), (EALIGN, dict(ws=P8, ws_bytes=64)), (EALIGN, dict(ws=P, ws_bytes=8)),
+    (ESHAPE, dict(dropout=-0.1)), (ESHAPE, dict(dropout=1.0)), (ESHAPE, dict(dropout=float("nan"))), (ESHAPE, dict(dropout=0.999995)),
+    (ENULL, dict(rng=None)), (EALIGN, dict(rng=P4)), (OK, dict(rows=0)), (OK, dict(cols=0, x=None, q=None, weight=None, scale=None))])
+def test_norm_refusals(lib, want, change):
+    assert call(lib.fp8_layernorm_quantize, NORM, **change) == want
+
+
+NORM_BACK = dict(dy=P, h=P, mean=P, rstd=P, weight=P, dres=None, xtype=0, rows=4, cols=64, dropout=0.5, rng=P, dx=P, dbranch=P2, dweight=P, dbias=P,
+                 ws=P, ws_bytes=512, stream=None)
+
+
+@pytest.mark.parametrize("want,change", [
+    (EDTYPE, dict(xtype=3)), (ESHAPE, dict(rows=-2)), (EALIGN, dict(cols=24)), (ENULL, dict(dy=None)), (ENULL, dict(h=None)), (ENULL, dict(mean=None)),
+    (ENULL, dict(rstd=None)), (ENULL, dict(weight=None)), (ENULL, dict(dx=None)), (EALIGN, dict(dy=P8)), (EALIGN, dict(h=P8)),
+    (EALIGN, dict(weight=P8)), (EALIGN, dict(dres=P8)), (EALIGN, dict(dx=P8)), (EALIGN, dict(dbranch=P8)), (EALIGN, dict(dweight=P8)),
+    (EALIGN, dict(dbias=P8)), (EALIGN, dict(ws=P8)), (ENULL, dict(ws=None, ws_bytes=0)), (EWS, dict(ws_bytes=511)), (EWS, dict(ws_bytes=255, dbias=None)),
+    (ESHAPE, dict(dbranch=P)), (ESHAPE, dict(dropout=1.5)), (ENULL, dict(rng=None)), (OK, dict(rows=0, dweight=None, dbias=None)), (OK, dict(cols=0))])
+def test_norm_backward_refusals(lib, want, change):
+    assert call(lib.fp8_layernorm_backward, NORM_BACK, **change) == want
+
+
+@pytest.mark.parametrize("name", ["layer", "layer_back"])
+def test_a_wrong_number_of_arguments_is_a_type_error(name):
+    module = binding._MODULE or binding._load_module()
+    with pytest.raises(TypeError):
+        getattr(module, name)(0, 0)
+    with pytest.raises(TypeError):
+        getattr(module, name)(*[None] * 40)
+
+
+def test_binding_refuses_host_tensors():
+    x, w = torch.zeros(4, 32), torch.zeros(32)
+    q, one = torch.zeros(4, 32, dtype=torch.uint8), torch.ones(1)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        fm.fp8_layernorm_quantize(x, w, w, 1e-5, "e4m3", one, q)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        fm.fp8_layernorm_backward(x, x, torch.ones(4), torch.ones(4), w, x)
