@@ -21,8 +21,8 @@ __all__ = ["E4M3", "E5M2", "F32", "BF16", "ACCUM_EXACT", "ACCUM_MFMA_FP8", "QUAN
            "fp8_quantize_mx", "fp8_gemm_mx", "mx_scale_ld", "mx_scale_pos", "fp8_quantize_update",
            "fp8_quantize_update_noalloc", "fp8_rmsnorm_quantize", "fp8_rmsnorm_quantize_blockwise",
            "fp8_rmsnorm_backward", "fp8_gemm_gated", "fp8_gemm_fused", "fp8_act_backward", "fp8_gated_backward",
-           "fp8_layernorm_quantize", "fp8_layernorm_backward",
-           "EXPORTED_SYMBOLS"]
+           "fp8_layernorm_quantize", "fp8_layernorm_backward", "fp8_embedding", "fp8_embedding_backward",
+           "embedding_workspace_bytes", "EXPORTED_SYMBOLS"]
 
 E4M3, E5M2 = 0, 1
 F32, BF16 = 0, 1
@@ -37,7 +37,8 @@ EXPORTED_SYMBOLS = ("fp8mi_status_string", "fp8mi_version", "fp8_quantize", "fp8
                     "fp8_shared_scale", "fp8_dequant_sum", "fp8_quantize_mx", "fp8_gemm_mx",
                     "fp8_quantize_update", "fp8_quantize_update_noalloc", "fp8_rmsnorm_quantize",
                     "fp8_rmsnorm_quantize_blockwise", "fp8_rmsnorm_backward", "fp8_gemm_gated", "fp8_gemm_fused",
-                    "fp8_act_backward", "fp8_gated_backward", "fp8_layernorm_quantize", "fp8_layernorm_backward")
+                    "fp8_act_backward", "fp8_gated_backward", "fp8_layernorm_quantize", "fp8_layernorm_backward",
+                    "fp8_embedding", "fp8_embedding_backward", "fp8mi_embedding_workspace")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
@@ -116,9 +117,13 @@ def load_library():
     lib.fp8_layernorm_quantize.argtypes = [vp, vp, vp, vp, ci, i64, i64, cf, cf, vp, ci, vp, vp, vp, vp, vp, vp, vp, vp,
                                            sz, vp]
     lib.fp8_layernorm_backward.argtypes = [vp, vp, vp, vp, vp, vp, ci, i64, i64, cf, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.fp8_embedding.argtypes = [vp, ci, i64, vp, ci, i64, i64, vp, cf, vp, ci, vp]
+    lib.fp8_embedding_backward.argtypes = [vp, ci, i64, vp, ci, i64, i64, cf, vp, vp, ci, vp, sz, vp]
+    lib.fp8mi_embedding_workspace.argtypes = [i64, i64]
+    lib.fp8mi_embedding_workspace.restype = sz
     for name in ("fp8_rmsnorm_quantize", "fp8_rmsnorm_quantize_blockwise", "fp8_rmsnorm_backward", "fp8_gemm_gated",
                  "fp8_gemm_fused", "fp8_act_backward", "fp8_gated_backward", "fp8_layernorm_quantize",
-                 "fp8_layernorm_backward"):
+                 "fp8_layernorm_backward", "fp8_embedding", "fp8_embedding_backward"):
         getattr(lib, name).restype = ci
     _LIB = lib
     return lib
@@ -200,7 +205,7 @@ def _call(name, status):
 # feed-forward operators, those at the ends of a model) are marshalled by the extension module of csrc/marshal.cpp.
 _MARSHALLED = ("fp8_gemm", "fp8_gemm_gated", "fp8_gemm_fused", "fp8_rmsnorm_quantize", "fp8_rmsnorm_quantize_blockwise",
                "fp8_rmsnorm_backward", "fp8_act_backward", "fp8_gated_backward", "fp8_layernorm_quantize",
-               "fp8_layernorm_backward")
+               "fp8_layernorm_backward", "fp8_embedding", "fp8_embedding_backward")
 _MODULE = None
 # The current stream's handle and device without building the Python objects
 # around them (about 2 us of a small call).
@@ -615,3 +620,31 @@ def fp8_layernorm_backward(dy, h, mean, rstd, weight, dx, dweight=None, dbias=No
     if status:
         _settle(status, fp8_layernorm_backward, dy, h, mean, rstd, weight, dx, dweight, dbias, dresidual, dbranch,
                 dropout, rng, workspace, stream)
+
+
+def fp8_embedding(tokens, table, out, scale=1.0, fmt=None, sinv=None, stream=None) -> None:
+    """out[t] = table[tokens[t]] * scale, a row of zeros where the token lies outside the table.
+
+    tokens: int32 or int64 [rows]; table: [vocab x cols] fp32 or bf16, or uint8 codes of the format `fmt` with their
+    inverse scale sinv (fp32[1]); out: [rows x cols] fp32 or bf16.  cols must be a multiple of 16."""
+    index, handle = _where(stream)
+    status = (_MODULE or _load_module()).embed(index, handle, tokens, table, out, scale, fmt, sinv)
+    if status:
+        _settle(status, fp8_embedding, tokens, table, out, scale, fmt, sinv, stream)
+
+
+def embedding_workspace_bytes(rows: int, cols: int) -> int:
+    """Workspace of fp8_embedding_backward for so many tokens and columns."""
+    return int(load_library().fp8mi_embedding_workspace(rows, cols))
+
+
+def fp8_embedding_backward(tokens, dy, dtable, scale=1.0, base=None, workspace=None, stream=None) -> None:
+    """dtable[v] = base[v] + scale * the sum of dy[t] over the places of token v, in the order of t (fp32 sums).
+
+    tokens: int32 or int64 [rows], at most 2^20; those outside the table take no part; dy: [rows x cols] fp32 or bf16;
+    dtable, base: [vocab x cols] fp32 or bf16, of one type (base may be dtable: a gradient to add to); workspace: uint8
+    of embedding_workspace_bytes(rows, cols).  cols must be a multiple of 16."""
+    index, handle = _where(stream)
+    status = (_MODULE or _load_module()).embed_back(index, handle, tokens, dy, dtable, scale, base, workspace)
+    if status:
+        _settle(status, fp8_embedding_backward, tokens, dy, dtable, scale, base, workspace, stream)

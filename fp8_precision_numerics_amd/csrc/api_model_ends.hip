@@ -23,6 +23,11 @@ int make_dropout(float p, const uint64_t* rng, Dropout* out) {
   return FP8MI_OK;
 }
 
+constexpr int64_t kMaxEmbedCols = int64_t(1) << 20;  // workgroups a row, of which a grid has thousands
+
+bool index_ok(int t) { return t == FP8MI_I32 || t == FP8MI_I64; }
+bool index_aligned(const void* p, int t) { return (reinterpret_cast<uintptr_t>(p) & (t == FP8MI_I64 ? 7u : 3u)) == 0; }
+
 }  // namespace
 
 extern "C" {
@@ -78,6 +83,42 @@ int fp8_layernorm_backward(const void* dy, const void* h, const float* mean, con
   if (dev != FP8MI_OK) return dev;
   return launched(launch_layernorm_backward(dy, h, mean, rstd, weight, dresidual, xtype, rows, cols, drop, dx, dbranch,
                                             dweight, dbias, workspace, workspace_bytes, (hipStream_t)stream));
+}
+
+int fp8_embedding(const void* tokens, int itype, int64_t rows, const void* table, int ttype, int64_t vocab, int64_t cols,
+                  const float* sinv, float scale, void* out, int otype, void* stream) {
+  const bool codes = ttype == FP8MI_OUT_E4M3 || ttype == FP8MI_OUT_E5M2;
+  if (!index_ok(itype) || !dtype_ok(otype) || (ttype != FP8MI_OUT_F32 && ttype != FP8MI_OUT_BF16 && !codes)) return FP8MI_ERR_DTYPE;
+  if (!dims_ok(rows, cols) || !dims_ok(vocab, cols) || vocab > kMaxDim || cols > kMaxEmbedCols) return FP8MI_ERR_SHAPE;
+  if ((cols & 15) != 0) return FP8MI_ERR_ALIGN;
+  if (rows * cols == 0) return FP8MI_OK;
+  if (!tokens || (vocab && !table) || !out || (codes && !sinv)) return FP8MI_ERR_NULL;
+  if (!index_aligned(tokens, itype) || !aligned16(table) || !aligned16(out)) return FP8MI_ERR_ALIGN;
+  const int dev = check_device();
+  if (dev != FP8MI_OK) return dev;
+  return launched(launch_embedding(tokens, itype == FP8MI_I64, rows, table, ttype, vocab, cols, sinv, scale, out, otype, (hipStream_t)stream));
+}
+
+size_t fp8mi_embedding_workspace(int64_t rows, int64_t cols) {
+  if (rows < 0 || cols < 0 || rows > kMaxTokens || cols > kMaxEmbedCols) return 0;
+  return embedding_workspace(rows, cols);
+}
+
+int fp8_embedding_backward(const void* tokens, int itype, int64_t rows, const void* dy, int dytype, int64_t vocab,
+                           int64_t cols, float scale, const void* base, void* dtable, int ttype, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  if (!index_ok(itype) || !dtype_ok(dytype) || !dtype_ok(ttype)) return FP8MI_ERR_DTYPE;
+  if (!dims_ok(rows, cols) || !dims_ok(vocab, cols) || vocab > kMaxDim || cols > kMaxEmbedCols || rows > kMaxTokens) return FP8MI_ERR_SHAPE;
+  if ((cols & 15) != 0) return FP8MI_ERR_ALIGN;
+  if (workspace && !aligned16(workspace)) return FP8MI_ERR_ALIGN;
+  if (vocab * cols == 0 || (rows == 0 && base == dtable)) return FP8MI_OK;
+  if (!dtable || (rows && (!tokens || !dy || !workspace))) return FP8MI_ERR_NULL;
+  if (!aligned16(dy) || !aligned16(base) || !aligned16(dtable) || !index_aligned(tokens, itype)) return FP8MI_ERR_ALIGN;
+  if (rows && workspace_bytes < embedding_workspace(rows, cols)) return FP8MI_ERR_WORKSPACE;
+  const int dev = check_device();
+  if (dev != FP8MI_OK) return dev;
+  return launched(launch_embedding_backward(tokens, itype == FP8MI_I64, rows, dy, dytype, vocab, cols, scale, base, dtable, ttype, workspace,
+                                            (hipStream_t)stream));
 }
 
 }  // extern "C"

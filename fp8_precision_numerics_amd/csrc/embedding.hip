@@ -1,0 +1,439 @@
+// Embedding lookup with scaling, and its gradient by sorted tokens.
+//
+//   out[t] = round(scale * table[id_t])              (zeros where the id lies outside the table)
+//   dtable[v] = round(base[v] + scale * sum over { t : id_t = v } of dy[t])
+//
+// Both are bound by memory.  The lookup is a gather of whole rows: a lane moves octets
+// (eight values: 16 bytes of bf16, 8 of codes), consecutive lanes consecutive ones.
+//
+// The gradient adds rows in an order that is fixed (t ascending, joined in pieces), so
+// that its bits repeat: tokens are sorted by (id, t), stably and without atomics.
+//   rank_tokens_kernel   blocks of kSortBlock tokens: a token's place is the number of tokens of
+//                        its block that come before it, counted by comparing it with all of them
+//                        (LDS broadcasts, one wave per sixteenth of the block): one launch, no
+//                        passes over digits.  8192 tokens are 67 M comparisons.
+//   merge_tokens_kernel  more blocks than one: a token's place in the whole is its place in its
+//                        block plus its rank in every other block, by bisection.
+//   token_sums_kernel    the sorted list in chunks of equal length, so that a common token costs
+//                        no workgroup more than a rare one: runs of one id that lie inside a
+//                        chunk are written, those that cross its ends leave partial rows.
+//   token_joins_kernel   adds the partial rows of each run that crosses.
+// and before them fill_rows_kernel writes base (or zeros) to every row.
+#include "launch.hpp"
+#include "model_ends.hpp"
+#include "row_octets.hpp"
+
+namespace fp8mi {
+namespace {
+
+constexpr uint32_t kNoToken = 0xFFFFFFFFu;  // sorts behind every id
+constexpr int kLookNT = 256;
+
+__device__ __forceinline__ int64_t token_at(const void* tokens, bool wide, int64_t t) {
+  return wide ? reinterpret_cast<const int64_t*>(tokens)[t] : reinterpret_cast<const int32_t*>(tokens)[t];
+}
+
+// ---------------------------------------------------------------------------
+// Lookup
+// ---------------------------------------------------------------------------
+struct LookupArgs {
+  const void* tokens;
+  const void* table;
+  const float* sinv;  // of codes
+  void* out;
+  int64_t rows, vocab, octets;
+  float scale;
+  int lanes;          // lanes a row, a power of two up to kLookNT
+  int slices;         // workgroups a row
+  bool wide;          // int64 tokens
+};
+
+// Table types: kF32, kBF16, and codes.
+enum : int { kTableE4M3 = 2, kTableE5M2 = 3 };
+
+// Eight codes (bytes of w.x, then w.y), exactly.
+template <int FMT>
+__device__ __forceinline__ void decode8(uint2 w, float* f) {
+  const uint32_t p[2] = {w.x, w.y};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    v2f lo, hi;
+    if constexpr (FMT == kE4M3) {
+      lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)p[i], false);
+      hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)p[i], true);
+    } else {
+      lo = __builtin_amdgcn_cvt_pk_f32_bf8((int)p[i], false);
+      hi = __builtin_amdgcn_cvt_pk_f32_bf8((int)p[i], true);
+    }
+    f[4 * i] = lo[0];
+    f[4 * i + 1] = lo[1];
+    f[4 * i + 2] = hi[0];
+    f[4 * i + 3] = hi[1];
+  }
+}
+
+template <int TT, int OT>
+__global__ __launch_bounds__(kLookNT) void lookup_kernel(LookupArgs a) {
+  const int block = blockIdx.x / a.slices, blocks = gridDim.x / a.slices;
+  const int slice = blockIdx.x - block * a.slices;
+  const int lane = threadIdx.x & (a.lanes - 1), side = kLookNT / a.lanes;  // rows side by side
+  float inv = 1.0f;
+  if constexpr (TT == kTableE4M3 || TT == kTableE5M2) inv = *a.sinv;
+  for (int64_t t = (int64_t)block * side + threadIdx.x / a.lanes; t < a.rows; t += (int64_t)blocks * side) {
+    const int64_t id = token_at(a.tokens, a.wide, t);
+    const bool inside = id >= 0 && id < a.vocab;
+    for (int64_t o = lane + (int64_t)slice * a.lanes; o < a.octets; o += (int64_t)a.lanes * a.slices) {
+      float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (inside) {
+        if constexpr (TT == kF32 || TT == kBF16) {
+          Octet<TT> v;
+          v.load(a.table, id * a.octets + o);
+          v.widen(f);
+        } else {
+          decode8<TT == kTableE4M3 ? kE4M3 : kE5M2>(reinterpret_cast<const uint2*>(a.table)[id * a.octets + o], f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] *= inv;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] *= a.scale;
+      }
+      Octet<OT> r;
+      r.narrow(f);
+      r.store_nt(a.out, t * a.octets + o);
+    }
+  }
+}
+
+// Lanes of a row: the smallest power of two that holds its octets, up to a workgroup.
+int row_lanes(int64_t octets) {
+  int lanes = 2;
+  while (lanes < kLookNT && lanes < octets) lanes *= 2;
+  return lanes;
+}
+
+// ---------------------------------------------------------------------------
+// Sort
+// ---------------------------------------------------------------------------
+constexpr int kSortBlock = 8192;
+constexpr int kSortWaves = 16;
+constexpr int kSortPart = kSortBlock / kSortWaves;  // ids a wave compares with
+
+struct SortArgs {
+  const void* tokens;
+  uint32_t* keys;   // sorted within blocks
+  int32_t* places;  // the tokens' numbers, likewise
+  int64_t rows, vocab;
+  bool wide;
+};
+
+// A workgroup ranks 64 tokens of a block (one a lane), wave w against ids w * kSortPart .. of it.
+__global__ __launch_bounds__(64 * kSortWaves) void rank_tokens_kernel(SortArgs a) {
+  __shared__ __attribute__((aligned(16))) uint32_t ids[kSortBlock];
+  __shared__ int counts[kSortWaves][64];
+  const int64_t first = (int64_t)blockIdx.y * kSortBlock;
+  const int n = (int)(a.rows - first < kSortBlock ? a.rows - first : kSortBlock);
+  for (int j = threadIdx.x; j < kSortBlock; j += 64 * kSortWaves) {
+    uint32_t key = kNoToken;
+    if (j < n) {
+      const int64_t id = token_at(a.tokens, a.wide, first + j);
+      if (id >= 0 && id < a.vocab) key = (uint32_t)id;
+    }
+    ids[j] = key;
+  }
+  __syncthreads();
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = blockIdx.x * 64, mine = group + lane;
+  const uint32_t key = ids[mine];
+  const int lo = w * kSortPart, hi = lo + kSortPart < ((n + 63) & ~63) ? lo + kSortPart : (n + 63) & ~63;
+  int count = 0;
+  // Groups of 64 ids before the lanes' own count where they are not above, those behind where they are below.
+  for (int j0 = lo; j0 < hi; j0 += 64) {
+    if (j0 == group) {
+      for (int j = j0; j < j0 + 64; ++j) count += ids[j] < key || (ids[j] == key && j < mine) ? 1 : 0;
+    } else {
+      // "not above" is "below" the next number; no id reaches kNoToken, whose own order among
+      // themselves does not matter, but must be one: those behind count none of them
+      const uint32_t limit = j0 < group && key != kNoToken ? key + 1u : key;
+      const bool all = j0 < group && key == kNoToken;
+#pragma unroll 4
+      for (int j = j0; j < j0 + 64; j += 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(&ids[j]);
+        count += (v.x < limit) + (v.y < limit) + (v.z < limit) + (v.w < limit);
+      }
+      if (all) {
+        // every id of an earlier group comes before a token that has none
+        for (int j = j0; j < j0 + 64; ++j) count += ids[j] == kNoToken ? 1 : 0;
+      }
+    }
+  }
+  counts[w][lane] = count;
+  __syncthreads();
+  if (w == 0 && mine < n) {
+    int place = 0;
+#pragma unroll
+    for (int p = 0; p < kSortWaves; ++p) place += counts[p][lane];
+    a.keys[first + place] = key;
+    a.places[first + place] = (int32_t)(first + mine);
+  }
+}
+
+// Number of keys of keys[0 .. n) that are below `limit` (equal: they count too).
+__device__ __forceinline__ int count_below(const uint32_t* keys, int n, uint32_t limit, bool equal) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    const uint32_t k = keys[mid];
+    if (k < limit || (equal && k == limit)) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo;
+}
+
+__global__ __launch_bounds__(256) void merge_tokens_kernel(const uint32_t* keys, const int32_t* places, int64_t rows,
+                                                          uint32_t* out_keys, int32_t* out_places) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= rows) return;
+  const int64_t own = i / kSortBlock, blocks = (rows + kSortBlock - 1) / kSortBlock;
+  const uint32_t key = keys[i];
+  int64_t place = i - own * kSortBlock;
+  for (int64_t b = 0; b < blocks; ++b) {
+    if (b == own) continue;
+    const int64_t first = b * kSortBlock;
+    const int n = (int)(rows - first < kSortBlock ? rows - first : kSortBlock);
+    place += count_below(keys + first, n, key, b < own);
+  }
+  out_keys[place] = key;
+  out_places[place] = places[i];
+}
+
+// ---------------------------------------------------------------------------
+// Sums
+// ---------------------------------------------------------------------------
+struct SumArgs {
+  const uint32_t* keys;
+  const int32_t* places;
+  const void* dy;
+  const void* base;  // null: zeros
+  void* dtable;
+  float* partials;   // [chunks x 2 x cols]: a chunk's sum of the run that enters it, of the one that leaves it
+  int64_t rows, octets;
+  float scale;
+  int chunk;         // sorted tokens a chunk
+  int chunks;
+  int lanes, slices; // as in LookupArgs; lanes x slices cover a row
+};
+
+template <int OT>
+__device__ __forceinline__ void write_row(const SumArgs& a, uint32_t key, int64_t o, const float* acc) {
+  const int64_t at = (int64_t)key * a.octets + o;
+  float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (a.base) {
+    Octet<OT> b;
+    b.load(a.base, at);
+    b.widen(f);
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] = __builtin_fmaf(acc[e], a.scale, f[e]);
+  Octet<OT> r;
+  r.narrow(f);
+  r.store(a.dtable, at);
+}
+
+__device__ __forceinline__ void write_partial(const SumArgs& a, int64_t chunk, int side, int64_t o, const float* acc) {
+  float4* p = reinterpret_cast<float4*>(a.partials + ((chunk * 2 + side) * a.octets + o) * 8);
+  p[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+  p[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+}
+
+// The chunk and the octet of a thread; false where it has none.
+__device__ __forceinline__ bool chunk_of(const SumArgs& a, int64_t* chunk, int64_t* o) {
+  const int64_t block = blockIdx.x / a.slices;
+  *chunk = block * (kLookNT / a.lanes) + threadIdx.x / a.lanes;
+  *o = (threadIdx.x & (a.lanes - 1)) + (int64_t)(blockIdx.x - block * a.slices) * a.lanes;
+  return *chunk < a.chunks && *o < a.octets;
+}
+
+template <int DT, int OT>
+__global__ __launch_bounds__(kLookNT) void token_sums_kernel(SumArgs a) {
+  int64_t chunk, o;
+  if (!chunk_of(a, &chunk, &o)) return;
+  const int64_t first = chunk * a.chunk;
+  const int n = (int)(a.rows - first < a.chunk ? a.rows - first : a.chunk);
+  uint32_t key = a.keys[first];
+  const bool enters = first > 0 && a.keys[first - 1] == key;
+  const bool leaves = first + n < a.rows && a.keys[first + n - 1] == a.keys[first + n];
+  bool head = enters;  // the present run came in from the chunk before
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  constexpr int U = 8;  // rows requested at once
+  for (int i = 0; i < n; i += U) {
+    Octet<DT> v[U];
+    uint32_t ks[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      ks[u] = kNoToken;
+      v[u].clear();
+      if (i + u < n) {
+        ks[u] = a.keys[first + i + u];
+        if (ks[u] != kNoToken) v[u].load_nt(a.dy, (int64_t)a.places[first + i + u] * a.octets + o);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i + u < n) {
+        if (ks[u] != key) {
+          if (head) write_partial(a, chunk, 0, o, acc);
+          else write_row<OT>(a, key, o, acc);  // keys ascend, so the one that ends here is a token's
+          head = false;
+          key = ks[u];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
+        }
+        float f[8];
+        v[u].widen(f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] += f[e];
+      }
+    }
+  }
+  if (key == kNoToken) return;
+  if (head) write_partial(a, chunk, 0, o, acc);
+  else if (leaves) write_partial(a, chunk, 1, o, acc);
+  else write_row<OT>(a, key, o, acc);
+}
+
+// A run that leaves the chunk in which it begins: its partial rows, in order.
+template <int OT>
+__global__ __launch_bounds__(kLookNT) void token_joins_kernel(SumArgs a) {
+  int64_t chunk, o;
+  if (!chunk_of(a, &chunk, &o)) return;
+  const int64_t first = chunk * a.chunk, end = first + a.chunk;
+  if (end >= a.rows) return;
+  const uint32_t key = a.keys[end];
+  if (key == kNoToken || a.keys[end - 1] != key) return;                       // nothing leaves
+  if (first > 0 && a.keys[first] == key && a.keys[first - 1] == key) return;   // it began earlier
+  float acc[8];
+  auto add = [&](int64_t c, int side, bool begin) {
+    const float4* p = reinterpret_cast<const float4*>(a.partials + ((c * 2 + side) * a.octets + o) * 8);
+    const float4 lo = p[0], hi = p[1];
+    const float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = begin ? f[e] : acc[e] + f[e];
+  };
+  add(chunk, 1, true);
+  // The chunks that the run enters: up to the one that holds its last token.
+  const int64_t last = end + count_below(a.keys + end, (int)(a.rows - end), key, true) - 1;
+  const int64_t final = last / a.chunk;
+#pragma unroll 4
+  for (int64_t c = chunk + 1; c <= final; ++c) add(c, 0, false);
+  write_row<OT>(a, key, o, acc);
+}
+
+// base, or zeros without one, into the whole table: 16 bytes a lane and turn.
+__global__ __launch_bounds__(256) void fill_rows_kernel(const uint4* base, uint4* to, int64_t count) {
+  typedef unsigned int vec4 __attribute__((ext_vector_type(4)));
+  constexpr int U = 4;
+  const int64_t step = (int64_t)gridDim.x * 256;
+  const vec4* src = reinterpret_cast<const vec4*>(base);
+  vec4* dst = reinterpret_cast<vec4*>(to);
+  int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  for (; i + (U - 1) * step < count; i += U * step) {
+    vec4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = base ? __builtin_nontemporal_load(src + i + u * step) : (vec4){0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int u = 0; u < U; ++u) __builtin_nontemporal_store(v[u], dst + i + u * step);
+  }
+  for (; i < count; i += step) dst[i] = base ? src[i] : (vec4){0u, 0u, 0u, 0u};
+}
+
+// Sorted tokens a chunk: 16 (two requests of eight rows a lane) until that makes 4096
+// chunks, which fill the device; then longer ones.
+int64_t chunk_size(int64_t rows) {
+  const int64_t c = (rows + 4095) / 4096;
+  return c < 16 ? 16 : (c + 7) / 8 * 8;
+}
+
+int64_t up16(int64_t bytes) { return (bytes + 15) & ~int64_t(15); }
+
+template <int TT>
+hipError_t lookup_run(const LookupArgs& a, int otype, unsigned grid, hipStream_t st) {
+  if (otype == kBF16) hipLaunchKernelGGL((lookup_kernel<TT, kBF16>), dim3(grid), dim3(kLookNT), 0, st, a);
+  else hipLaunchKernelGGL((lookup_kernel<TT, kF32>), dim3(grid), dim3(kLookNT), 0, st, a);
+  return hipGetLastError();
+}
+
+template <int OT>
+hipError_t sums_run(const SumArgs& a, int dytype, unsigned grid, hipStream_t st) {
+  if (dytype == kBF16) hipLaunchKernelGGL((token_sums_kernel<kBF16, OT>), dim3(grid), dim3(kLookNT), 0, st, a);
+  else hipLaunchKernelGGL((token_sums_kernel<kF32, OT>), dim3(grid), dim3(kLookNT), 0, st, a);
+  if (a.chunks > 1) hipLaunchKernelGGL(token_joins_kernel<OT>, dim3(grid), dim3(kLookNT), 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_embedding(const void* tokens, bool wide, int64_t rows, const void* table, int ttype, int64_t vocab,
+                            int64_t cols, const float* sinv, float scale, void* out, int otype, hipStream_t stream) {
+  LookupArgs a{tokens, table, sinv, out, rows, vocab, cols / 8, scale, 0, 1, wide};
+  a.lanes = row_lanes(a.octets);
+  int64_t blocks = (rows * a.lanes + kLookNT - 1) / kLookNT;
+  if (blocks > persistent_groups(32)) blocks = persistent_groups(32);
+  // A row over several workgroups only where there are too few rows to fill the device.
+  while (a.slices * a.lanes < a.octets && blocks * a.slices < persistent_groups(2)) ++a.slices;
+  const unsigned grid = (unsigned)(blocks * a.slices);
+  if (ttype == kF32) return lookup_run<kF32>(a, otype, grid, stream);
+  if (ttype == kBF16) return lookup_run<kBF16>(a, otype, grid, stream);
+  if (ttype == kTableE4M3) return lookup_run<kTableE4M3>(a, otype, grid, stream);
+  return lookup_run<kTableE5M2>(a, otype, grid, stream);
+}
+
+size_t embedding_workspace(int64_t rows, int64_t cols) {
+  const int64_t chunks = (rows + chunk_size(rows) - 1) / chunk_size(rows);
+  return (size_t)((rows > kSortBlock ? 4 : 2) * up16(rows * 4) + (chunks > 1 ? chunks * 2 * cols * 4 : 0));
+}
+
+hipError_t launch_embedding_backward(const void* tokens, bool wide, int64_t rows, const void* dy, int dytype,
+                                     int64_t vocab, int64_t cols, float scale, const void* base, void* dtable,
+                                     int ttype, void* workspace, hipStream_t stream) {
+  const int64_t words = vocab * (cols / 8) * (ttype == kBF16 ? 1 : 2);
+  if (base != dtable) {
+    int64_t groups = (words + 1023) / 1024;
+    if (groups > persistent_groups(8)) groups = persistent_groups(8);
+    hipLaunchKernelGGL(fill_rows_kernel, dim3((unsigned)groups), dim3(256), 0, stream,
+                       reinterpret_cast<const uint4*>(base), reinterpret_cast<uint4*>(dtable), words);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (rows == 0) return hipSuccess;
+  uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
+  auto take = [&]() {
+    void* p = ws;
+    ws += up16(rows * 4);
+    return p;
+  };
+  SortArgs s{tokens, reinterpret_cast<uint32_t*>(take()), nullptr, rows, vocab, wide};
+  s.places = reinterpret_cast<int32_t*>(take());
+  const int64_t blocks = (rows + kSortBlock - 1) / kSortBlock;
+  const int64_t in_block = rows < kSortBlock ? rows : kSortBlock;
+  hipLaunchKernelGGL(rank_tokens_kernel, dim3((unsigned)((in_block + 63) / 64), (unsigned)blocks), dim3(64 * kSortWaves), 0,
+                     stream, s);
+  SumArgs a{s.keys, s.places, dy, base, dtable, nullptr, rows, cols / 8, scale, (int)chunk_size(rows), 0, 0, 0};
+  if (blocks > 1) {
+    uint32_t* keys = reinterpret_cast<uint32_t*>(take());
+    int32_t* places = reinterpret_cast<int32_t*>(take());
+    hipLaunchKernelGGL(merge_tokens_kernel, dim3((unsigned)((rows + 255) / 256)), dim3(256), 0, stream, s.keys, s.places,
+                       rows, keys, places);
+    a.keys = keys;
+    a.places = places;
+  }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  a.partials = reinterpret_cast<float*>(ws);
+  a.chunks = (int)((rows + a.chunk - 1) / a.chunk);
+  a.lanes = row_lanes(a.octets);
+  a.slices = (int)((a.octets + a.lanes - 1) / a.lanes);
+  const unsigned grid = (unsigned)(((int64_t)a.chunks * a.lanes + kLookNT - 1) / kLookNT * a.slices);
+  return ttype == kBF16 ? sums_run<kBF16>(a, dytype, grid, stream) : sums_run<kF32>(a, dytype, grid, stream);
+}
+
+}  // namespace fp8mi

@@ -33,6 +33,8 @@ decltype(&fp8_act_backward) p_act_back;
 decltype(&fp8_gated_backward) p_gated_back;
 decltype(&fp8_layernorm_quantize) p_layer;
 decltype(&fp8_layernorm_backward) p_layer_back;
+decltype(&fp8_embedding) p_embed;
+decltype(&fp8_embedding_backward) p_embed_back;
 
 // One call's operands: every tensor must be on the first one's device.
 class Call {
@@ -56,7 +58,7 @@ class Call {
     const at::Tensor* t = tensor(i, name);
     if (!t) raise(PyExc_ValueError, "%s must be a GPU tensor", name);
     if (!t->is_cuda()) raise(PyExc_ValueError, "%s must be a GPU tensor", name);
-    if (t->dim() != dims) raise(PyExc_ValueError, "%s must have %s", name, dims == 2 ? "2 dimensions" : "another shape");
+    if (t->dim() != dims) raise(PyExc_ValueError, "%s must have %s", name, dims == 2 ? "2 dimensions" : "1 dimension");
     device_ = t->get_device();
     return *t;
   }
@@ -144,6 +146,19 @@ int float_type(const at::Tensor& t, const char* name, PyObject* error) {
   if (t.scalar_type() == at::kFloat) return FP8MI_F32;
   if (t.scalar_type() == at::kBFloat16) return FP8MI_BF16;
   raise(error, "%s must be float32 or bfloat16, got %s", name, c10::toString(t.scalar_type()));
+}
+
+int index_type(const at::Tensor& t, const char* name) {
+  if (t.scalar_type() == at::kInt) return FP8MI_I32;
+  if (t.scalar_type() == at::kLong) return FP8MI_I64;
+  raise(PyExc_TypeError, "%s must be int32 or int64, got %s", name, c10::toString(t.scalar_type()));
+}
+
+// A [rows x cols] matrix whose rows or columns are not known beforehand.
+const at::Tensor& matrix(const Call& c, int i, const char* name) {
+  const at::Tensor* t = c.tensor(i, name);
+  if (!t || t->dim() != 2) raise(PyExc_ValueError, "%s must be a GPU tensor of 2 dimensions", name);
+  return *t;
 }
 
 // Output of a fused product: codes where a format is given, else fp32 or bf16.
@@ -415,6 +430,48 @@ PyObject* layer_back(PyObject* const* args, Py_ssize_t n) {
                                       (const uint64_t*)rng, dx, branch, (float*)dw, (float*)db, ws, bytes, c.stream);
 }
 
+// cur stream tokens table out scale fmt sinv
+PyObject* embed(PyObject* const* args, Py_ssize_t n) {
+  Call c(args, n, 8);
+  const at::Tensor& tokens = c.first(2, "tokens", 1);
+  const int it = index_type(tokens, "tokens");
+  const at::Tensor& table = matrix(c, 3, "table");
+  const int64_t rows = tokens.size(0), vocab = table.size(0), cols = table.size(1);
+  void* ptok = c.check(&tokens, "tokens", tokens.scalar_type(), false, {});
+  int tt;
+  if (c.none(6)) tt = float_type(table, "table", PyExc_TypeError) == FP8MI_F32 ? FP8MI_OUT_F32 : FP8MI_OUT_BF16;
+  else tt = c.format(6) == FP8MI_E4M3 ? FP8MI_OUT_E4M3 : FP8MI_OUT_E5M2;
+  void* ptab = c.check(&table, "table", c.none(6) ? table.scalar_type() : at::kByte, false, {});
+  const at::Tensor& out = matrix(c, 4, "out");
+  const int ot = float_type(out, "out", PyExc_TypeError);
+  void* po = c.mat(4, "out", out.scalar_type(), rows, cols);
+  const float scale = (float)c.number(5);
+  float* sinv = c.scalar(7, "sinv");
+  if (c.elsewhere()) return c.device();
+  return invoke(p_embed, ptok, it, rows, ptab, tt, vocab, cols, sinv, scale, po, ot, c.stream);
+}
+
+// cur stream tokens dy dtable scale base workspace
+PyObject* embed_back(PyObject* const* args, Py_ssize_t n) {
+  Call c(args, n, 8);
+  const at::Tensor& tokens = c.first(2, "tokens", 1);
+  const int it = index_type(tokens, "tokens");
+  const at::Tensor& table = matrix(c, 4, "dtable");
+  const int64_t rows = tokens.size(0), vocab = table.size(0), cols = table.size(1);
+  size_t bytes;
+  void* ptok = c.check(&tokens, "tokens", tokens.scalar_type(), false, {});
+  const int tt = float_type(table, "dtable", PyExc_TypeError);
+  void* ptab = c.check(&table, "dtable", table.scalar_type(), false, {});
+  const at::Tensor& dy = matrix(c, 3, "dy");
+  const int dt = float_type(dy, "dy", PyExc_TypeError);
+  void* pdy = c.mat(3, "dy", dy.scalar_type(), rows, cols);
+  const float scale = (float)c.number(5);
+  void* base = c.mat(6, "base", table.scalar_type(), vocab, cols);
+  void* ws = c.space(7, &bytes);
+  if (c.elsewhere()) return c.device();
+  return invoke(p_embed_back, ptok, it, rows, pdy, dt, vocab, cols, scale, base, ptab, tt, ws, bytes, c.stream);
+}
+
 template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   try {
@@ -430,7 +487,7 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
 // Addresses of the entry points, in the order of the declarations above.
 PyObject* bind(PyObject* const* args, Py_ssize_t n) {
   void* const slots[] = {&p_gemm, &p_gated, &p_fused, &p_norm, &p_norm_blocks, &p_norm_back, &p_act_back, &p_gated_back,
-                         &p_layer, &p_layer_back};
+                         &p_layer, &p_layer_back, &p_embed, &p_embed_back};
   constexpr Py_ssize_t count = sizeof(slots) / sizeof(slots[0]);
   if (n != count) raise(PyExc_TypeError, "%s", "an address for every entry point");
   for (Py_ssize_t i = 0; i < count; ++i) {
@@ -445,7 +502,7 @@ PyObject* bind(PyObject* const* args, Py_ssize_t n) {
 PyMethodDef methods[] = {ENTRY("bind", bind), ENTRY("gemm", gemm), ENTRY("gated", gated), ENTRY("fused", fused),
                          ENTRY("norm", norm), ENTRY("norm_blocks", norm_blocks), ENTRY("norm_back", norm_back),
                          ENTRY("act_back", act_back), ENTRY("gated_back", gated_back), ENTRY("layer", layer),
-                         ENTRY("layer_back", layer_back), {nullptr, nullptr, 0, nullptr}};
+                         ENTRY("layer_back", layer_back), ENTRY("embed", embed), ENTRY("embed_back", embed_back), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fp8mi_marshal", nullptr, -1, methods};
 
 }  // namespace

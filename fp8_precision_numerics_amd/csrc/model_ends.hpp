@@ -21,4 +21,16 @@ hipError_t launch_layernorm_backward(const void* dy, const void* h, const float*
                                      const Dropout& drop, void* dx, void* dbranch, float* dweight, float* dbias,
                                      void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+// `wide`: int64 tokens, else int32.  Table types: an fp8mi_output.
+hipError_t launch_embedding(const void* tokens, bool wide, int64_t rows, const void* table, int ttype, int64_t vocab,
+                            int64_t cols, const float* sinv, float scale, void* out, int otype, hipStream_t stream);
+
+// Workspace of the gradient, and the most tokens that one call sorts.
+constexpr int64_t kMaxTokens = int64_t(1) << 20;
+size_t embedding_workspace(int64_t rows, int64_t cols);
+
+hipError_t launch_embedding_backward(const void* tokens, bool wide, int64_t rows, const void* dy, int dytype,
+                                     int64_t vocab, int64_t cols, float scale, const void* base, void* dtable,
+                                     int ttype, void* workspace, hipStream_t stream);
+
 }  // namespace fp8mi

@@ -626,6 +626,47 @@ FP8MI_API int fp8_layernorm_backward(const void* dy, const void* h, const float*
                            const uint64_t* rng, void* dx, void* dbranch, float* dweight, float* dbias, void* workspace,
                            size_t workspace_bytes, void* stream);
 
+typedef enum { FP8MI_I32 = 0, FP8MI_I64 = 1 } fp8mi_index; /* types of token numbers */
+
+/*
+ * fp8_embedding — rows of a table, scaled.
+ *
+ *   out[t] = round_to_otype(fp32(table[tokens[t]] * scale)), zeros where tokens[t] lies outside [0, vocab)
+ *
+ * tokens     device, [rows] of itype (fp8mi_index), aligned to its size.
+ * table      device, [vocab x cols] of ttype (fp8mi_output): fp32, bf16, or FP8 codes (of a
+ *            head's weight, for instance), whose values are first multiplied with sinv[0].
+ * sinv       device, 1 fp32, the codes' inverse scale; not read for fp32 and bf16 (may be NULL).
+ * scale      host.
+ * out        device, [rows x cols] of otype (fp32 or bf16).
+ * cols must be a multiple of 16, cols <= 2^20; table and out 16-B aligned.  rows may be 0.
+ */
+FP8MI_API int fp8_embedding(const void* tokens, int itype, int64_t rows, const void* table, int ttype, int64_t vocab, int64_t cols,
+                  const float* sinv, float scale, void* out, int otype, void* stream);
+
+/*
+ * fp8_embedding_backward — the table's gradient, by sorted tokens.
+ *
+ *   dtable[v] = round_to_ttype(base[v] + scale * sum over { t : tokens[t] = v } of dy[t])    (fp32 sums)
+ *
+ * tokens     device, [rows] of itype; those outside [0, vocab) take no part.  rows <= 2^20.
+ * dy         device, [rows x cols] of dytype (fp32 or bf16).
+ * base       device, [vocab x cols] of ttype: a gradient to add to (the head's, where the
+ *            two share their weight), or NULL: zeros.  It may be dtable itself; then only the rows of
+ *            tokens that occur are touched.
+ * dtable     device, [vocab x cols] of ttype (fp32 or bf16), all of it overwritten.
+ * workspace  device scratch of at least fp8mi_embedding_workspace(rows, cols) bytes (else
+ *            FP8MI_ERR_WORKSPACE).
+ * cols must be a multiple of 16, cols <= 2^20; dy, base, dtable and workspace 16-B aligned.  The rows are added
+ * in the order of t, in pieces whose ends depend on the tokens alone: the bits repeat.
+ */
+FP8MI_API int fp8_embedding_backward(const void* tokens, int itype, int64_t rows, const void* dy, int dytype, int64_t vocab,
+                           int64_t cols, float scale, const void* base, void* dtable, int ttype, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that fp8_embedding_backward asks for (0: sizes that it refuses, or no tokens). */
+FP8MI_API size_t fp8mi_embedding_workspace(int64_t rows, int64_t cols);
+
 #ifdef __cplusplus
 }
 #endif

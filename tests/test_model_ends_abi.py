@@ -56,7 +56,40 @@ def test_norm_backward_refusals(lib, want, change):
     assert call(lib.fp8_layernorm_backward, NORM_BACK, **change) == want
 
 
-@pytest.mark.parametrize("name", ["layer", "layer_back"])
+EMBED = dict(tokens=P, itype=1, rows=4, table=P, ttype=2, vocab=100, cols=64, sinv=P, scale=1.0, out=P, otype=1, stream=None)
+
+
+@pytest.mark.parametrize("want,change", [
+    (EDTYPE, dict(itype=2)), (EDTYPE, dict(ttype=4)), (EDTYPE, dict(otype=2)), (ESHAPE, dict(rows=-1)), (ESHAPE, dict(vocab=-1)), (ESHAPE, dict(vocab=1 << 31)),
+    (ESHAPE, dict(cols=-16)), (ESHAPE, dict(cols=(1 << 20) + 16)), (EALIGN, dict(cols=72)), (ENULL, dict(tokens=None)), (ENULL, dict(table=None)),
+    (ENULL, dict(out=None)), (ENULL, dict(sinv=None)), (EALIGN, dict(tokens=P4)), (EALIGN, dict(tokens=ctypes.c_void_p(0x10002), itype=0)), (EALIGN, dict(table=P8)),
+    (EALIGN, dict(out=P8)), (OK, dict(rows=0, tokens=None)), (OK, dict(cols=0))])
+def test_embedding_refusals(lib, want, change):
+    assert call(lib.fp8_embedding, EMBED, **change) == want
+
+
+EMBED_BACK = dict(tokens=P, itype=0, rows=40, dy=P, dytype=1, vocab=100, cols=64, scale=1.0, base=None, dtable=P, ttype=0, ws=P, ws_bytes=2 * 160 + 3 * 2 * 64 * 4,
+                  stream=None)
+
+
+@pytest.mark.parametrize("want,change", [
+    (EDTYPE, dict(itype=-1)), (EDTYPE, dict(dytype=2)), (EDTYPE, dict(ttype=3)), (ESHAPE, dict(rows=-1)), (ESHAPE, dict(rows=(1 << 20) + 1)), (ESHAPE, dict(vocab=-1)),
+    (ESHAPE, dict(cols=(1 << 20) + 16)), (EALIGN, dict(cols=24)), (ENULL, dict(tokens=None)), (ENULL, dict(dy=None)), (ENULL, dict(dtable=None)), (ENULL, dict(ws=None)),
+    (EALIGN, dict(dy=P8)), (EALIGN, dict(base=P8)), (EALIGN, dict(dtable=P8)), (EALIGN, dict(ws=P8)), (EALIGN, dict(tokens=ctypes.c_void_p(0x10002))),
+    (EWS, dict(ws_bytes=2 * 160 + 3 * 2 * 64 * 4 - 1)), (OK, dict(vocab=0)), (OK, dict(cols=0)), (OK, dict(rows=0, base=P))])
+def test_embedding_backward_refusals(lib, want, change):
+    assert call(lib.fp8_embedding_backward, EMBED_BACK, **change) == want
+
+
+def test_embedding_workspace():
+    """Keys and places of 4 bytes a token (twice where blocks of 8192 are merged), two partial rows for each chunk of 16 (or a 4096th of the tokens, up to eights)."""
+    assert fm.embedding_workspace_bytes(0, 64) == 0 and fm.embedding_workspace_bytes(-1, 64) == 0 and fm.embedding_workspace_bytes((1 << 20) + 1, 64) == 0
+    assert fm.embedding_workspace_bytes(16, 64) == 2 * 64 and fm.embedding_workspace_bytes(17, 64) == 2 * 80 + 2 * 2 * 64 * 4
+    assert fm.embedding_workspace_bytes(8192, 64) == 2 * 32768 + 512 * 512 and fm.embedding_workspace_bytes(8193, 64) == 4 * 32784 + 513 * 512
+    assert fm.embedding_workspace_bytes(1 << 20, 64) == 4 * (4 << 20) + 4096 * 512
+
+
+@pytest.mark.parametrize("name", ["layer", "layer_back", "embed", "embed_back"])
 def test_a_wrong_number_of_arguments_is_a_type_error(name):
     module = binding._MODULE or binding._load_module()
     with pytest.raises(TypeError):
