@@ -22,7 +22,8 @@ __all__ = ["E4M3", "E5M2", "F32", "BF16", "ACCUM_EXACT", "ACCUM_MFMA_FP8", "QUAN
            "fp8_quantize_update_noalloc", "fp8_rmsnorm_quantize", "fp8_rmsnorm_quantize_blockwise",
            "fp8_rmsnorm_backward", "fp8_gemm_gated", "fp8_gemm_fused", "fp8_act_backward", "fp8_gated_backward",
            "fp8_layernorm_quantize", "fp8_layernorm_backward", "fp8_embedding", "fp8_embedding_backward",
-           "embedding_workspace_bytes", "EXPORTED_SYMBOLS"]
+           "embedding_workspace_bytes", "fp8_vocab_cross_entropy", "fp8_vocab_cross_entropy_backward",
+           "vocab_workspace_bytes", "EXPORTED_SYMBOLS"]
 
 E4M3, E5M2 = 0, 1
 F32, BF16 = 0, 1
@@ -38,7 +39,8 @@ EXPORTED_SYMBOLS = ("fp8mi_status_string", "fp8mi_version", "fp8_quantize", "fp8
                     "fp8_quantize_update", "fp8_quantize_update_noalloc", "fp8_rmsnorm_quantize",
                     "fp8_rmsnorm_quantize_blockwise", "fp8_rmsnorm_backward", "fp8_gemm_gated", "fp8_gemm_fused",
                     "fp8_act_backward", "fp8_gated_backward", "fp8_layernorm_quantize", "fp8_layernorm_backward",
-                    "fp8_embedding", "fp8_embedding_backward", "fp8mi_embedding_workspace")
+                    "fp8_embedding", "fp8_embedding_backward", "fp8mi_embedding_workspace",
+                    "fp8_vocab_cross_entropy", "fp8_vocab_cross_entropy_backward", "fp8mi_vocab_workspace")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
@@ -121,9 +123,15 @@ def load_library():
     lib.fp8_embedding_backward.argtypes = [vp, ci, i64, vp, ci, i64, i64, cf, vp, vp, ci, vp, sz, vp]
     lib.fp8mi_embedding_workspace.argtypes = [i64, i64]
     lib.fp8mi_embedding_workspace.restype = sz
+    lib.fp8_vocab_cross_entropy.argtypes = [vp, ci, vp, ci, i64, i64, i64, vp, vp, vp, ci, vp, vp, ci, vp, sz, vp]
+    lib.fp8_vocab_cross_entropy_backward.argtypes = [vp, ci, vp, ci, i64, i64, i64, vp, vp, vp, ci, vp, vp, ci, vp, vp,
+                                                     vp, ci, vp, ci, vp, vp, ci, vp, sz, vp]
+    lib.fp8mi_vocab_workspace.argtypes = [i64, i64, i64, i64]
+    lib.fp8mi_vocab_workspace.restype = sz
     for name in ("fp8_rmsnorm_quantize", "fp8_rmsnorm_quantize_blockwise", "fp8_rmsnorm_backward", "fp8_gemm_gated",
                  "fp8_gemm_fused", "fp8_act_backward", "fp8_gated_backward", "fp8_layernorm_quantize",
-                 "fp8_layernorm_backward", "fp8_embedding", "fp8_embedding_backward"):
+                 "fp8_layernorm_backward", "fp8_embedding", "fp8_embedding_backward", "fp8_vocab_cross_entropy",
+                 "fp8_vocab_cross_entropy_backward"):
         getattr(lib, name).restype = ci
     _LIB = lib
     return lib
@@ -205,7 +213,8 @@ def _call(name, status):
 # feed-forward operators, those at the ends of a model) are marshalled by the extension module of csrc/marshal.cpp.
 _MARSHALLED = ("fp8_gemm", "fp8_gemm_gated", "fp8_gemm_fused", "fp8_rmsnorm_quantize", "fp8_rmsnorm_quantize_blockwise",
                "fp8_rmsnorm_backward", "fp8_act_backward", "fp8_gated_backward", "fp8_layernorm_quantize",
-               "fp8_layernorm_backward", "fp8_embedding", "fp8_embedding_backward")
+               "fp8_layernorm_backward", "fp8_embedding", "fp8_embedding_backward", "fp8_vocab_cross_entropy",
+               "fp8_vocab_cross_entropy_backward")
 _MODULE = None
 # The current stream's handle and device without building the Python objects
 # around them (about 2 us of a small call).
@@ -648,3 +657,36 @@ def fp8_embedding_backward(tokens, dy, dtable, scale=1.0, base=None, workspace=N
     status = (_MODULE or _load_module()).embed_back(index, handle, tokens, dy, dtable, scale, base, workspace)
     if status:
         _settle(status, fp8_embedding_backward, tokens, dy, dtable, scale, base, workspace, stream)
+
+
+def vocab_workspace_bytes(tokens: int, vocab: int, hidden: int, pieces: int = 1) -> int:
+    """Workspace with which the vocabulary's cross entropy, forward and backward, takes the vocabulary in at most so
+    many pieces (0: the least that it accepts)."""
+    return int(load_library().fp8mi_vocab_workspace(tokens, vocab, hidden, pieces))
+
+
+def fp8_vocab_cross_entropy(x, fx, w, fw, sinv_x, sinv_w, targets, loss, lse, accum="exact", workspace=None,
+                            stream=None) -> None:
+    """loss[m] = lse[m] - z[m, targets[m]], lse = log sum exp z, z = (X · Wᵀ) · sinv_x · sinv_w, no logit stored.
+
+    x: codes [M x K]; w: codes [V x K]; targets: int32 or int64 [M] (a row whose target lies outside [0, V) has loss 0);
+    loss, lse: fp32 [M], either may be None; accum as for fp8_gemm; workspace: uint8, vocab_workspace_bytes tells."""
+    index, handle = _where(stream)
+    status = (_MODULE or _load_module()).vocab(index, handle, x, fx, w, fw, sinv_x, sinv_w, targets, loss, lse, accum,
+        workspace)
+    if status:
+        _settle(status, fp8_vocab_cross_entropy, x, fx, w, fw, sinv_x, sinv_w, targets, loss, lse, accum, workspace,
+                stream)
+
+
+def fp8_vocab_cross_entropy_backward(x, fx, w, fw, sinv_x, sinv_w, targets, lse, dloss, fmt, scale, scale_inv, dx=None,
+                                     dw=None, amax=None, sat=None, accum="exact", workspace=None, stream=None) -> None:
+    """Gradients of sum(dloss * loss): d = dloss · (exp(z - lse) - [column = target]) as codes of format fmt with the
+    given scale, dx [M x K] = codes · W, dw [V x K] = codesᵀ · X (fp32 or bf16; either may be None), amax and sat of d.
+    lse: the forward's; dloss: fp32 [M]; the other arguments as for fp8_vocab_cross_entropy."""
+    index, handle = _where(stream)
+    status = (_MODULE or _load_module()).vocab_back(index, handle, x, fx, w, fw, sinv_x, sinv_w, targets, lse, dloss,
+        fmt, scale, scale_inv, dx, dw, amax, sat, accum, workspace)
+    if status:
+        _settle(status, fp8_vocab_cross_entropy_backward, x, fx, w, fw, sinv_x, sinv_w, targets, lse, dloss, fmt,
+                scale, scale_inv, dx, dw, amax, sat, accum, workspace, stream)

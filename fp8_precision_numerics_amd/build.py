@@ -33,7 +33,7 @@ MARSHALPATH = os.path.join(LIBDIR, "_fp8mi_marshal.so")
 BUILDDIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["api.hip", "quantize.hip", "amax_update.hip", "gemm.hip", "gemm_requant.hip", "grouped_gemm.hip", "allreduce.hip", "mx.hip", "rms_norm.hip", "act_backward.hip",
-           "gemm_fused.hip", "gemm_gated.hip", "gemm_few_rows.hip", "layer_norm.hip", "embedding.hip", "api_model_ends.hip"]
+           "gemm_fused.hip", "gemm_gated.hip", "gemm_few_rows.hip", "layer_norm.hip", "embedding.hip", "vocab_loss.hip", "vocab_grad.hip", "vocab_product.hip", "api_model_ends.hip"]
 ARCH = "gfx950"
 FLAGS = ["-O3", "-std=c++17", "-fPIC", "-fvisibility=hidden", f"--offload-arch={ARCH}",
          "-mcode-object-version=5",

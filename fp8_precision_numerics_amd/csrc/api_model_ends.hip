@@ -5,6 +5,7 @@
 #include "api_common.hpp"
 #include "device_common.hpp"
 #include "model_ends.hpp"
+#include "vocab.hpp"
 
 using namespace fp8mi;
 
@@ -27,6 +28,25 @@ constexpr int64_t kMaxEmbedCols = int64_t(1) << 20;  // workgroups a row, of whi
 
 bool index_ok(int t) { return t == FP8MI_I32 || t == FP8MI_I64; }
 bool index_aligned(const void* p, int t) { return (reinterpret_cast<uintptr_t>(p) & (t == FP8MI_I64 ? 7u : 3u)) == 0; }
+
+constexpr int64_t kMaxVocabK = int64_t(1) << 22;  // 256 rows of a piece in a 31-bit offset
+
+// What the loss's two entry points share, M != 0.
+int check_vocab(const uint8_t* x, int fx, const uint8_t* w, int fw, int64_t M, int64_t V, int64_t K, const float* sinv_x,
+                const float* sinv_w, const void* targets, int itype, int accum, const void* workspace) {
+  if (!fmt_ok(fx) || !fmt_ok(fw)) return FP8MI_ERR_FORMAT;
+  if (!index_ok(itype)) return FP8MI_ERR_DTYPE;
+  if (!accum_ok(accum)) return FP8MI_ERR_ACCUM;
+  if (M < 0 || V < 1 || K <= 0 || M > kMaxGemmK - 16 || V > kMaxDim || K > kMaxVocabK) return FP8MI_ERR_SHAPE;
+  if (!dims_ok(M, K) || !dims_ok(V, K) || M * K > kMaxBufferBytes) return FP8MI_ERR_SHAPE;
+  if (((M + 63) / 64) * ((V + 127) / 128 + 1) > kMaxDim) return FP8MI_ERR_SHAPE;
+  if ((K & 15) != 0) return FP8MI_ERR_ALIGN;
+  if (workspace && !aligned16(workspace)) return FP8MI_ERR_ALIGN;
+  if (M == 0) return FP8MI_OK;
+  if (!x || !w || !sinv_x || !sinv_w || !targets || !workspace) return FP8MI_ERR_NULL;
+  if (!aligned16(x) || !aligned16(w) || !index_aligned(targets, itype)) return FP8MI_ERR_ALIGN;
+  return FP8MI_OK;
+}
 
 }  // namespace
 
@@ -119,6 +139,52 @@ int fp8_embedding_backward(const void* tokens, int itype, int64_t rows, const vo
   if (dev != FP8MI_OK) return dev;
   return launched(launch_embedding_backward(tokens, itype == FP8MI_I64, rows, dy, dytype, vocab, cols, scale, base, dtable, ttype, workspace,
                                             (hipStream_t)stream));
+}
+
+size_t fp8mi_vocab_workspace(int64_t M, int64_t V, int64_t K, int64_t pieces) {
+  if (M < 0 || V < 1 || K <= 0 || M > kMaxGemmK - 16 || V > kMaxDim || K > kMaxVocabK || pieces < 0) return 0;
+  return vocab_workspace(M, V, K, pieces);
+}
+
+int fp8_vocab_cross_entropy(const uint8_t* x, int fx, const uint8_t* w, int fw, int64_t M, int64_t V, int64_t K,
+                            const float* sinv_x, const float* sinv_w, const void* targets, int itype, float* loss,
+                            float* lse, int accum, void* workspace, size_t workspace_bytes, void* stream) {
+  const int bad = check_vocab(x, fx, w, fw, M, V, K, sinv_x, sinv_w, targets, itype, accum, workspace);
+  if (bad != FP8MI_OK) return bad;
+  if (M == 0) return FP8MI_OK;
+  if (!loss && !lse) return FP8MI_ERR_NULL;
+  if (workspace_bytes < vocab_loss_bytes(M, V < kPieceCols ? V : kPieceCols)) return FP8MI_ERR_WORKSPACE;
+  const int dev = check_device();
+  if (dev != FP8MI_OK) return dev;
+  const VocabOperands o{x, w, fx, fw, sinv_x, sinv_w, M, K};
+  return launched(launch_vocab_cross_entropy(o, V, Targets{targets, itype == FP8MI_I64}, loss, lse, accum, workspace,
+                                             workspace_bytes, (hipStream_t)stream));
+}
+
+int fp8_vocab_cross_entropy_backward(const uint8_t* x, int fx, const uint8_t* w, int fw, int64_t M, int64_t V, int64_t K,
+                                     const float* sinv_x, const float* sinv_w, const void* targets, int itype,
+                                     const float* lse, const float* dloss, int fmt, const float* scale,
+                                     const float* scale_inv, void* dx, int dxtype, void* dw, int dwtype, float* amax,
+                                     unsigned long long* sat, int accum, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
+  if (!fmt_ok(fmt)) return FP8MI_ERR_FORMAT;
+  if ((dx && !dtype_ok(dxtype)) || (dw && !dtype_ok(dwtype))) return FP8MI_ERR_DTYPE;
+  const int bad = check_vocab(x, fx, w, fw, M, V, K, sinv_x, sinv_w, targets, itype, accum, workspace);
+  if (bad != FP8MI_OK) return bad;
+  if (!aligned16(dx) || !aligned16(dw)) return FP8MI_ERR_ALIGN;
+  if (M == 0) {
+    if (!dw && !amax && !sat) return FP8MI_OK;
+  } else {
+    if (!dx && !dw) return FP8MI_ERR_NULL;
+    if (!lse || !dloss || !scale || !scale_inv) return FP8MI_ERR_NULL;
+    if (workspace_bytes < vocab_workspace(M, V, K, 0)) return FP8MI_ERR_WORKSPACE;
+  }
+  const int dev = check_device();
+  if (dev != FP8MI_OK) return dev;
+  const VocabOperands o{x, w, fx, fw, sinv_x, sinv_w, M, K};
+  return launched(launch_vocab_cross_entropy_backward(o, V, Targets{targets, itype == FP8MI_I64}, lse, dloss, fmt, scale,
+                                                      scale_inv, dx, dxtype, dw, dwtype, amax, sat, accum, workspace,
+                                                      workspace_bytes, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -353,8 +353,6 @@ int64_t chunk_size(int64_t rows) {
   return c < 16 ? 16 : (c + 7) / 8 * 8;
 }
 
-int64_t up16(int64_t bytes) { return (bytes + 15) & ~int64_t(15); }
-
 template <int TT>
 hipError_t lookup_run(const LookupArgs& a, int otype, unsigned grid, hipStream_t st) {
   if (otype == kBF16) hipLaunchKernelGGL((lookup_kernel<TT, kBF16>), dim3(grid), dim3(kLookNT), 0, st, a);
@@ -370,7 +368,18 @@ hipError_t sums_run(const SumArgs& a, int dytype, unsigned grid, hipStream_t st)
   return hipGetLastError();
 }
 
+int64_t up16(int64_t bytes) { return (bytes + 15) & ~int64_t(15); }
+
 }  // namespace
+
+hipError_t launch_fill_rows(const void* base, void* to, int64_t words, hipStream_t stream) {
+  int64_t groups = (words + 1023) / 1024;
+  if (groups > persistent_groups(8)) groups = persistent_groups(8);
+  if (groups == 0) return hipSuccess;
+  hipLaunchKernelGGL(fill_rows_kernel, dim3((unsigned)groups), dim3(256), 0, stream, reinterpret_cast<const uint4*>(base),
+                     reinterpret_cast<uint4*>(to), words);
+  return hipGetLastError();
+}
 
 hipError_t launch_embedding(const void* tokens, bool wide, int64_t rows, const void* table, int ttype, int64_t vocab,
                             int64_t cols, const float* sinv, float scale, void* out, int otype, hipStream_t stream) {
@@ -397,11 +406,7 @@ hipError_t launch_embedding_backward(const void* tokens, bool wide, int64_t rows
                                      int ttype, void* workspace, hipStream_t stream) {
   const int64_t words = vocab * (cols / 8) * (ttype == kBF16 ? 1 : 2);
   if (base != dtable) {
-    int64_t groups = (words + 1023) / 1024;
-    if (groups > persistent_groups(8)) groups = persistent_groups(8);
-    hipLaunchKernelGGL(fill_rows_kernel, dim3((unsigned)groups), dim3(256), 0, stream,
-                       reinterpret_cast<const uint4*>(base), reinterpret_cast<uint4*>(dtable), words);
-    const hipError_t e = hipGetLastError();
+    const hipError_t e = launch_fill_rows(base, dtable, words, stream);
     if (e != hipSuccess) return e;
   }
   if (rows == 0) return hipSuccess;

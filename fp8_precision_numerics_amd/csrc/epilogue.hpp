@@ -2,6 +2,7 @@
 //
 //   fused   z = c + bias;   y = act(z) + residual
 //   gated   y = act(c_gate) * c_up
+//   product y = c + add
 //
 // with c the fp32 GEMM result already times sinv_a * sinv_b.  z (gated: both
 // projections) may be kept in bf16 for the gradient; it is rounded from the fp32
@@ -41,9 +42,24 @@ template <class T>
 struct is_epilogue {
   static constexpr bool value = false;
 };
-// The two epilogues as kernel arguments of their own types.
+// Epilogues that take the accumulators of a whole tile (gemm_kernel.hpp) specialise this.
+template <class T>
+struct is_tile_epilogue {
+  static constexpr bool value = false;
+};
+// The epilogues as kernel arguments of their own types.
 struct FusedEpi : EpiArgs {};
 struct GatedEpi : EpiArgs {};
+// A product whose A rows are padded: lda bytes apart, zeros from K to the next multiple of 16
+// (K itself may be any number), added to the fp32 matrix `add` [M x N] (may be null, or y where y is fp32).
+struct ProductEpi : EpiArgs {
+  const float* add;
+  int lda;
+};
+template <>
+struct is_epilogue<ProductEpi> {
+  static constexpr bool value = true;
+};
 template <>
 struct is_epilogue<FusedEpi> {
   static constexpr bool value = true;
@@ -181,6 +197,18 @@ __device__ __forceinline__ uint4 load_bf16x8(const uint16_t* p, bool vec, int le
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Eight fp32 values, likewise (to is zero on entry).
+__device__ __forceinline__ void load_f32x8(const float* p, bool vec, int left, v4f* to) {
+  if (vec) {
+    to[0] = reinterpret_cast<const v4f*>(p)[0];
+    to[1] = reinterpret_cast<const v4f*>(p)[1];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < left) to[e >> 2][e & 3] = p[e];
+  }
+}
+
 // A workgroup's amax and count into the outputs (cleared beforehand): the waves meet in
 // `scratch` (LDS, two words a wave, free of other use), then one device-scope atomic a
 // workgroup, skipped where it would change nothing (the outputs only grow).  One
@@ -228,7 +256,8 @@ __device__ __forceinline__ void clear_epilogue_stats(const EpiArgs& a) {
 // 105 us against 84).  The next row's values are read from LDS while the present row is
 // worked on (8192 x 2 x 16384 x 4096 exact: 1552 against 1474 us, a plain GEMM of that
 // size beside them 1511 and 1451).
-template <int BN, int NT, int PASS, int PAIR, class TW>
+// PRODUCT: a ProductEpi's values of `add` are requested one row ahead, in the residual's place.
+template <int BN, int NT, int PASS, int PAIR, bool PRODUCT, class TW>
 struct EpiPass {
   static constexpr bool GATED = PAIR != 0;
   static constexpr int CPR = (GATED ? BN / 2 : BN) / 8;  // chunks per row
@@ -242,7 +271,9 @@ struct EpiPass {
   float bias[8];
   uint4 res[2];
   float scale;
-  __device__ __forceinline__ EpiPass(const EpiArgs& a_, int64_t M_, int64_t N_, int64_t m_base, int64_t n_base, int t)
+  const float* add = nullptr;
+  template <class ARGS>
+  __device__ __forceinline__ EpiPass(const ARGS& a_, int64_t M_, int64_t N_, int64_t m_base, int64_t n_base, int t)
       : a(a_), M(M_), N(N_), m0(m_base) {
     const int c = t % CPR;
     r0 = t / CPR;
@@ -252,18 +283,25 @@ struct EpiPass {
     left = n < N ? (int)(N - n < 8 ? N - n : 8) : 0;
     vec = (N & 7) == 0;
     uint4 b = make_uint4(0u, 0u, 0u, 0u);
-    if constexpr (!GATED) {
+    if constexpr (!GATED && !PRODUCT) {
       if (a.bias && left) b = load_bf16x8(a.bias + n, vec, left);
     }
+    if constexpr (PRODUCT) add = a_.add;
     unpack_bf16x8(b, bias);
     res[0] = res[1] = make_uint4(0u, 0u, 0u, 0u);
     scale = (a.out == kYE4M3 || a.out == kYE5M2) ? *a.out_scale : 1.0f;
   }
   __device__ __forceinline__ void request(int pass_row, int i, uint4* to) const {
-    if constexpr (!GATED) {
+    if constexpr (!GATED && !PRODUCT) {
       const int64_t m = m0 + pass_row + r0 + i * SWEEP;
       if (a.residual && left && i < ROWS && m < M) *to = load_bf16x8(a.residual + m * N + n, vec, left);
     }
+  }
+  // Row i's eight values of `add`, zeros without it.
+  __device__ __forceinline__ void request_add(int pass_row, int i, v4f* to) const {
+    to[0] = to[1] = (v4f){0.f, 0.f, 0.f, 0.f};
+    const int64_t m = m0 + pass_row + r0 + i * SWEEP;
+    if (add && left && i < ROWS && m < M) load_f32x8(add + m * N + n, vec, left, to);
   }
   __device__ __forceinline__ void prefetch(int pass_row) {
     if (a.split > 1) return;
@@ -308,6 +346,8 @@ struct EpiPass {
     float nv[8], nu[GATED ? 8 : 1];
     take(tw, r0, col, nv);
     if constexpr (GATED) take(tw, r0, col + PAIR, nu);
+    v4f next[2];
+    if constexpr (PRODUCT) request_add(pass_row, 0, next);
 #pragma unroll 1
     for (int i = 0; i < ROWS; ++i) {
       const int r = r0 + i * SWEEP;
@@ -319,9 +359,15 @@ struct EpiPass {
         v[e] = nv[e];
         if constexpr (GATED) up[e] = nu[e];
       }
-      unpack_bf16x8(res[0], rs);
-      res[0] = res[1];
-      request(pass_row, i + 2, &res[1]);
+      if constexpr (PRODUCT) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) rs[e] = next[e >> 2][e & 3];
+        request_add(pass_row, i + 1, next);
+      } else {
+        unpack_bf16x8(res[0], rs);
+        res[0] = res[1];
+        request(pass_row, i + 2, &res[1]);
+      }
       const int rn = i + 1 < ROWS ? r + SWEEP : r;
       take(tw, rn, col, nv);
       if constexpr (GATED) take(tw, rn, col + PAIR, nu);

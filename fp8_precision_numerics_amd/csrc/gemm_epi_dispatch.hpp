@@ -11,10 +11,11 @@ namespace fp8mi {
 
 // The sums of a split product's parts, scaled, through the epilogue: eight columns
 // of a row a thread.
-template <bool GATED>
-__global__ __launch_bounds__(256) void epilogue_partials_kernel(EpiArgs a, int64_t M, int64_t N,
+template <class EPI>
+__global__ __launch_bounds__(256) void epilogue_partials_kernel(EPI a, int64_t M, int64_t N,
                                                                const float* __restrict__ sinv_a,
                                                                const float* __restrict__ sinv_b) {
+  constexpr bool GATED = std::is_same<EPI, GatedEpi>::value, PRODUCT = std::is_same<EPI, ProductEpi>::value;
   const int64_t cpr = (N + 7) / 8, total = M * cpr, ld = GATED ? 2 * N : N;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   LaneStats st;
@@ -26,7 +27,7 @@ __global__ __launch_bounds__(256) void epilogue_partials_kernel(EpiArgs a, int64
     const float sc = sinv_a[0] * sinv_b[0];
     float v[GATED ? 2 : 1][8], bias[8], res[8];
     uint4 bb = make_uint4(0u, 0u, 0u, 0u), rr = bb;
-    if constexpr (!GATED) {
+    if constexpr (!GATED && !PRODUCT) {
       if (a.bias) bb = load_bf16x8(a.bias + n, vec, left);
       if (a.residual) rr = load_bf16x8(a.residual + m * N + n, vec, left);
     }
@@ -59,6 +60,12 @@ __global__ __launch_bounds__(256) void epilogue_partials_kernel(EpiArgs a, int64
       for (int e = 0; e < 8; ++e) v[p][e] *= sc;
     unpack_bf16x8(bb, bias);
     unpack_bf16x8(rr, res);
+    if constexpr (PRODUCT) {
+      v4f sum[2] = {(v4f){0.f, 0.f, 0.f, 0.f}, (v4f){0.f, 0.f, 0.f, 0.f}};
+      if (a.add) load_f32x8(a.add + m * N + n, vec, left, sum);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) res[e] = sum[e >> 2][e & 3];
+    }
     const float scale = (a.out == kYE4M3 || a.out == kYE5M2) ? *a.out_scale : 1.0f;
     epilogue8<GATED>(a, v[0], v[GATED ? 1 : 0], bias, res, m, n, N, vec, left, scale, st);
   }
@@ -67,7 +74,7 @@ __global__ __launch_bounds__(256) void epilogue_partials_kernel(EpiArgs a, int64
 
 // `split` > 1: that many workgroups share a tile's K (no part is empty) over
 // epi.partials, and a second kernel finishes.
-template <int BM, int BN, int WM, int WN, int FA, int FB, int MODE, class EPI, int STAGES = 2>
+template <int BM, int BN, int WM, int WN, int FA, int FB, int MODE, class EPI, int STAGES = 2, bool BT = false>
 inline hipError_t epi_run(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, int64_t K, const float* sa,
                           const float* sb, EPI epi, int split, hipStream_t st) {
   constexpr bool GATED = std::is_same<EPI, GatedEpi>::value;
@@ -81,13 +88,13 @@ inline hipError_t epi_run(const uint8_t* A, const uint8_t* B, int64_t M, int64_t
     const hipError_t e = launch_clear_stats(reinterpret_cast<float*>(epi.amax_bits), epi.sat, st);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((gemm_kernel<BM, BN, WM, WN, FA, FB, kF32, MODE, false, EPI, STAGES>),
+  hipLaunchKernelGGL((gemm_kernel<BM, BN, WM, WN, FA, FB, kF32, MODE, BT, EPI, STAGES>),
                      dim3((unsigned)(tiles_m * tiles_n * epi.split)), dim3(64 * WM * WN), 0, st, A, B, (int)M, (int)N,
                      (int)K, sa, sb, (void*)nullptr, tiles_m, tiles_n, group_m, epi, MxScales{nullptr, nullptr});
   if (epi.split > 1) {
     const int64_t chunks = M * ((N + 7) / 8);
-    hipLaunchKernelGGL(epilogue_partials_kernel<GATED>, dim3((unsigned)((chunks + 255) / 256)), dim3(256), 0, st,
-                       static_cast<const EpiArgs&>(epi), M, N, sa, sb);
+    hipLaunchKernelGGL(epilogue_partials_kernel<EPI>, dim3((unsigned)((chunks + 255) / 256)), dim3(256), 0, st, epi, M,
+                       N, sa, sb);
   }
   return hipGetLastError();
 }

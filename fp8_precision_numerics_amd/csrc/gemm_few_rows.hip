@@ -29,6 +29,7 @@
 #include "gemm_few_rows.hpp"
 #include "gemm_tile.hpp"
 #include "launch.hpp"
+#include "vocab_epilogue.hpp"
 
 namespace fp8mi {
 namespace {
@@ -62,11 +63,12 @@ __device__ __forceinline__ v8bf widen_part(const Slice& s, int i) {
   return (i & 1) ? widen8_scaled_bf16<F>(g.z, g.w, 1.0f) : widen8_scaled_bf16<F>(g.x, g.y, 1.0f);
 }
 
-template <int FA, int FB, bool GATED>
+// EPI: EpiArgs, or LossEpi (whose finish_rows takes the sums).
+template <int FA, int FB, bool GATED, class EPI>
 __global__ __launch_bounds__(64 * kWavesFew) void gemm_few_rows_kernel(const uint8_t* __restrict__ A,
                                                                       const uint8_t* __restrict__ B, int M, int N,
                                                                       int K, const float* __restrict__ sinv_a,
-                                                                      const float* __restrict__ sinv_b, EpiArgs epi,
+                                                                      const float* __restrict__ sinv_b, EPI epi,
                                                                       int split) {
   constexpr int NW = kWavesFew;
   constexpr int NB = GATED ? 2 : 1;
@@ -144,59 +146,72 @@ __global__ __launch_bounds__(64 * kWavesFew) void gemm_few_rows_kernel(const uin
   for (int j = 0; j < NB; ++j) *reinterpret_cast<v4f*>(&red[w][j][rl][4 * kq]) = acc[j];
   __syncthreads();
 
-  // 8 columns a thread: of each tile, 16 rows of two chunks.
-  LaneStats st;
-  for (int t = threadIdx.x; t < tiles_wg * 32; t += 64 * NW) {
-    const int slot = t / 32, m = (t >> 1) & 15;
-    const int64_t n = ((int64_t)blockIdx.x * tiles_wg + slot) * 16 + (t & 1) * 8;
-    const int left = n < N ? (int)(N - n < 8 ? N - n : 8) : 0;
-    const bool vec = (N & 7) == 0;
-    if (m < M && left) {
-      const float sc = sinv_a[0] * sinv_b[0];
-      float v[NB][8], bias[8], res[8];
-      uint4 bb = make_uint4(0u, 0u, 0u, 0u), rr = bb;
-      if constexpr (!GATED) {
-        if (epi.bias) bb = load_bf16x8(epi.bias + n, vec, left);
-        if (epi.residual) rr = load_bf16x8(epi.residual + (int64_t)m * N + n, vec, left);
+  if constexpr (is_tile_epilogue<EPI>::value) {
+    epi.template finish_rows<NW>(&red[0][0], split, tiles_wg, sinv_a[0] * sinv_b[0], M, N);
+  } else {
+    // 8 columns a thread: of each tile, 16 rows of two chunks.
+    LaneStats st;
+    for (int t = threadIdx.x; t < tiles_wg * 32; t += 64 * NW) {
+      const int slot = t / 32, m = (t >> 1) & 15;
+      const int64_t n = ((int64_t)blockIdx.x * tiles_wg + slot) * 16 + (t & 1) * 8;
+      const int left = n < N ? (int)(N - n < 8 ? N - n : 8) : 0;
+      const bool vec = (N & 7) == 0;
+      if (m < M && left) {
+        const float sc = sinv_a[0] * sinv_b[0];
+        float v[NB][8], bias[8], res[8];
+        uint4 bb = make_uint4(0u, 0u, 0u, 0u), rr = bb;
+        if constexpr (!GATED) {
+          if (epi.bias) bb = load_bf16x8(epi.bias + n, vec, left);
+          if (epi.residual) rr = load_bf16x8(epi.residual + (int64_t)m * N + n, vec, left);
+        }
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[j][e] = 0.0f;
+          for (int q = slot * split; q < (slot + 1) * split; ++q)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const v4f p = *reinterpret_cast<const v4f*>(&red[q][j][m][(t & 1) * 8 + 4 * h]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) v[j][4 * h + e] += p[e];
+            }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[j][e] *= sc;
+        }
+        unpack_bf16x8(bb, bias);
+        unpack_bf16x8(rr, res);
+        const float scale = (epi.out == kYE4M3 || epi.out == kYE5M2) ? *epi.out_scale : 1.0f;
+        epilogue8<GATED>(epi, v[0], v[NB - 1], bias, res, m, n, N, vec, left, scale, st);
       }
-#pragma unroll
-      for (int j = 0; j < NB; ++j) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[j][e] = 0.0f;
-        for (int q = slot * split; q < (slot + 1) * split; ++q)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const v4f p = *reinterpret_cast<const v4f*>(&red[q][j][m][(t & 1) * 8 + 4 * h]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[j][4 * h + e] += p[e];
-          }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[j][e] *= sc;
-      }
-      unpack_bf16x8(bb, bias);
-      unpack_bf16x8(rr, res);
-      const float scale = (epi.out == kYE4M3 || epi.out == kYE5M2) ? *epi.out_scale : 1.0f;
-      epilogue8<GATED>(epi, v[0], v[NB - 1], bias, res, m, n, N, vec, left, scale, st);
     }
+    if (epi.amax_bits || epi.sat) publish_epilogue_stats(epi, st, reinterpret_cast<uint32_t*>(red));
   }
-  if (epi.amax_bits || epi.sat) publish_epilogue_stats(epi, st, reinterpret_cast<uint32_t*>(red));
 }
 
-template <int FA, int FB, bool GATED>
-hipError_t few_run(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, int64_t K, const float* sa,
-                   const float* sb, const EpiArgs& epi, hipStream_t st) {
+// Waves that share a tile's K: as many as give the chip about 8 a compute unit.
+int few_split(int64_t N) {
   const int64_t tiles = (N + 15) / 16;
   int split = 1;
   while (split < kWavesFew && tiles * split < persistent_groups(8)) split *= 2;
-  const int tiles_wg = kWavesFew / split;
-  hipLaunchKernelGGL((gemm_few_rows_kernel<FA, FB, GATED>), dim3((unsigned)((tiles + tiles_wg - 1) / tiles_wg)),
-                     dim3(64 * kWavesFew), 0, st, A, B, (int)M, (int)N, (int)K, sa, sb, epi, split);
+  return split;
+}
+
+int few_groups(int64_t N) {
+  const int64_t tiles = (N + 15) / 16, tiles_wg = kWavesFew / few_split(N);
+  return (int)((tiles + tiles_wg - 1) / tiles_wg);
+}
+
+template <int FA, int FB, bool GATED, class EPI>
+hipError_t few_run(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, int64_t K, const float* sa,
+                   const float* sb, const EPI& epi, hipStream_t st) {
+  hipLaunchKernelGGL((gemm_few_rows_kernel<FA, FB, GATED, EPI>), dim3((unsigned)few_groups(N)), dim3(64 * kWavesFew), 0,
+                     st, A, B, (int)M, (int)N, (int)K, sa, sb, epi, few_split(N));
   return hipGetLastError();
 }
 
-template <bool GATED>
+template <bool GATED, class EPI>
 hipError_t few_fmt(const uint8_t* A, int fa, const uint8_t* B, int fb, int64_t M, int64_t N, int64_t K,
-                   const float* sa, const float* sb, const EpiArgs& epi, hipStream_t st) {
+                   const float* sa, const float* sb, const EPI& epi, hipStream_t st) {
   if (fa == kE4M3 && fb == kE4M3) return few_run<kE4M3, kE4M3, GATED>(A, B, M, N, K, sa, sb, epi, st);
   if (fa == kE5M2 && fb == kE4M3) return few_run<kE5M2, kE4M3, GATED>(A, B, M, N, K, sa, sb, epi, st);
   if (fa == kE4M3 && fb == kE5M2) return few_run<kE4M3, kE5M2, GATED>(A, B, M, N, K, sa, sb, epi, st);
@@ -209,6 +224,14 @@ hipError_t launch_gemm_few_rows(const uint8_t* A, int fa, const uint8_t* B, int 
                                 const float* sinv_a, const float* sinv_b, const EpiArgs& epi, bool gated,
                                 hipStream_t stream) {
   if (gated) return few_fmt<true>(A, fa, B, fb, M, N, K, sinv_a, sinv_b, epi, stream);
+  return few_fmt<false>(A, fa, B, fb, M, N, K, sinv_a, sinv_b, epi, stream);
+}
+
+hipError_t launch_loss_few_rows(const uint8_t* A, int fa, const uint8_t* B, int fb, int64_t M, int64_t N, int64_t K,
+                                const float* sinv_a, const float* sinv_b, const LossEpi& epi, bool count_only,
+                                int* groups, hipStream_t stream) {
+  *groups = few_groups(N);
+  if (count_only) return hipSuccess;
   return few_fmt<false>(A, fa, B, fb, M, N, K, sinv_a, sinv_b, epi, stream);
 }
 

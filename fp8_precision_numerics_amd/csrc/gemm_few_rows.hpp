@@ -15,4 +15,12 @@ hipError_t launch_gemm_few_rows(const uint8_t* A, int fa, const uint8_t* B, int 
                                 const float* sinv_a, const float* sinv_b, const EpiArgs& epi, bool gated,
                                 hipStream_t stream);
 
+struct LossEpi;  // vocab_epilogue.hpp
+
+// The same with the loss over the vocabulary behind it; returns the workgroups of such a product
+// (epi.partials holds a slot for each) in *groups.  With `count_only` nothing is launched.
+hipError_t launch_loss_few_rows(const uint8_t* A, int fa, const uint8_t* B, int fb, int64_t M, int64_t N, int64_t K,
+                                const float* sinv_a, const float* sinv_b, const LossEpi& epi, bool count_only,
+                                int* groups, hipStream_t stream);
+
 }  // namespace fp8mi

@@ -93,7 +93,8 @@ __device__ __forceinline__ void dma_lds4(__amdgpu_buffer_rsrc_t r, uint32_t lds,
 constexpr int kDmaGroups = 4;
 
 // The operand slabs of one output tile: rows [m0, m_end) of A and [n0, n_end)
-// of B, both row-major with K bytes per row, fetched 128 K bytes per step.
+// of B, both row-major with K bytes per row (A's rows may be lda >= K apart, zeros
+// from K to the next multiple of 16), fetched 128 K bytes per step.
 // Direct loads: load q of wave w fills tile rows (w + q*NW)*8 .. +7; lane i
 // fills position i & 7 of row i >> 3 of that group with the granule stored
 // there under the swizzle (which depends on the row's low 4 bits only, i.e. not
@@ -138,7 +139,7 @@ struct SlabLoader {
   const uint8_t* A;
   const uint8_t* B;
   int64_t m0, m_end, n0, n_end;
-  int K, w, voff;
+  int K, lda, w, voff;
   int ldb;            // BT: bytes per K row of B (= N)
   uint32_t voff_bt;   // BT: the lane's offset in the first K row group, or kOutOfRange
   __amdgpu_buffer_rsrc_t ra, rb;
@@ -157,11 +158,11 @@ struct SlabLoader {
   }
 
   __device__ __forceinline__ SlabLoader(const uint8_t* A_, int64_t m0_, int64_t m_end_, const uint8_t* B_,
-                                        int64_t n0_, int64_t n_end_, int K_, int w_, int lane)
-      : A(A_), B(B_), m0(m0_), m_end(m_end_), n0(n0_), n_end(n_end_), K(K_), w(w_) {
-    ra = operand_rsrc(A + m0 * K, m_end - m0, K);
+                                        int64_t n0_, int64_t n_end_, int K_, int w_, int lane, int lda_ = 0)
+      : A(A_), B(B_), m0(m0_), m_end(m_end_), n0(n0_), n_end(n_end_), K(K_), lda(lda_ ? lda_ : K_), w(w_) {
+    ra = operand_rsrc(A + m0 * lda, m_end - m0, lda);
     const int lrow = w * 8 + (lane >> 3);
-    voff = lrow * K + (((lane & 7) ^ lds_swz(lrow)) & 7) * 16;
+    voff = lrow * lda + (((lane & 7) ^ lds_swz(lrow)) & 7) * 16;
     if constexpr (PAIR) {
       ldb = K;
       voff_bt = 0;
@@ -192,7 +193,7 @@ struct SlabLoader {
     for (int e = 0; e < PER; ++e) {
       const int d = g * PER + e;
       if (d >= LQA + LQB) break;
-      if (d < LQA) dma_lds16(ra, la + d * NW * 1024, voff + d * NW * 8 * K, k0);
+      if (d < LQA) dma_lds16(ra, la + d * NW * 1024, voff + d * NW * 8 * lda, k0);
       else if constexpr (BT)  // a full step: every K row exists, only the column needs the range check
         dma_lds16(rb, lb + (d - LQA) * NW * 1024, (int)voff_bt, ((d - LQA) * NW * RPB + k0) * ldb);
       else if constexpr (PAIR) {
@@ -206,7 +207,7 @@ struct SlabLoader {
   // registers; B likewise, or (BT) by direct loads whose VGPR offset carries
   // the row, so K rows past the end read as zero.
   __device__ __forceinline__ void ragged(uint8_t* dst, int kt, int t) const {
-    tile_load_zero_fill<BM, 64 * NW>(A, K, m0, m_end, kt * kBK, K, dst, t);
+    tile_load_zero_fill<BM, 64 * NW>(A, lda, m0, m_end, kt * kBK, K, dst, t);
     if constexpr (BT) {
       const uint32_t lb = lds_addr(dst + BM * kBK) + w * 1024;
 #pragma unroll
@@ -630,9 +631,10 @@ __device__ __forceinline__ uint2 lds_read_tr8(const uint8_t* p) {
   return make_uint2((uint32_t)r[0], (uint32_t)r[1]);
 }
 
-// ARGS: RequantArgs, or (epilogue.hpp) FusedEpi or GatedEpi, which replace the
+// ARGS: RequantArgs, or (epilogue.hpp) FusedEpi, GatedEpi or ProductEpi, which replace the
 // output's writing by the feed-forward epilogues (OUT is then kF32, the type in
-// which the tile is staged, and C is unused).
+// which the tile is staged, and C is unused); or a tile epilogue (is_tile_epilogue), which
+// takes the tile from the accumulators itself (its finish_tile).
 // STAGES: LDS buffers of the K loop, 2 or 3.
 template <int BM, int BN, int WM, int WN, int FA, int FB, int OUT, int MODE, bool BT = false, class ARGS = RequantArgs,
           int STAGES = 2>
@@ -649,9 +651,11 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(
   constexpr int BLK = (MODE == kAccumExact || MXE) ? 32 : 16;
   constexpr bool EPI = is_epilogue<ARGS>::value;
   constexpr bool GATED = std::is_same<ARGS, GatedEpi>::value;
+  constexpr bool PRODUCT = std::is_same<ARGS, ProductEpi>::value;
+  constexpr bool TILE_EPI = is_tile_epilogue<ARGS>::value;
   constexpr int PAIR = GATED ? BLK : 0;
   constexpr int OUT_BN = GATED ? BN / 2 : BN;  // output columns of a tile
-  static_assert(!EPI || (OUT == kF32 && !MXS), "the feed-forward epilogues stage fp32 tiles");
+  static_assert(!(EPI || TILE_EPI) || (OUT == kF32 && !MXS), "the feed-forward epilogues stage fp32 tiles");
   constexpr int FM = WTM / BLK, FN = WTN / BLK;
   static_assert(FM >= 1 && FN >= 1 && WTM % BLK == 0 && WTN % BLK == 0, "wave tile shape");
   // A stage: the A slab, the B slab, and (MXFP8) their block scales.
@@ -687,9 +691,11 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(
     }
   }
 
-  const SlabLoader<BM, BN, NW, BT, PAIR> slabs(A, m_base, M, B, n_base, N, K, w, lane);
+  int lda = 0;  // K
+  if constexpr (PRODUCT) lda = rq.lda;
+  const SlabLoader<BM, BN, NW, BT, PAIR> slabs(A, m_base, M, B, n_base, N, K, w, lane, lda);
   static_assert(!BT || !MXS, "MXFP8 operands are K-contiguous");
-  // EPI: each XCD begins the K loop at another of its nturn full steps.  Rows are often
+  // EPI, TILE_EPI: each XCD begins the K loop at another of its nturn full steps.  Rows are often
   // a power of two apart, and all the chip's tiles at the same K would ask the same few
   // memory channels; the tiles of one XCD stay together, since they share its L2.
   // Measured on MI355X with inputs out of the caches: fused 8192 x 4096 x 16384 on the
@@ -697,7 +703,7 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(
   // whose steps are twice as long, unchanged.  (The plain GEMM keeps its order of sums.)
   int turn = 0, nturn = 0;
   auto issue_direct = [&](uint8_t* dst, int kt, int g) {
-    if constexpr (EPI) {
+    if constexpr (EPI || TILE_EPI) {
       kt += turn;
       kt -= kt >= nturn ? nturn : 0;
     }
@@ -733,7 +739,7 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(
   uint8_t* const s0 = smem;
   uint8_t* const s1 = smem + STAGE;
   int nfull = K / kBK;
-  if constexpr (EPI) {
+  if constexpr (EPI || TILE_EPI) {
     nfull = ragged_k ? nk - 1 : nk;  // of this part
     nturn = nfull;
     turn = (int)(((blockIdx.x & 7u) * (unsigned)nfull) >> 3);
@@ -801,7 +807,7 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(
     static_assert(PASS == BM || OUT == kF32 || OUT == kBF16, "FP8 tiles go out in one pass");
     TW tw{smem, PASS};
     if constexpr (EPI) {
-      EpiPass<BN, NT, PASS, PAIR, TW> pass(rq, M, N, m_base, n_base, t);
+      EpiPass<BN, NT, PASS, PAIR, PRODUCT, TW> pass(rq, M, N, m_base, n_base, t);
       const bool whole = rq.split <= 1;
       float* partials = rq.partials + (whole ? 0 : (int64_t)part * M * (GATED ? 2 * (int64_t)N : (int64_t)N));
       LaneStats st;
@@ -942,7 +948,8 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(
     // the instruction: no per-tensor factor.
     float sc = MX ? 1.0f : sinv_a[0] * sinv_b[0];
     if constexpr (EPI) sc = rq.split > 1 ? 1.0f : sc;
-    write_tile_checked([&](int r_lo, int r_hi, auto& tw, auto mask) {
+    if constexpr (TILE_EPI) rq.template finish_tile<BM, BN, WM, WN, BLK>(acc, sc, smem, M, N, m_base, n_base, tn, w, lane);
+    else write_tile_checked([&](int r_lo, int r_hi, auto& tw, auto mask) {
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
         const int r = wm * WTM + i * 16 + (lane & 15);
@@ -1114,7 +1121,8 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(
     float sc = MXE ? 1.0f : sinv_a[0] * sinv_b[0];
     if constexpr (EPI) sc = rq.split > 1 ? 1.0f : sc;
     const float* fac = reinterpret_cast<const float*>(refs + 512);
-    write_tile_checked([&](int r_lo, int r_hi, auto& tw, auto mask) {
+    if constexpr (TILE_EPI) rq.template finish_tile<BM, BN, WM, WN, BLK>(acc, sc, smem, M, N, m_base, n_base, tn, w, lane);
+    else write_tile_checked([&](int r_lo, int r_hi, auto& tw, auto mask) {
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
         const int r = wm * WTM + i * 32 + (lane & 31);

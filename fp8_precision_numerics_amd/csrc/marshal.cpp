@@ -35,6 +35,8 @@ decltype(&fp8_layernorm_quantize) p_layer;
 decltype(&fp8_layernorm_backward) p_layer_back;
 decltype(&fp8_embedding) p_embed;
 decltype(&fp8_embedding_backward) p_embed_back;
+decltype(&fp8_vocab_cross_entropy) p_vocab;
+decltype(&fp8_vocab_cross_entropy_backward) p_vocab_back;
 
 // One call's operands: every tensor must be on the first one's device.
 class Call {
@@ -472,6 +474,65 @@ PyObject* embed_back(PyObject* const* args, Py_ssize_t n) {
   return invoke(p_embed_back, ptok, it, rows, pdy, dt, vocab, cols, scale, base, ptab, tt, ws, bytes, c.stream);
 }
 
+// A vector of whole numbers, one a row: its type.
+void* indices(const Call& c, int i, const char* name, int64_t n, int* type) {
+  const at::Tensor* t = c.tensor(i, name);
+  if (!t) raise(PyExc_ValueError, "%s must be a GPU tensor", name);
+  *type = index_type(*t, name);
+  return c.vec(i, name, t->scalar_type(), n);
+}
+
+// cur stream x fx w fw sinv_x sinv_w targets loss lse accum workspace
+PyObject* vocab(PyObject* const* args, Py_ssize_t n) {
+  Call c(args, n, 13);
+  const at::Tensor& x = c.first(2, "x", 2);
+  const at::Tensor& w = matrix(c, 4, "w");
+  const int64_t M = x.size(0), K = x.size(1), V = w.size(0);
+  size_t bytes;
+  int it;
+  const uint8_t* px = codes(c, "x", x);
+  const uint8_t* pw = static_cast<const uint8_t*>(c.mat(4, "w", at::kByte, V, K));
+  const int fx = c.format(3), fw = c.format(5);
+  float *sx = c.scalar(6, "sinv_x"), *sw = c.scalar(7, "sinv_w");
+  void* pt = indices(c, 8, "targets", M, &it);
+  void* loss = c.vec(9, "loss", at::kFloat, M);
+  void* lse = c.vec(10, "lse", at::kFloat, M);
+  const int accum = c.accum(11);
+  void* ws = c.space(12, &bytes);
+  if (c.elsewhere()) return c.device();
+  return invoke(p_vocab, px, fx, pw, fw, M, V, K, sx, sw, pt, it, (float*)loss, (float*)lse, accum, ws, bytes, c.stream);
+}
+
+// cur stream x fx w fw sinv_x sinv_w targets lse dloss fmt scale scale_inv dx dw amax sat accum workspace
+PyObject* vocab_back(PyObject* const* args, Py_ssize_t n) {
+  Call c(args, n, 20);
+  const at::Tensor& x = c.first(2, "x", 2);
+  const at::Tensor& w = matrix(c, 4, "w");
+  const int64_t M = x.size(0), K = x.size(1), V = w.size(0);
+  size_t bytes;
+  int it;
+  const uint8_t* px = codes(c, "x", x);
+  const uint8_t* pw = static_cast<const uint8_t*>(c.mat(4, "w", at::kByte, V, K));
+  const int fx = c.format(3), fw = c.format(5);
+  float *sx = c.scalar(6, "sinv_x"), *sw = c.scalar(7, "sinv_w");
+  void* pt = indices(c, 8, "targets", M, &it);
+  void* lse = c.vec(9, "lse", at::kFloat, M);
+  void* dloss = c.vec(10, "dloss", at::kFloat, M);
+  const int fmt = c.format(11);
+  float *scale = c.scalar(12, "scale"), *inv = c.scalar(13, "scale_inv");
+  const at::Tensor *tx = c.tensor(14, "dx"), *tw = c.tensor(15, "dw");
+  const int xt = tx ? float_type(*tx, "dx", PyExc_TypeError) : FP8MI_F32, wt = tw ? float_type(*tw, "dw", PyExc_TypeError) : FP8MI_F32;
+  void* dx = tx ? c.mat(14, "dx", tx->scalar_type(), M, K) : nullptr;
+  void* dw = tw ? c.mat(15, "dw", tw->scalar_type(), V, K) : nullptr;
+  float* amax = c.scalar(16, "amax");
+  unsigned long long* sat = c.count(17);
+  const int accum = c.accum(18);
+  void* ws = c.space(19, &bytes);
+  if (c.elsewhere()) return c.device();
+  return invoke(p_vocab_back, px, fx, pw, fw, M, V, K, sx, sw, pt, it, (const float*)lse, (const float*)dloss, fmt, scale, inv, dx, xt,
+                                      dw, wt, amax, sat, accum, ws, bytes, c.stream);
+}
+
 template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   try {
@@ -487,7 +548,8 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
 // Addresses of the entry points, in the order of the declarations above.
 PyObject* bind(PyObject* const* args, Py_ssize_t n) {
   void* const slots[] = {&p_gemm, &p_gated, &p_fused, &p_norm, &p_norm_blocks, &p_norm_back, &p_act_back, &p_gated_back,
-                         &p_layer, &p_layer_back, &p_embed, &p_embed_back};
+                         &p_layer, &p_layer_back, &p_embed, &p_embed_back, &p_vocab,
+                         &p_vocab_back};
   constexpr Py_ssize_t count = sizeof(slots) / sizeof(slots[0]);
   if (n != count) raise(PyExc_TypeError, "%s", "an address for every entry point");
   for (Py_ssize_t i = 0; i < count; ++i) {
@@ -502,7 +564,8 @@ PyObject* bind(PyObject* const* args, Py_ssize_t n) {
 PyMethodDef methods[] = {ENTRY("bind", bind), ENTRY("gemm", gemm), ENTRY("gated", gated), ENTRY("fused", fused),
                          ENTRY("norm", norm), ENTRY("norm_blocks", norm_blocks), ENTRY("norm_back", norm_back),
                          ENTRY("act_back", act_back), ENTRY("gated_back", gated_back), ENTRY("layer", layer),
-                         ENTRY("layer_back", layer_back), ENTRY("embed", embed), ENTRY("embed_back", embed_back), {nullptr, nullptr, 0, nullptr}};
+                         ENTRY("layer_back", layer_back), ENTRY("embed", embed), ENTRY("embed_back", embed_back),
+                         ENTRY("vocab", vocab), ENTRY("vocab_back", vocab_back), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fp8mi_marshal", nullptr, -1, methods};
 
 }  // namespace

@@ -33,4 +33,23 @@ hipError_t launch_embedding_backward(const void* tokens, bool wide, int64_t rows
                                      int64_t vocab, int64_t cols, float scale, const void* base, void* dtable,
                                      int ttype, void* workspace, hipStream_t stream);
 
+// `words` of 16 bytes from base, or of zeros without one.
+hipError_t launch_fill_rows(const void* base, void* to, int64_t words, hipStream_t stream);
+
+struct VocabOperands;  // vocab.hpp
+struct Targets;        // vocab_epilogue.hpp
+
+// Workspace with which the loss over M rows, a vocabulary of V and rows of K codes goes in at most
+// `pieces` pieces, forward and backward.
+size_t vocab_workspace(int64_t M, int64_t V, int64_t K, int64_t pieces);
+
+hipError_t launch_vocab_cross_entropy(const VocabOperands& o, int64_t V, const Targets& targets, float* loss, float* lse,
+                                      int accum, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+hipError_t launch_vocab_cross_entropy_backward(const VocabOperands& o, int64_t V, const Targets& targets, const float* lse,
+                                               const float* dloss, int fmt, const float* scale, const float* scale_inv,
+                                               void* dx, int dxtype, void* dw, int dwtype, float* amax,
+                                               unsigned long long* sat, int accum, void* workspace,
+                                               size_t workspace_bytes, hipStream_t stream);
+
 }  // namespace fp8mi

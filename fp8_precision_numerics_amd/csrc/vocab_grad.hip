@@ -1,0 +1,99 @@
+// The vocabulary's cross entropy, backward: the logits of a piece of the vocabulary
+// again, as codes of their gradient (vocab_epilogue.hpp), and the two products on those.
+//
+//   d = dloss (exp(z - lse) - [column = target]),  codes q = round_to_fp8(d scale)
+//   dx = (q W) sinv_d sinv_w,  dw = (q^T x) sinv_d sinv_x
+//
+// Three products of 2 M V K operations on the matrix cores.  Of the M x V gradients only a piece's
+// codes exist at a time, row-major and transposed, the orientations in which the two products read
+// their first operand; dx grows over the pieces in fp32.
+#include "gemm_few_rows.hpp"
+#include "launch.hpp"
+#include "model_ends.hpp"
+#include "vocab_dispatch.hpp"
+
+namespace fp8mi {
+namespace {
+
+int64_t up256(int64_t n) { return (n + 255) & ~int64_t(255); }
+
+// The codes both ways for pieces of P columns, and the fp32 sums of dx where there are several.
+int64_t grad_bytes(int64_t M, int64_t V, int64_t K, int64_t P) {
+  return up256(M * up16(P)) + up256(P * up16(M)) + (P < V ? up256(M * K * 4) : 0);
+}
+
+// The longest piece that the products' offsets reach.
+int64_t most_columns(int64_t K) {
+  const int64_t most = ((int64_t(1) << 31) - 1) / K / kPieceCols * kPieceCols;
+  return most < (int64_t(1) << 22) ? most : (int64_t(1) << 22);
+}
+
+}  // namespace
+
+hipError_t launch_vocab_grad(const VocabOperands& o, int64_t col, int64_t N, const LogitGradEpi& epi, int accum, hipStream_t stream) {
+  // Few rows: the forward's products were exact, and these have to be of the same logits.
+  return vocab_launch(o, col, N, epi, o.M <= kFewRows ? (int)kAccumExact : accum, stream);
+}
+
+size_t vocab_workspace(int64_t M, int64_t V, int64_t K, int64_t pieces) {
+  int64_t P = pieces > 0 ? up256((V + pieces - 1) / pieces) : kPieceCols;
+  P = P < V ? P : V;
+  size_t back = (size_t)grad_bytes(M, V, K, P);
+  const size_t whole = (size_t)grad_bytes(M, V, K, V), fwd = vocab_loss_bytes(M, P);
+  // one piece needs no sums of dx, so it may be the smaller
+  if (V <= most_columns(K) && whole < back) back = whole;
+  return M == 0 ? 0 : (back > fwd ? back : fwd);
+}
+
+hipError_t launch_vocab_cross_entropy_backward(const VocabOperands& o, int64_t V, const Targets& targets, const float* lse,
+                                               const float* dloss, int fmt, const float* scale, const float* scale_inv,
+                                               void* dx, int dxtype, void* dw, int dwtype, float* amax,
+                                               unsigned long long* sat, int accum, void* workspace,
+                                               size_t workspace_bytes, hipStream_t stream) {
+  if (amax || sat) {
+    const hipError_t e = launch_clear_stats(amax, sat, stream);
+    if (e != hipSuccess) return e;
+  }
+  const int64_t M = o.M, K = o.K, ldt = up16(M);
+  const int64_t dwsize = dwtype == kBF16 ? 2 : 4;
+  if (M == 0) return dw ? launch_fill_rows(nullptr, dw, V * K * dwsize / 16, stream) : hipSuccess;
+  // The longest piece that fits, then pieces of equal length.
+  const int64_t most = most_columns(K);
+  int64_t P = V;
+  if (V > most || grad_bytes(M, V, K, V) > (int64_t)workspace_bytes) {
+    int64_t fit = ((int64_t)workspace_bytes - up256(M * K * 4) - 512) / (M + ldt) / kPieceCols * kPieceCols;
+    fit = fit < kPieceCols ? kPieceCols : fit;  // the entry point has seen to that much
+    fit = fit < most ? fit : most;
+    const int64_t pieces = (V + fit - 1) / fit;
+    P = up256((V + pieces - 1) / pieces);
+  }
+  uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
+  uint8_t* const q = ws;
+  uint8_t* const q_t = q + up256(M * up16(P));
+  uint8_t* rest = q_t + up256(P * ldt);
+  // An fp32 dx is its own sum.
+  float* sum = dxtype == kF32 ? reinterpret_cast<float*>(dx) : reinterpret_cast<float*>(rest);
+  if (P < V) rest += up256(M * K * 4);
+  const size_t left = workspace_bytes > (size_t)(rest - ws) ? workspace_bytes - (size_t)(rest - ws) : 0;
+  for (int64_t col = 0; col < V; col += P) {
+    const int64_t n = V - col < P ? V - col : P;
+    const LogitGradEpi epi{lse, dloss, scale, dx ? q : nullptr, dw ? q_t : nullptr, reinterpret_cast<uint32_t*>(amax), sat, targets,
+                           V, col, up16(n), ldt, fmt};
+    hipError_t e = launch_vocab_grad(o, col, n, epi, accum, stream);
+    if (e != hipSuccess) return e;
+    if (dx) {
+      const bool first = col == 0, last = col + n >= V;
+      e = launch_vocab_product(q, up16(n), fmt, o.b + col * K, o.fb, M, K, n, scale_inv, o.sinv_b, first ? nullptr : sum,
+                               last ? dx : (void*)sum, last ? dxtype : (int)kF32, accum, rest, left, stream);
+      if (e != hipSuccess) return e;
+    }
+    if (dw) {
+      e = launch_vocab_product(q_t, ldt, fmt, o.a, o.fa, n, K, M, scale_inv, o.sinv_a, nullptr,
+                               reinterpret_cast<uint8_t*>(dw) + col * K * dwsize, dwtype, accum, rest, left, stream);
+      if (e != hipSuccess) return e;
+    }
+  }
+  return hipSuccess;
+}
+
+}  // namespace fp8mi

@@ -1,0 +1,141 @@
+// Softmax cross entropy over a vocabulary without its logits: the head's product
+// with the loss behind it (vocab_epilogue.hpp), forward.
+//
+//   z = (x W^T) sinv_x sinv_w [M x V],  lse = log sum_v exp z,  loss = lse - z[target]
+//
+// Matrix-core-bound for many rows (2 M V K operations), bound by the weight's V K bytes
+// for a few, which take the streaming kernel of gemm_few_rows.hip.  A tile leaves the maximum and
+// the sum of each of its rows (8 bytes a row and 256 columns: 1/64 of bf16 logits), a second kernel joins
+// them; a workspace too small for the whole vocabulary's is served in pieces, the joined
+// pair of each row carried from one to the next.
+#include "gemm_few_rows.hpp"
+#include "launch.hpp"
+#include "model_ends.hpp"
+#include "vocab_dispatch.hpp"
+
+namespace fp8mi {
+namespace {
+
+struct JoinArgs {
+  const float2* partials;  // [tiles x M]
+  float2* state;           // [M]: the columns before these
+  const float* mine;
+  Targets targets;
+  float* loss;
+  float* lse;
+  int64_t M, vocab;
+  int tiles;
+  bool first, last;
+};
+
+// {m, s} of two sets of columns together.
+__device__ __forceinline__ float2 join(float2 a, float2 b) {
+  const float m = __builtin_fmaxf(a.x, b.x), ref = LossEpi::reference(m);
+  return make_float2(m, a.y * exp_of(a.x - ref) + b.y * exp_of(b.x - ref));
+}
+
+// R rows a workgroup of 256, 256 / R lanes down the tiles of each.
+template <int R>
+__global__ __launch_bounds__(256) void vocab_join_kernel(JoinArgs a) {
+  constexpr int L = 256 / R;
+  __shared__ float2 buf[256];
+  const int t = threadIdx.x, l = t / R;
+  const int64_t row = (int64_t)blockIdx.x * R + t % R;
+  const bool here = row < a.M;
+  constexpr int U = 8;
+  const float2 none = make_float2(-__builtin_inff(), 0.0f);
+  float2 v = none;
+  if (here) {
+    for (int k = l; k < a.tiles; k += U * L) {
+      float2 p[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) p[u] = k + u * L < a.tiles ? a.partials[(int64_t)(k + u * L) * a.M + row] : none;
+#pragma unroll
+      for (int u = 0; u < U; ++u) v = join(v, p[u]);
+    }
+  }
+  buf[t] = v;
+  __syncthreads();
+#pragma unroll
+  for (int half = L / 2; half > 0; half >>= 1) {
+    if (l < half) buf[t] = join(buf[t], buf[t + half * R]);
+    __syncthreads();
+  }
+  if (l != 0 || !here) return;
+  v = buf[t];
+  if (!a.first) v = join(a.state[row], v);
+  if (!a.last) {
+    a.state[row] = v;
+    return;
+  }
+  const float lse = v.x + logf(v.y);
+  if (a.lse) a.lse[row] = lse;
+  if (a.loss) a.loss[row] = a.targets.inside(row, a.vocab) ? lse - a.mine[row] : 0.0f;
+}
+
+// 16 rows a workgroup where they make one for every other compute unit (whole lines of the partials are read),
+// otherwise a row each.
+void join_launch(const JoinArgs& a, hipStream_t st) {
+  if (a.M >= 2048) hipLaunchKernelGGL(vocab_join_kernel<16>, dim3((unsigned)((a.M + 15) / 16)), dim3(256), 0, st, a);
+  else hipLaunchKernelGGL(vocab_join_kernel<1>, dim3((unsigned)a.M), dim3(256), 0, st, a);
+}
+
+}  // namespace
+
+int vocab_tile_cols(const VocabOperands& o, int64_t N, int accum) {
+  return vocab_shape(o, N, accum) == 0 ? 256 : 128;
+}
+
+hipError_t launch_vocab_logits(const VocabOperands& o, int64_t col, int64_t N, const LossEpi& epi, int accum, hipStream_t stream) {
+  return vocab_launch(o, col, N, epi, accum, stream);
+}
+
+size_t vocab_loss_bytes(int64_t M, int64_t P) {
+  return (size_t)(up16(M * 4) + up16(M * 8) + M * 8 * ((P + 127) / 128));
+}
+
+hipError_t launch_vocab_cross_entropy(const VocabOperands& o, int64_t V, const Targets& targets, float* loss, float* lse,
+                                      int accum, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
+  JoinArgs j{nullptr, nullptr, reinterpret_cast<float*>(ws), targets, loss, lse, o.M, V, 0, true, true};
+  LossEpi epi{nullptr, reinterpret_cast<float*>(ws), targets, 0};
+  ws += up16(o.M * 4);
+  j.state = reinterpret_cast<float2*>(ws);
+  ws += up16(o.M * 8);
+  j.partials = epi.partials = reinterpret_cast<float2*>(ws);
+  // slots for the pairs of so many tiles
+  const int64_t slots = (int64_t)(workspace_bytes - (size_t)(ws - reinterpret_cast<uint8_t*>(workspace))) / (o.M * 8);
+  for (int64_t col = 0; col < V;) {
+    int64_t n = V - col;
+    hipError_t e;
+    if (o.M <= kFewRows) {
+      const auto run = [&](bool count_only) {
+        epi.col0 = col;
+        return launch_loss_few_rows(o.a, o.fa, o.b + col * o.K, o.fb, o.M, n, o.K, o.sinv_a, o.sinv_b, epi, count_only, &j.tiles, stream);
+      };
+      run(true);
+      while (j.tiles > slots) {  // half the columns, in whole tiles of 16
+        n = (n / 2 + 15) / 16 * 16;
+        run(true);
+      }
+      e = run(false);
+    } else {
+      const int64_t fit = slots * 128;  // the narrower tiles'
+      if (n > fit) n = fit / kPieceCols * kPieceCols;
+      epi.col0 = col;
+      e = launch_vocab_logits(o, col, n, epi, accum, stream);
+      const int cols = vocab_tile_cols(o, n, accum);
+      j.tiles = (int)((n + cols - 1) / cols);
+    }
+    if (e != hipSuccess) return e;
+    j.first = col == 0;
+    col += n;
+    j.last = col >= V;
+    join_launch(j, stream);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace fp8mi

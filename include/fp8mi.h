@@ -667,6 +667,66 @@ FP8MI_API int fp8_embedding_backward(const void* tokens, int itype, int64_t rows
 /* Bytes of workspace that fp8_embedding_backward asks for (0: sizes that it refuses, or no tokens). */
 FP8MI_API size_t fp8mi_embedding_workspace(int64_t rows, int64_t cols);
 
+/*
+ * fp8_vocab_cross_entropy — softmax cross entropy over a vocabulary, with its projection
+ * inside; the logits are never stored.
+ *
+ *   z[m][v] = sinv_x * sinv_w * sum_k dec_fx(x[m][k]) dec_fw(w[v][k])
+ *   lse[m]  = log sum_v exp(z[m][v])
+ *   loss[m] = lse[m] - z[m][targets[m]]          (0 where targets[m] lies outside [0, V))
+ *
+ * x          device, [M x K] codes of format fx (the hidden states).
+ * w          device, [V x K] codes of format fw (the vocabulary's weight).
+ * targets    device, [M] of itype (fp8mi_index), aligned to its size.
+ * loss, lse  device, [M] fp32; either may be NULL.
+ * accum      fp8mi_accum, as for fp8_gemm.  Calls of at most 16 rows use the exact arithmetic
+ *            in both modes.
+ * workspace  device scratch of the caller, 16-B aligned: the target's logit, and the maximum and sum of
+ *            each row for every 128 columns.  Where it is smaller than that for the whole
+ *            vocabulary, the vocabulary is taken in pieces (at least 256 columns' worth is needed, else
+ *            FP8MI_ERR_WORKSPACE; fp8mi_vocab_workspace tells).
+ * Exponentials and sums are fp32, relative to each row's largest logit.  A NaN or infinite logit makes the row's
+ * loss and lse NaN (an lse that no finite logit enters is NaN too).
+ * K must be a multiple of 16, K <= 2^22; M <= 2^23 - 16, M * K < 2^31; V >= 1; x and w 16-B aligned.
+ */
+FP8MI_API int fp8_vocab_cross_entropy(const uint8_t* x, int fx, const uint8_t* w, int fw, int64_t M, int64_t V, int64_t K,
+                            const float* sinv_x, const float* sinv_w, const void* targets, int itype, float* loss,
+                            float* lse, int accum, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * fp8_vocab_cross_entropy_backward — its gradients, by the logits' gradient in FP8.
+ *
+ *   d[m][v] = dloss[m] * (exp(z[m][v] - lse[m]) - [v = targets[m]])   (a row of zeros where targets[m] lies outside [0, V))
+ *   q       = round_to_fp8(fp32(d * scale)), as fp8_quantize
+ *   dx[m][k] = scale_inv * sinv_w * sum_v dec(q[m][v]) dec_fw(w[v][k])
+ *   dw[v][k] = scale_inv * sinv_x * sum_m dec(q[m][v]) dec_fx(x[m][k])
+ *   amax, sat  of the unscaled d / of d * scale, as fp8_quantize
+ *
+ * The logits are computed again, in pieces of the vocabulary; only one piece's codes exist at a time.
+ * lse        device, [M] fp32, from the forward (of the same accum).
+ * dloss      device, [M] fp32: the gradient of each row's loss (1 / rows for their mean).
+ * fmt        fp8mi_format of d (E5M2 under the HYBRID recipe).
+ * scale, scale_inv  device, 1 fp32 each: the gradient's (delayed) scale and its inverse.
+ * dx         device, [M x K] of dxtype (fp32 or bf16), overwritten, or NULL.
+ * dw         device, [V x K] of dwtype, overwritten, or NULL.
+ * amax, sat  device, 1 fp32 / 1 uint64, overwritten, or NULL.
+ * accum      of the logits and of both products.
+ * workspace  device scratch of the caller, 16-B aligned: the more there is, the fewer the pieces
+ *            (each costs a pass over dx's fp32 sums).  At least
+ *            fp8mi_vocab_workspace(M, V, K, 0) bytes, else FP8MI_ERR_WORKSPACE.
+ * One of dx and dw is needed; both 16-B aligned.  The other arguments and the rules are the forward's.
+ */
+FP8MI_API int fp8_vocab_cross_entropy_backward(const uint8_t* x, int fx, const uint8_t* w, int fw, int64_t M, int64_t V, int64_t K,
+                                     const float* sinv_x, const float* sinv_w, const void* targets, int itype,
+                                     const float* lse, const float* dloss, int fmt, const float* scale,
+                                     const float* scale_inv, void* dx, int dxtype, void* dw, int dwtype, float* amax,
+                                     unsigned long long* sat, int accum, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
+/* Bytes of workspace with which both calls take the vocabulary in at most `pieces` pieces (0: the least that
+ * they accept).  0 for sizes that they refuse, and for no rows. */
+FP8MI_API size_t fp8mi_vocab_workspace(int64_t M, int64_t V, int64_t K, int64_t pieces);
+
 #ifdef __cplusplus
 }
 #endif

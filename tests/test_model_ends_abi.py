@@ -89,7 +89,43 @@ def test_embedding_workspace():
     assert fm.embedding_workspace_bytes(1 << 20, 64) == 4 * (4 << 20) + 4096 * 512
 
 
-@pytest.mark.parametrize("name", ["layer", "layer_back", "embed", "embed_back"])
+LEAST = 2 * 256 * 32 + 32 * 64 * 4           # 32 rows: codes both ways for 256 columns, and dx's sums
+VOCAB = dict(x=P, fx=0, w=P, fw=0, M=32, V=1000, K=64, sx=P, sw=P, targets=P, itype=1, loss=P, lse=P, accum=0, ws=P, ws_bytes=32 * 4 + 32 * 8 + 32 * 8 * 2, stream=None)
+VOCAB_BACK = dict(x=P, fx=0, w=P, fw=0, M=32, V=1000, K=64, sx=P, sw=P, targets=P, itype=0, lse=P, dloss=P, fmt=1, scale=P, inv=P, dx=P, dxtype=1, dw=P, dwtype=0,
+                  amax=None, sat=None, accum=1, ws=P, ws_bytes=LEAST, stream=None)
+VOCAB_BAD = [(EFMT, dict(fx=2)), (EFMT, dict(fw=-1)), (EDTYPE, dict(itype=2)), (EACCUM, dict(accum=2)), (ESHAPE, dict(M=-1)), (ESHAPE, dict(V=0)), (ESHAPE, dict(K=0)),
+             (ESHAPE, dict(V=1 << 31)), (ESHAPE, dict(M=(1 << 23) - 15, K=16)), (ESHAPE, dict(M=1 << 20, K=2048)), (ESHAPE, dict(K=(1 << 22) + 16)), (EALIGN, dict(K=72)),
+             (EALIGN, dict(ws=P8)), (ENULL, dict(x=None)), (ENULL, dict(w=None)), (ENULL, dict(sx=None)), (ENULL, dict(sw=None)), (ENULL, dict(targets=None)),
+             (ENULL, dict(ws=None)), (EALIGN, dict(x=P8)), (EALIGN, dict(w=P8)), (EALIGN, dict(targets=ctypes.c_void_p(0x10002)))]
+
+
+@pytest.mark.parametrize("want,change", VOCAB_BAD + [
+    (EALIGN, dict(targets=P4)), (ENULL, dict(loss=None, lse=None)), (EWS, dict(ws_bytes=32 * 4 + 32 * 8 + 32 * 8 * 2 - 1)), (OK, dict(M=0, x=None, ws=None, ws_bytes=0)),
+    (OK, dict(M=0, loss=None, lse=None))])
+def test_vocab_refusals(lib, want, change):
+    assert call(lib.fp8_vocab_cross_entropy, VOCAB, **change) == want
+
+
+@pytest.mark.parametrize("want,change", VOCAB_BAD + [
+    (EFMT, dict(fmt=2)), (EDTYPE, dict(dxtype=2)), (EDTYPE, dict(dwtype=-1)), (ENULL, dict(dx=None, dw=None)), (EALIGN, dict(dx=P8)), (EALIGN, dict(dw=P8)),
+    (ENULL, dict(lse=None)), (ENULL, dict(dloss=None)), (ENULL, dict(scale=None)), (ENULL, dict(inv=None)), (EWS, dict(ws_bytes=LEAST - 1)),
+    (OK, dict(M=0, dw=None)), (OK, dict(M=0, dx=None, dw=None, x=None))])
+def test_vocab_backward_refusals(lib, want, change):
+    assert call(lib.fp8_vocab_cross_entropy_backward, VOCAB_BACK, **change) == want
+
+
+def test_vocab_workspace():
+    assert fm.vocab_workspace_bytes(0, 1000, 64) == 0 and fm.vocab_workspace_bytes(32, 0, 64) == 0 and fm.vocab_workspace_bytes(32, 1000, (1 << 22) + 16) == 0
+    assert fm.vocab_workspace_bytes(32, 1000, 64, 0) == LEAST and fm.vocab_workspace_bytes(32, 1000, 64, 4) == LEAST
+    # one piece: codes of 1000 columns, rows of 1008 and of 32, each rounded up to 256
+    assert fm.vocab_workspace_bytes(32, 1000, 64) == 32256 + 32000
+    # a whole vocabulary of few columns needs no sums of dx, and less than a piece with them
+    assert fm.vocab_workspace_bytes(16, 300, 64, 0) == fm.vocab_workspace_bytes(16, 300, 64) == 4864 + 4864
+    # a hidden size this small leaves the forward's pairs the larger
+    assert fm.vocab_workspace_bytes(1, 100000, 16, 1) == 100096 + 256 * ((16 * 100000 + 255) // 256)
+
+
+@pytest.mark.parametrize("name", ["layer", "layer_back", "embed", "embed_back", "vocab", "vocab_back"])
 def test_a_wrong_number_of_arguments_is_a_type_error(name):
     module = binding._MODULE or binding._load_module()
     with pytest.raises(TypeError):
