@@ -290,14 +290,49 @@ __device__ __forceinline__ void layer_gradient(const LayerBackArgs& a, const Dro
   }
 }
 
-template <int XT, bool WG, int VPT>
-__global__ __launch_bounds__(WG ? 1024 : 256) void layernorm_backward_kernel(LayerBackArgs a) {
+// One row as loaded.
+template <int XT, int VPT>
+struct BackRow {
+  Octet<XT> dy[VPT], h[VPT], dr[VPT];
+  float m, r;
+  __device__ __forceinline__ void load(const LayerBackArgs& a, int64_t row, int64_t octets, int t, int TPR) {
+    const bool here = row < a.rows;
+    m = r = 0.0f;
+    if (here) {
+      m = a.mean[row];
+      r = a.rstd[row];
+    }
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      dy[v].clear();
+      h[v].clear();
+      dr[v].clear();
+      if (here && t + v * TPR < octets) {
+        const int64_t o = row * octets + t + v * TPR;
+        dy[v].load(a.dy, o);
+        h[v].load(a.h, o);
+        if (a.dres) dr[v].load(a.dres, o);
+      }
+    }
+  }
+};
+
+// NT: the largest workgroup.  PRE: a row is requested while the one before it is worked on, which takes the place of
+// more workgroups (each costs a partial row).  Rows of more than 8192 values have workgroups of up to 1024
+// threads, whose 128 registers do not hold another row (2000 x 16384: 76 us; with 512 threads of four octets and the row
+// requested ahead, which spills, 112).
+template <int XT, bool WG, int VPT, int NT, bool PRE>
+__global__ __launch_bounds__(NT) void layernorm_backward_kernel(LayerBackArgs a) {
   __shared__ float2 buf[2][kMaxWaves];
   const int TPR = WG ? blockDim.x : 64, RPB = WG ? 1 : 4;
   const int t = WG ? threadIdx.x : threadIdx.x & 63;
   const int64_t octets = a.cols / 8;
   const float inv_n = 1.0f / (float)a.cols;
   const Dropper drop(a.drop);
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  int64_t row = (int64_t)blockIdx.x * RPB + (WG ? 0 : threadIdx.x >> 6);
+  BackRow<XT, VPT> next;
+  if constexpr (PRE) next.load(a, row, octets, t, TPR);
   Octet<XT> wt[VPT];
   float dw[VPT][8], db[VPT][8];
 #pragma unroll
@@ -308,27 +343,22 @@ __global__ __launch_bounds__(WG ? 1024 : 256) void layernorm_backward_kernel(Lay
     for (int e = 0; e < 8; ++e) dw[v][e] = db[v][e] = 0.0f;
   }
   int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * RPB + (WG ? 0 : threadIdx.x >> 6); row < a.rows; row += (int64_t)gridDim.x * RPB) {
+  for (; row < a.rows; row += step) {
     const int64_t base = row * octets;
-    Octet<XT> dy[VPT], h[VPT], dr[VPT];
-    const float m = a.mean[row], r = a.rstd[row];
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      dy[v].clear();
-      h[v].clear();
-      dr[v].clear();
-      if (t + v * TPR < octets) {
-        dy[v].load(a.dy, base + t + v * TPR);
-        h[v].load(a.h, base + t + v * TPR);
-        if (a.dres) dr[v].load(a.dres, base + t + v * TPR);
-      }
+    BackRow<XT, VPT> now;
+    if constexpr (PRE) {
+      now = next;
+      next.load(a, row + step, octets, t, TPR);
+    } else {
+      now.load(a, row, octets, t, TPR);
     }
+    const float m = now.m, r = now.r;
     float2 sum = make_float2(0.0f, 0.0f);  // a lane past the row's end holds dy = 0
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       float d[8], f[8], w[8];
-      dy[v].widen(d);
-      h[v].widen(f);
+      now.dy[v].widen(d);
+      now.h[v].widen(f);
       wt[v].widen(w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -346,7 +376,7 @@ __global__ __launch_bounds__(WG ? 1024 : 256) void layernorm_backward_kernel(Lay
       if (t + v * TPR >= octets) continue;
       float w[8];
       wt[v].widen(w);
-      layer_gradient<XT>(a, drop, dy[v], h[v], dr[v], w, m, r, means, base + t + v * TPR);
+      layer_gradient<XT>(a, drop, now.dy[v], now.h[v], now.dr[v], w, m, r, means, base + t + v * TPR);
     }
   }
   if (!a.dw && !a.db) return;
@@ -496,18 +526,23 @@ void layer_stats(const LayerArgs& a, bool stats, int g, hipStream_t st) {
   else layer_run<XT, FMT, false>(a, g, st);
 }
 
+// Workgroups of the gradient's kernel.  With a row requested ahead, two of wavefront rows a compute unit and as many of workgroup rows as make 512
+// octets (8192 x 4096, dropout: 66.0 us with one, 73.8 with two, whose partial rows cost more than they
+// gain; 4096 x 2048: 25.8, 21.1, with three 21.4; 8192 x 1040: 43.0, 26.2, with four 20.6; 8192 x 1024: 17.9, 17.5, 20.9).
 int layer_back_groups(int64_t rows, int64_t octets, int64_t slots) {
-  if (octets <= 128) return row_groups(rows, 4, 4, slots);
-  return row_groups(rows, 1, octets <= 1024 ? 2 : 1, slots);
+  if (octets <= 128) return row_groups(rows, 4, 2, slots);
+  const int64_t fill = (512 + octets / 2) / octets;
+  return row_groups(rows, 1, fill < 1 ? 1 : (int)fill, slots);
 }
 
 template <int XT>
 void layer_back_run(const LayerBackArgs& a, int g, hipStream_t st) {
   const int64_t o = a.cols / 8;
   const dim3 grid((unsigned)g);
-  if (o <= 64) hipLaunchKernelGGL((layernorm_backward_kernel<XT, false, 1>), grid, dim3(256), 0, st, a);
-  else if (o <= 128) hipLaunchKernelGGL((layernorm_backward_kernel<XT, false, 2>), grid, dim3(256), 0, st, a);
-  else if (o <= 2048) hipLaunchKernelGGL((layernorm_backward_kernel<XT, true, 2>), grid, dim3(row_threads(o)), 0, st, a);
+  if (o <= 64) hipLaunchKernelGGL((layernorm_backward_kernel<XT, false, 1, 256, true>), grid, dim3(256), 0, st, a);
+  else if (o <= 128) hipLaunchKernelGGL((layernorm_backward_kernel<XT, false, 2, 256, true>), grid, dim3(256), 0, st, a);
+  else if (o <= 1024) hipLaunchKernelGGL((layernorm_backward_kernel<XT, true, 2, 512, true>), grid, dim3(row_threads(o)), 0, st, a);
+  else if (o <= 2048) hipLaunchKernelGGL((layernorm_backward_kernel<XT, true, 2, 1024, false>), grid, dim3(row_threads(o)), 0, st, a);
   else hipLaunchKernelGGL((layernorm_backward_long_kernel<XT, 1024>), grid, dim3(1024), 0, st, a);
 }
 
