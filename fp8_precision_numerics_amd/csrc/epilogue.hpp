@@ -50,7 +50,7 @@ struct is_tile_epilogue {
 // The epilogues as kernel arguments of their own types.
 struct FusedEpi : EpiArgs {};
 struct GatedEpi : EpiArgs {};
-// A product whose A rows are padded: lda bytes apart, zeros from K to the next multiple of 16
+// A product whose A rows are padded: lda bytes apart, a multiple of 128, zeros from K on
 // (K itself may be any number), added to the fp32 matrix `add` [M x N] (may be null, or y where y is fp32).
 struct ProductEpi : EpiArgs {
   const float* add;

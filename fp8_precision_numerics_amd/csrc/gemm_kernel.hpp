@@ -93,8 +93,7 @@ __device__ __forceinline__ void dma_lds4(__amdgpu_buffer_rsrc_t r, uint32_t lds,
 constexpr int kDmaGroups = 4;
 
 // The operand slabs of one output tile: rows [m0, m_end) of A and [n0, n_end)
-// of B, both row-major with K bytes per row (A's rows may be lda >= K apart, zeros
-// from K to the next multiple of 16), fetched 128 K bytes per step.
+// of B, both row-major with K bytes per row, fetched 128 K bytes per step.
 // Direct loads: load q of wave w fills tile rows (w + q*NW)*8 .. +7; lane i
 // fills position i & 7 of row i >> 3 of that group with the granule stored
 // there under the swizzle (which depends on the row's low 4 bits only, i.e. not
@@ -127,7 +126,11 @@ constexpr uint32_t kOutOfRange = 0x80000000u;  // above any operand size these l
 // columns and its block of up columns land in the same lanes.  A load's 8 rows lie
 // in one block, so each load takes one of two resources (the gate's and the up
 // projection's rows from the tile start to F); rows past F read as zero.
-template <int BM, int BN, int NW, bool BT = false, int PAIR = 0>
+//
+// PADDED (with BT): A's rows are lda bytes apart, a multiple of 128, and hold zeros from K on, so that
+// a last step that is not whole needs no other way to load: B's rows at or past K read as
+// zero, the row being part of the VGPR offset in every step.
+template <int BM, int BN, int NW, bool BT = false, int PAIR = 0, bool PADDED = false>
 struct SlabLoader {
   static constexpr int LQA = BM / 8 / NW, LQB = BN / 8 / NW;  // direct-load instructions per wave per step
   static constexpr int PER = (LQA + LQB + kDmaGroups - 1) / kDmaGroups;
@@ -135,6 +138,7 @@ struct SlabLoader {
   static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "tile rows must split evenly over the wavefronts");
   static_assert(NW % 2 == 0, "the swizzle of a lane's load must not depend on its row group");
   static_assert(!BT || (BN >= 128 && BN <= 1024 && 128 % (RPB * NW) == 0), "BT slab shape");
+  static_assert(!PADDED || BT, "PADDED slabs are loaded as BT's");
   static_assert(PAIR == 0 || (!BT && PAIR % 16 == 0 && BN % (2 * PAIR) == 0), "PAIR slab shape");
   const uint8_t* A;
   const uint8_t* B;
@@ -194,6 +198,8 @@ struct SlabLoader {
       const int d = g * PER + e;
       if (d >= LQA + LQB) break;
       if (d < LQA) dma_lds16(ra, la + d * NW * 1024, voff + d * NW * 8 * lda, k0);
+      else if constexpr (PADDED)
+        dma_lds16(rb, lb + (d - LQA) * NW * 1024, (int)(voff_bt + (uint32_t)(((d - LQA) * NW * RPB + k0) * ldb)), 0);
       else if constexpr (BT)  // a full step: every K row exists, only the column needs the range check
         dma_lds16(rb, lb + (d - LQA) * NW * 1024, (int)voff_bt, ((d - LQA) * NW * RPB + k0) * ldb);
       else if constexpr (PAIR) {
@@ -207,7 +213,7 @@ struct SlabLoader {
   // registers; B likewise, or (BT) by direct loads whose VGPR offset carries
   // the row, so K rows past the end read as zero.
   __device__ __forceinline__ void ragged(uint8_t* dst, int kt, int t) const {
-    tile_load_zero_fill<BM, 64 * NW>(A, lda, m0, m_end, kt * kBK, K, dst, t);
+    tile_load_zero_fill<BM, 64 * NW>(A, K, m0, m_end, kt * kBK, K, dst, t);
     if constexpr (BT) {
       const uint32_t lb = lds_addr(dst + BM * kBK) + w * 1024;
 #pragma unroll
@@ -677,7 +683,7 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(
   const int64_t m_base = (int64_t)tm * BM, n_base = (int64_t)tn * OUT_BN;
   // K steps kt0 .. kt0 + nk - 1 (all of them, unless split), the last one ragged or not.
   int nk = (K + kBK - 1) / kBK, kt0 = 0;
-  bool ragged_k = (K % kBK) != 0;
+  bool ragged_k = (K % kBK) != 0 && !PRODUCT;
   if constexpr (EPI) {
     if (rq.split > 1) {
       const int per = (nk + rq.split - 1) / rq.split;
@@ -693,7 +699,8 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(
 
   int lda = 0;  // K
   if constexpr (PRODUCT) lda = rq.lda;
-  const SlabLoader<BM, BN, NW, BT, PAIR> slabs(A, m_base, M, B, n_base, N, K, w, lane, lda);
+  static_assert(!PRODUCT || BT, "a product on padded rows takes B [K x N]");
+  const SlabLoader<BM, BN, NW, BT, PAIR, PRODUCT> slabs(A, m_base, M, B, n_base, N, K, w, lane, lda);
   static_assert(!BT || !MXS, "MXFP8 operands are K-contiguous");
   // EPI, TILE_EPI: each XCD begins the K loop at another of its nturn full steps.  Rows are often
   // a power of two apart, and all the chip's tiles at the same K would ask the same few
@@ -712,7 +719,9 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(
       if (g == 0) MxScaleLoader<BM, BN, NW>(mxs, m_base, M, n_base, N, K, w, lane).issue(dst + SLABS, kt);
     }
   };
-  auto stage_ragged = [&](int kt, int stage) { slabs.ragged(smem + stage * STAGE, kt + kt0, t); };
+  auto stage_ragged = [&](int kt, int stage) {
+    if constexpr (!PRODUCT) slabs.ragged(smem + stage * STAGE, kt + kt0, t);
+  };
 
   // Fragment reads.  FP8 path (16x16x128): lane l takes row l & 15 of a
   // 16-row block and the 32-byte K slice l >> 4 (granules 2h, 2h+1).  bf16

@@ -36,42 +36,50 @@ constexpr int kShapeStep = 128;  // K bytes of a main-loop step
 struct TileChoice {
   int shape;  // 0: 256 x 256, 1: 128 x 128, 2: 64 x 128, 3: 64 x 128 in three stages
   int split;
+  double us;  // the estimate
 };
+
+struct TileCost {
+  int bm, bn;
+  double start, alone, each, odd;
+};
+inline const TileCost* tile_costs(bool fp8_cores) {
+  static constexpr TileCost kExact[4] = {{256, 256, 10.5, 2.13, 2.22, 1.04},
+                                         {128, 128, 6.9, 0.86, 0.72, 1.11},
+                                         {64, 128, 6.4, 0.60, 0.43, 1.20},
+                                         {64, 128, 6.6, 0.48, 0.49, 1.12}};
+  static constexpr TileCost kFp8[4] = {{256, 256, 9.0, 1.00, 1.27, 1.23},
+                                       {128, 128, 6.3, 0.77, 0.50, 1.23},
+                                       {64, 128, 5.7, 0.60, 0.34, 1.32},
+                                       {64, 128, 5.9, 0.39, 0.35, 1.27}};
+  return fp8_cores ? kFp8 : kExact;
+}
+
+// The estimate for one shape and split.
+inline double tile_time(const TileCost& c, int split, int64_t M, int64_t brows, int64_t K, int64_t cus) {
+  const int64_t steps = (K + kShapeStep - 1) / kShapeStep;
+  const int64_t tiles = ((M + c.bm - 1) / c.bm) * ((brows + c.bn - 1) / c.bn);
+  const double traffic = (double)split * M * brows * 4.0;
+  const int64_t load = (tiles * split + cus - 1) / cus;
+  const double busy = load * c.each * (K % kShapeStep ? c.odd : 1.0);
+  const double step = c.alone > busy ? c.alone : busy;
+  return c.start + (double)((steps + split - 1) / split) * step + (split > 1 ? 2.0 + 2.0 * traffic / 5.2e6 : 0.0);
+}
 
 // `brows`: rows of B; `cus`: compute units of the device.
 inline TileChoice choose_tile(int64_t M, int64_t brows, int64_t K, bool fp8_cores, size_t workspace_bytes,
                               int64_t cus) {
-  struct Cost {
-    int bm, bn;
-    double start, alone, each, odd;
-  };
-  static constexpr Cost kExact[4] = {{256, 256, 10.5, 2.13, 2.22, 1.04},
-                                     {128, 128, 6.9, 0.86, 0.72, 1.11},
-                                     {64, 128, 6.4, 0.60, 0.43, 1.20},
-                                     {64, 128, 6.6, 0.48, 0.49, 1.12}};
-  static constexpr Cost kFp8[4] = {{256, 256, 9.0, 1.00, 1.27, 1.23},
-                                   {128, 128, 6.3, 0.77, 0.50, 1.23},
-                                   {64, 128, 5.7, 0.60, 0.34, 1.32},
-                                   {64, 128, 5.9, 0.39, 0.35, 1.27}};
-  const Cost* costs = fp8_cores ? kFp8 : kExact;
+  const TileCost* costs = tile_costs(fp8_cores);
   const int64_t steps = (K + kShapeStep - 1) / kShapeStep;
-  TileChoice best{2, 1};
-  double least = 1e300;
+  TileChoice best{2, 1, 1e300};
   for (int i = 0; i < 4; ++i) {
-    const Cost& c = costs[i];
+    const TileCost& c = costs[i];
     const int64_t tiles = ((M + c.bm - 1) / c.bm) * ((brows + c.bn - 1) / c.bn);
     for (int split = 1; split <= 32 && split <= steps; split = split < 4 ? split + 1 : split + split / 2) {
       const double traffic = (double)split * M * brows * 4.0;
       if (split > 1 && (traffic > (double)workspace_bytes || tiles * split > 4 * cus)) break;
-      const int64_t load = (tiles * split + cus - 1) / cus;
-      const double busy = load * c.each * (K % kShapeStep ? c.odd : 1.0);
-      const double step = c.alone > busy ? c.alone : busy;
-      const double t = c.start + (double)((steps + split - 1) / split) * step +
-                       (split > 1 ? 2.0 + 2.0 * traffic / 5.2e6 : 0.0);
-      if (t < least) {
-        least = t;
-        best = TileChoice{i, split};
-      }
+      const double t = tile_time(c, split, M, brows, K, cus);
+      if (t < best.us) best = TileChoice{i, split, t};
     }
   }
   return best;

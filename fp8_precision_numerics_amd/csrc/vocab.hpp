@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "gemm_rounds.hpp"
 #include "vocab_epilogue.hpp"
 
 namespace fp8mi {
@@ -11,6 +12,8 @@ namespace fp8mi {
 // Pieces of the vocabulary are multiples of so many columns (the widest tile), but for the last.
 constexpr int64_t kPieceCols = 256;
 
+// Rows of codes are padded to whole steps of the products that read them.
+inline int64_t up128(int64_t n) { return (n + 127) & ~int64_t(127); }
 inline int64_t up16(int64_t n) { return (n + 15) & ~int64_t(15); }
 
 // Workspace of the forward for M rows and pieces of P columns: the target's logit and the
@@ -28,15 +31,14 @@ struct VocabOperands {
   int64_t M, K;
 };
 
-// Columns of a tile of the loss's product (N: columns of the piece), whose partials a tile each.
-int vocab_tile_cols(const VocabOperands& o, int64_t N, int accum);
-
-// The products with either epilogue (M > 0, N > 0), on columns [col, col + N) of the vocabulary.
-hipError_t launch_vocab_logits(const VocabOperands& o, int64_t col, int64_t N, const LossEpi& epi, int accum, hipStream_t stream);
+// The products with either epilogue (M > 0, N > 0), on columns [col, col + N) of the vocabulary;
+// *tiles: the loss's pairs a row.
+hipError_t launch_vocab_logits(const VocabOperands& o, int64_t col, int64_t N, const LossEpi& epi, int accum, int* tiles,
+                               hipStream_t stream);
 hipError_t launch_vocab_grad(const VocabOperands& o, int64_t col, int64_t N, const LogitGradEpi& epi, int accum, hipStream_t stream);
 
 // y [M x N] = (A [M x lda] B [K x N]) sinv_a sinv_b + add; K is any number, A's rows hold zeros from K
-// to the next multiple of 16; K * N < 2^31, N a multiple of 16; `workspace` for the parts of a split K.
+// to lda = up128(K); K * N < 2^31, N a multiple of 16; `workspace` for the parts of a split K.
 hipError_t launch_vocab_product(const uint8_t* A, int64_t lda, int fa, const uint8_t* B, int fb, int64_t M, int64_t N, int64_t K,
                                 const float* sinv_a, const float* sinv_b, const float* add, void* y, int ytype, int accum,
                                 void* workspace, size_t workspace_bytes, hipStream_t stream);

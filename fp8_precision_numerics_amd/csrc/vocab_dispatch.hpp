@@ -47,6 +47,7 @@ inline hipError_t vocab_fmt(const VocabOperands& o, const uint8_t* b, int64_t N,
   return vocab_shaped<kE5M2, kE5M2, MODE>(o, b, N, epi, st);
 }
 
+// One launch on columns [col, col + N).
 template <class EPI>
 inline hipError_t vocab_launch(const VocabOperands& o, int64_t col, int64_t N, const EPI& epi, int accum, hipStream_t st) {
   const uint8_t* b = o.b + col * o.K;

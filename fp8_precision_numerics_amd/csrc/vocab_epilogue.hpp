@@ -11,8 +11,9 @@
 // tile is staged.  The gradient's codes are packed four columns to a dword for the row-major tile
 // in LDS, and transposed between the four lanes of four consecutive rows for the other one.
 //
-// exp(z - m) is 2^((z - m) log2 e) (V_EXP_F32): the difference first, so its error is relative
-// to the difference, not to the logits.  An infinite or NaN logit makes its row's loss NaN; a
+// exp(z - m) is 2^(c s - m log2 e) (V_EXP_F32) with c the accumulator and s = sinv_a sinv_b log2 e:
+// one multiply-add, exact until its rounding, so the exponent is off by two roundings of |z| and |m|, far
+// inside what the product's own bound allows z.  An infinite or NaN logit makes its row's loss NaN; a
 // row whose target lies outside the vocabulary has no gradient, whatever its logits are.
 #pragma once
 
@@ -23,6 +24,8 @@ namespace fp8mi {
 
 
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+// exp(v * sc - m), where s = sc log2 e and t = -m log2 e.
+__device__ __forceinline__ float exp_of(float v, float s, float t) { return __builtin_amdgcn_exp2f(__builtin_fmaf(v, s, t)); }
 
 // Targets of the rows, int64 or int32.
 struct Targets {
@@ -88,7 +91,10 @@ struct LossEpi {
       want[i] = m < M ? targets.at(m, col0 + n_base) : -1;
     }
     __syncthreads();  // the LDS is free
-    auto rows = [&](auto edge) {
+    // `edge`: the tile crosses the last column; `neg`: sc is negative (or NaN), so that the largest logit is
+    // not the largest accumulator's.
+    auto rows = [&](auto edge, auto neg) {
+      const float s = sc * kLog2e;
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
         const int r = wm * WTM + i * BLK + (lane & (BLK - 1));
@@ -98,31 +104,44 @@ struct LossEpi {
 #pragma unroll
             for (int g = 0; g < G; ++g) {
               const int c = wn * WTN + j * BLK + block_col<BLK>(lane, g);
-              const v4f v = block_quad<BLK>(acc[i][j], g) * sc;
+              const v4f v = block_quad<BLK>(acc[i][j], g);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) f((decltype(edge)::value && c + e >= cols_left) ? -__builtin_inff() : v[e], c + e);
+              for (int e = 0; e < 4; ++e) {
+                if (decltype(edge)::value && c + e >= cols_left) continue;
+                f(v[e], c + e);
+              }
             }
         };
         float top = -__builtin_inff();
-        each([&](float x, int) { top = __builtin_fmaxf(top, x); });
+        if constexpr (decltype(neg)::value) {
+          each([&](float v, int) { top = __builtin_fmaxf(top, v * sc); });
+        } else {
+          each([&](float v, int) { top = __builtin_fmaxf(top, v); });
+          // -inf where the wave has no column, whatever sc is
+          top = top == -__builtin_inff() ? top : top * sc;
+        }
         top = lanes_max<BLK>(top);
-        const float ref = reference(top);
+        const float t = -reference(top) * kLog2e;
         float sum = 0.0f;
-        each([&](float x, int) { sum += exp_of(x - ref); });
+        each([&](float v, int) { sum += exp_of(v, s, t); });
         sum = lanes_sum<BLK>(sum);
         if (lane < BLK) part[wn * BM + r] = make_float2(top, sum);
         // few waves hold the target of any of their rows
-        const int t = want[i];
-        const bool here = t >= wn * WTN && t < (wn + 1) * WTN && t < cols_left;
+        const int w0 = want[i];
+        const bool here = w0 >= wn * WTN && w0 < (wn + 1) * WTN && w0 < cols_left;
         if (__any(here)) {
-          each([&](float x, int c) {
-            if (here && c == t) mine[m_base + r] = x;
+          each([&](float v, int c) {
+            if (here && c == w0) mine[m_base + r] = v * sc;
           });
         }
       }
     };
-    if (cols_left == BN) rows(std::false_type{});
-    else rows(std::true_type{});
+    auto with_edge = [&](auto neg) {
+      if (cols_left == BN) rows(std::false_type{}, neg);
+      else rows(std::true_type{}, neg);
+    };
+    if (__builtin_expect(sc >= 0.0f, 1)) with_edge(std::false_type{});
+    else with_edge(std::true_type{});
     __syncthreads();
     const int t = threadIdx.x;
     if (t < BM && m_base + t < M) {
@@ -208,14 +227,14 @@ struct LogitGradEpi {
   const float* lse;    // [M]
   const float* dloss;  // [M]
   const float* scale;
-  uint8_t* q;          // [M x ldq] codes of d, zeros from column N to ldq; or null
+  uint8_t* q;          // [M x ldq] codes of d, zeros from column N to the next multiple of 128; or null
   uint8_t* q_t;        // [N x ldt] of its transpose, zeros from M to ldt; or null
   uint32_t* amax_bits; // cleared beforehand; may be null
   unsigned long long* sat;
   Targets targets;
   int64_t vocab;       // a row whose target lies outside has no gradient
   int64_t col0;
-  int64_t ldq, ldt;    // multiples of 16, less than 16 above N and M
+  int64_t ldq, ldt;    // multiples of 128; ldt less than 128 above M
   int fmt;
 
   template <int BM, int BN, int WM, int WN, int BLK, class ACC>
@@ -234,66 +253,101 @@ struct LogitGradEpi {
     const int cols_left = (int)(N - n_base < BN ? N - n_base : BN);
     const CodeTile<BN> rows_tile{smem};
     const CodeTile<BM> cols_tile{smem + BM * BN};
-    const float out = *scale;
     const uint32_t pair = 0x0C0C0400u + 0x0101u * (lane & 3);  // bytes 2 and 3 are not used (constant 0)
-    constexpr int kDead = -2;  // a row without a gradient: selected, not multiplied away, since its logits may be NaN
+    const float out = *scale, s = sc * kLog2e;
+    constexpr float kMax = Fp8Traits<FMT>::max_value;
+    // A row without a gradient (past the edge, or its target outside) has its codes masked and takes no part
+    // in the statistics: a factor of 0 would not do, since its logits may be NaN.
     int want[FM];
-    float top[FM], grad[FM];   // lse and dloss
+    float t[FM], grad[FM];  // -lse log2 e, and dloss
+    bool live[FM];
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
       const int64_t m = m_base + wm * WTM + i * BLK + (lane & (BLK - 1));
-      const bool live = m < M && targets.inside(m, vocab);
-      want[i] = live ? targets.at(m, col0 + n_base) : kDead;
-      top[i] = live ? lse[m] : 0.0f;
-      grad[i] = live ? dloss[m] : 0.0f;
+      live[i] = m < M && targets.inside(m, vocab);
+      want[i] = live[i] ? targets.at(m, col0 + n_base) : -1;
+      t[i] = live[i] ? lse[m] * -kLog2e : 0.0f;
+      grad[i] = live[i] ? dloss[m] : 0.0f;
     }
     __syncthreads();  // the LDS is free
     LaneStats st;
-    const bool with_sat = sat != nullptr;
+    const bool count = sat != nullptr;
+    auto rows = [&](auto edge) {
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      const int r = wm * WTM + i * BLK + (lane & (BLK - 1));
-      const bool dead = want[i] == kDead;
-      const bool here = want[i] >= wn * WTN && want[i] < (wn + 1) * WTN;
-      const bool any = __any(here);
+      for (int i = 0; i < FM; ++i) {
+        const int r = wm * WTM + i * BLK + (lane & (BLK - 1));
+        const uint32_t mask = live[i] ? 0xFFFFFFFFu : 0u;
+        const bool here = want[i] >= wn * WTN && want[i] < (wn + 1) * WTN;
+        const bool any = __any(here);
+        float top = 0.0f;  // the largest |exp(z - lse) - [target]| of the row's values
 #pragma unroll
-      for (int j = 0; j < FN; ++j)
+        for (int j = 0; j < FN; ++j)
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-          const int c = wn * WTN + j * BLK + block_col<BLK>(lane, g);
-          const v4f v = block_quad<BLK>(acc[i][j], g) * sc;
-          float d[4];
+          for (int g = 0; g < G; ++g) {
+            const int c = wn * WTN + j * BLK + block_col<BLK>(lane, g);
+            const v4f v = block_quad<BLK>(acc[i][j], g);
+            float p[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) d[e] = exp_of(v[e] - top[i]);
-          if (any) {
+            for (int e = 0; e < 4; ++e) p[e] = exp_of(v[e], s, t[i]);
+            if (any) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) d[e] -= c + e == want[i] ? 1.0f : 0.0f;
+              for (int e = 0; e < 4; ++e) p[e] -= c + e == want[i] ? 1.0f : 0.0f;
+            }
+            if constexpr (decltype(edge)::value) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) p[e] = c + e >= cols_left ? 0.0f : p[e];
+            }
+            float m = __builtin_elementwise_maximum(__builtin_fabsf(p[0]), __builtin_fabsf(p[1]));
+            m = __builtin_elementwise_maximum(__builtin_elementwise_maximum(__builtin_fabsf(p[2]), __builtin_fabsf(p[3])), m);
+            top = __builtin_elementwise_maximum(top, m);
+            // Roundings are monotone: where the largest stays inside, all do, and none is NaN.
+            float d[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d[e] = p[e] * grad[i] * out;
+            uint32_t word;
+            if (__builtin_expect(__builtin_fabsf(m * grad[i] * out) <= kMax, 1)) {
+              word = cvt_pk<FMT, true>(d[2], d[3], cvt_pk<FMT, false>(d[0], d[1], 0u));
+            } else {
+              word = encode4<FMT>(d[0], d[1], d[2], d[3]);
+              if (count && live[i]) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) st.sat += __builtin_fabsf(d[e]) > kMax ? 1u : 0u;
+              }
+            }
+            word &= mask;
+            if (q) *reinterpret_cast<uint32_t*>(rows_tile.at(r, c)) = word;
+            if (q_t) *reinterpret_cast<uint32_t*>(cols_tile.at(c + (lane & 3), r & ~3)) = transpose_quad(word, pair);
           }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) d[e] = (dead || c + e >= cols_left) ? 0.0f : d[e] * grad[i];
-          const uint32_t word = encode4_stats<FMT>(d, out, with_sat, st);
-          if (q) *reinterpret_cast<uint32_t*>(rows_tile.at(r, c)) = word;
-          if (q_t) *reinterpret_cast<uint32_t*>(cols_tile.at(c + (lane & 3), r & ~3)) = transpose_quad(word, pair);
-        }
-    }
+        if (live[i]) st.max = __builtin_elementwise_maximum(st.max, __builtin_fabsf(top * grad[i]));
+      }
+    };
+    if (cols_left == BN) rows(std::false_type{});
+    else rows(std::true_type{});
     __syncthreads();
-    const int t = threadIdx.x;
+    const int tid = threadIdx.x;
     if (q) {
       constexpr int GR = BN / 16;
-      for (int idx = t; idx < BM * GR; idx += NT) {
+      for (int idx = tid; idx < BM * GR; idx += NT) {
         const int r = idx / GR, byte = idx % GR * 16;
         if (m_base + r >= M) break;  // rows are visited in order
-        if (n_base + byte < ldq)
+        if (n_base + byte < ((N + 127) & ~int64_t(127)))
           *reinterpret_cast<uint4*>(q + (m_base + r) * ldq + n_base + byte) = *reinterpret_cast<const uint4*>(rows_tile.at(r, byte));
       }
     }
     if (q_t) {
       constexpr int GR = BM / 16;
-      for (int idx = t; idx < BN * GR; idx += NT) {
+      for (int idx = tid; idx < BN * GR; idx += NT) {
         const int r = idx / GR, byte = idx % GR * 16;
         if (r >= cols_left) break;
         if (m_base + byte < ldt)
           *reinterpret_cast<uint4*>(q_t + (n_base + r) * ldt + m_base + byte) = *reinterpret_cast<const uint4*>(cols_tile.at(r, byte));
+      }
+      if constexpr (BM < 128) {  // rows' padding past the last tile
+        static_assert(BM == 64, "half a step");
+        if (m_base + 2 * BM == ldt && m_base + BM >= M) {
+          for (int idx = tid; idx < cols_left * GR; idx += NT)
+            *reinterpret_cast<uint4*>(q_t + (n_base + idx / GR) * ldt + m_base + BM + idx % GR * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
       }
     }
     if (amax_bits || sat) {
@@ -303,24 +357,6 @@ struct LogitGradEpi {
       stats.sat = sat;
       publish_epilogue_stats(stats, st, reinterpret_cast<uint32_t*>(smem));
     }
-  }
-
-  // encode8 (stats.hpp) on four values.
-  template <int FMT>
-  static __device__ __forceinline__ uint32_t encode4_stats(const float* d, float scale, bool count, LaneStats& st) {
-    float m = __builtin_elementwise_maximum(__builtin_fabsf(d[0]), __builtin_fabsf(d[1]));
-    m = __builtin_elementwise_maximum(__builtin_elementwise_maximum(__builtin_fabsf(d[2]), __builtin_fabsf(d[3])), m);
-    st.max = __builtin_elementwise_maximum(st.max, m);
-    float p[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) p[e] = d[e] * scale;
-    if (__builtin_expect(__builtin_fabsf(m * scale) <= Fp8Traits<FMT>::max_value, 1))
-      return cvt_pk<FMT, true>(p[2], p[3], cvt_pk<FMT, false>(p[0], p[1], 0u));
-    if (count) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) st.sat += __builtin_fabsf(p[e]) > Fp8Traits<FMT>::max_value ? 1u : 0u;
-    }
-    return encode4<FMT>(p[0], p[1], p[2], p[3]);
   }
 };
 template <>

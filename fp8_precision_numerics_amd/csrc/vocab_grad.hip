@@ -19,7 +19,7 @@ int64_t up256(int64_t n) { return (n + 255) & ~int64_t(255); }
 
 // The codes both ways for pieces of P columns, and the fp32 sums of dx where there are several.
 int64_t grad_bytes(int64_t M, int64_t V, int64_t K, int64_t P) {
-  return up256(M * up16(P)) + up256(P * up16(M)) + (P < V ? up256(M * K * 4) : 0);
+  return up256(M * up128(P)) + up256(P * up128(M)) + (P < V ? up256(M * K * 4) : 0);
 }
 
 // The longest piece that the products' offsets reach.
@@ -28,11 +28,42 @@ int64_t most_columns(int64_t K) {
   return most < (int64_t(1) << 22) ? most : (int64_t(1) << 22);
 }
 
+// Few rows: the forward's products were exact, and the gradient's have to be of the same logits.
+int logits_mode(int64_t M, int accum) { return M <= kFewRows ? (int)kAccumExact : accum; }
+
+// Estimate of the passes over pieces of P columns, in microseconds: the three products of each, and its
+// passes over dx's fp32 sums.
+double pieces_time(const VocabOperands& o, int64_t V, int64_t P, int accum) {
+  const int64_t cus = persistent_groups(1);
+  const bool fp8 = accum == kAccumMfma8;
+  double t = 0.0;
+  for (int64_t col = 0; col < V; col += P) {
+    const int64_t n = V - col < P ? V - col : P;
+    double one = plan_rounds(o.M, n, o.K, logits_mode(o.M, accum) == kAccumMfma8, 0, cus).us + plan_rounds(o.K, o.M, n, fp8, 0, cus).us +
+                 plan_rounds(o.K, n, o.M, fp8, 0, cus).us;
+    if (P < V) one += 8.0 * o.M * o.K / 5.0e6;
+    if (n == P && V / P > 1) {  // all whole pieces at once
+      t += one * (double)(V / P);
+      col += (V / P - 1) * P;
+    } else {
+      t += one;
+    }
+  }
+  return t;
+}
+
 }  // namespace
 
 hipError_t launch_vocab_grad(const VocabOperands& o, int64_t col, int64_t N, const LogitGradEpi& epi, int accum, hipStream_t stream) {
-  // Few rows: the forward's products were exact, and these have to be of the same logits.
-  return vocab_launch(o, col, N, epi, o.M <= kFewRows ? (int)kAccumExact : accum, stream);
+  const int mode = logits_mode(o.M, accum);
+  const int64_t first = plan_rounds(o.M, N, o.K, mode == kAccumMfma8, 0, persistent_groups(1)).first;
+  hipError_t status = vocab_launch(o, col, first, epi, mode, stream);
+  if (status != hipSuccess || first == N) return status;
+  LogitGradEpi rest = epi;
+  rest.col0 += first;
+  if (rest.q) rest.q += first;
+  if (rest.q_t) rest.q_t += first * epi.ldt;
+  return vocab_launch(o, col + first, N - first, rest, mode, stream);
 }
 
 size_t vocab_workspace(int64_t M, int64_t V, int64_t K, int64_t pieces) {
@@ -54,7 +85,7 @@ hipError_t launch_vocab_cross_entropy_backward(const VocabOperands& o, int64_t V
     const hipError_t e = launch_clear_stats(amax, sat, stream);
     if (e != hipSuccess) return e;
   }
-  const int64_t M = o.M, K = o.K, ldt = up16(M);
+  const int64_t M = o.M, K = o.K, ldt = up128(M);
   const int64_t dwsize = dwtype == kBF16 ? 2 : 4;
   if (M == 0) return dw ? launch_fill_rows(nullptr, dw, V * K * dwsize / 16, stream) : hipSuccess;
   // The longest piece that fits, then pieces of equal length.
@@ -64,12 +95,22 @@ hipError_t launch_vocab_cross_entropy_backward(const VocabOperands& o, int64_t V
     int64_t fit = ((int64_t)workspace_bytes - up256(M * K * 4) - 512) / (M + ldt) / kPieceCols * kPieceCols;
     fit = fit < kPieceCols ? kPieceCols : fit;  // the entry point has seen to that much
     fit = fit < most ? fit : most;
-    const int64_t pieces = (V + fit - 1) / fit;
-    P = up256((V + pieces - 1) / pieces);
+    // As few pieces as fit, or up to four more where the estimate prefers them: tiles that fill whole rounds of
+    // the compute units are worth another pass over dx's sums (8192 x 4096 x 65536 on the FP8 cores over 512 MiB: four pieces of 16384 columns 5.21 ms, the three that fit 5.40).
+    const int64_t least = (V + fit - 1) / fit;
+    double best = 1e300;
+    for (int64_t pieces = least; pieces <= least + 4; ++pieces) {
+      const int64_t p = up256((V + pieces - 1) / pieces);
+      const double t = pieces_time(o, V, p, accum);
+      if (t < best) {
+        best = t;
+        P = p;
+      }
+    }
   }
   uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
   uint8_t* const q = ws;
-  uint8_t* const q_t = q + up256(M * up16(P));
+  uint8_t* const q_t = q + up256(M * up128(P));
   uint8_t* rest = q_t + up256(P * ldt);
   // An fp32 dx is its own sum.
   float* sum = dxtype == kF32 ? reinterpret_cast<float*>(dx) : reinterpret_cast<float*>(rest);
@@ -78,12 +119,12 @@ hipError_t launch_vocab_cross_entropy_backward(const VocabOperands& o, int64_t V
   for (int64_t col = 0; col < V; col += P) {
     const int64_t n = V - col < P ? V - col : P;
     const LogitGradEpi epi{lse, dloss, scale, dx ? q : nullptr, dw ? q_t : nullptr, reinterpret_cast<uint32_t*>(amax), sat, targets,
-                           V, col, up16(n), ldt, fmt};
+                           V, col, up128(n), ldt, fmt};
     hipError_t e = launch_vocab_grad(o, col, n, epi, accum, stream);
     if (e != hipSuccess) return e;
     if (dx) {
       const bool first = col == 0, last = col + n >= V;
-      e = launch_vocab_product(q, up16(n), fmt, o.b + col * K, o.fb, M, K, n, scale_inv, o.sinv_b, first ? nullptr : sum,
+      e = launch_vocab_product(q, up128(n), fmt, o.b + col * K, o.fb, M, K, n, scale_inv, o.sinv_b, first ? nullptr : sum,
                                last ? dx : (void*)sum, last ? dxtype : (int)kF32, accum, rest, left, stream);
       if (e != hipSuccess) return e;
     }

@@ -73,21 +73,30 @@ __global__ __launch_bounds__(256) void vocab_join_kernel(JoinArgs a) {
   if (a.loss) a.loss[row] = a.targets.inside(row, a.vocab) ? lse - a.mine[row] : 0.0f;
 }
 
-// 16 rows a workgroup where they make one for every other compute unit (whole lines of the partials are read),
-// otherwise a row each.
+// As many rows a workgroup (up to a line of the partials) as leave one for about every second compute unit.
 void join_launch(const JoinArgs& a, hipStream_t st) {
   if (a.M >= 2048) hipLaunchKernelGGL(vocab_join_kernel<16>, dim3((unsigned)((a.M + 15) / 16)), dim3(256), 0, st, a);
+  else if (a.M >= 512) hipLaunchKernelGGL(vocab_join_kernel<4>, dim3((unsigned)((a.M + 3) / 4)), dim3(256), 0, st, a);
   else hipLaunchKernelGGL(vocab_join_kernel<1>, dim3((unsigned)a.M), dim3(256), 0, st, a);
 }
 
 }  // namespace
 
-int vocab_tile_cols(const VocabOperands& o, int64_t N, int accum) {
-  return vocab_shape(o, N, accum) == 0 ? 256 : 128;
-}
-
-hipError_t launch_vocab_logits(const VocabOperands& o, int64_t col, int64_t N, const LossEpi& epi, int accum, hipStream_t stream) {
-  return vocab_launch(o, col, N, epi, accum, stream);
+hipError_t launch_vocab_logits(const VocabOperands& o, int64_t col, int64_t N, const LossEpi& epi, int accum, int* tiles,
+                               hipStream_t stream) {
+  const int64_t first = plan_rounds(o.M, N, o.K, accum == kAccumMfma8, 0, persistent_groups(1)).first;
+  LossEpi e = epi;
+  *tiles = 0;
+  for (int64_t at = 0; at < N;) {
+    const int64_t n = at == 0 ? first : N - first, wide = vocab_shape(o, n, accum) == 0 ? 256 : 128;
+    e.col0 = epi.col0 + at;
+    e.partials = epi.partials + (int64_t)*tiles * o.M;
+    const hipError_t status = vocab_launch(o, col + at, n, e, accum, stream);
+    if (status != hipSuccess) return status;
+    *tiles += (int)((n + wide - 1) / wide);
+    at += n;
+  }
+  return hipSuccess;
 }
 
 size_t vocab_loss_bytes(int64_t M, int64_t P) {
@@ -123,9 +132,7 @@ hipError_t launch_vocab_cross_entropy(const VocabOperands& o, int64_t V, const T
       const int64_t fit = slots * 128;  // the narrower tiles'
       if (n > fit) n = fit / kPieceCols * kPieceCols;
       epi.col0 = col;
-      e = launch_vocab_logits(o, col, n, epi, accum, stream);
-      const int cols = vocab_tile_cols(o, n, accum);
-      j.tiles = (int)((n + cols - 1) / cols);
+      e = launch_vocab_logits(o, col, n, epi, accum, &j.tiles, stream);
     }
     if (e != hipSuccess) return e;
     j.first = col == 0;

@@ -17,6 +17,7 @@ import pytest
 import torch
 
 import fp8_precision_numerics_amd as fm
+import vocab_cases
 from gpu_helpers import announce, device, mfma8_bound
 from oracle import codec, gemm, model_ends as me, scaling
 from test_gpu_feed_forward import EW, HALF, check_close, d64, rand_codes, scalar, u8
@@ -179,11 +180,7 @@ def test_backward(M, V, K, accum, fx, fw, fmt, types, pieces):
         assert torch.equal(dx, out[0])
 
 
-# Sizes that the estimate of gemm_shape.hpp gives each tile shape: 64 x 128, 128 x 128, 256 x 256, with edges.
-LARGE = [(200, 3001, 1040), (1023, 8190, 2064), (2047, 8201, 2048), (8192, 1111, 528)]
-
-
-@pytest.mark.parametrize("M,V,K", LARGE)
+@pytest.mark.parametrize("M,V,K", vocab_cases.LOGITS)
 @pytest.mark.parametrize("accum", ["exact", "mfma_fp8"])
 def test_large(M, V, K, accum):
     announce(f"cross entropy large {M}x{V}x{K} {accum}")

@@ -89,7 +89,7 @@ def test_embedding_workspace():
     assert fm.embedding_workspace_bytes(1 << 20, 64) == 4 * (4 << 20) + 4096 * 512
 
 
-LEAST = 2 * 256 * 32 + 32 * 64 * 4           # 32 rows: codes both ways for 256 columns, and dx's sums
+LEAST = 256 * 32 + 256 * 128 + 32 * 64 * 4   # 32 rows: codes both ways for 256 columns (rows padded to 128), and dx's sums
 VOCAB = dict(x=P, fx=0, w=P, fw=0, M=32, V=1000, K=64, sx=P, sw=P, targets=P, itype=1, loss=P, lse=P, accum=0, ws=P, ws_bytes=32 * 4 + 32 * 8 + 32 * 8 * 2, stream=None)
 VOCAB_BACK = dict(x=P, fx=0, w=P, fw=0, M=32, V=1000, K=64, sx=P, sw=P, targets=P, itype=0, lse=P, dloss=P, fmt=1, scale=P, inv=P, dx=P, dxtype=1, dw=P, dwtype=0,
                   amax=None, sat=None, accum=1, ws=P, ws_bytes=LEAST, stream=None)
@@ -117,12 +117,11 @@ def test_vocab_backward_refusals(lib, want, change):
 def test_vocab_workspace():
     assert fm.vocab_workspace_bytes(0, 1000, 64) == 0 and fm.vocab_workspace_bytes(32, 0, 64) == 0 and fm.vocab_workspace_bytes(32, 1000, (1 << 22) + 16) == 0
     assert fm.vocab_workspace_bytes(32, 1000, 64, 0) == LEAST and fm.vocab_workspace_bytes(32, 1000, 64, 4) == LEAST
-    # one piece: codes of 1000 columns, rows of 1008 and of 32, each rounded up to 256
-    assert fm.vocab_workspace_bytes(32, 1000, 64) == 32256 + 32000
+    # one piece: codes of 1000 columns, rows of 1024 and of 128, each rounded up to 256
+    assert fm.vocab_workspace_bytes(32, 1000, 64) == 32768 + 128000
     # a whole vocabulary of few columns needs no sums of dx, and less than a piece with them
-    assert fm.vocab_workspace_bytes(16, 300, 64, 0) == fm.vocab_workspace_bytes(16, 300, 64) == 4864 + 4864
-    # a hidden size this small leaves the forward's pairs the larger
-    assert fm.vocab_workspace_bytes(1, 100000, 16, 1) == 100096 + 256 * ((16 * 100000 + 255) // 256)
+    assert fm.vocab_workspace_bytes(16, 300, 1024, 0) == fm.vocab_workspace_bytes(16, 300, 1024) == 16 * 384 + 300 * 128
+    assert fm.vocab_workspace_bytes(16, 300, 64, 0) == 16 * 256 + 256 * 128 + 16 * 64 * 4
 
 
 @pytest.mark.parametrize("name", ["layer", "layer_back", "embed", "embed_back", "vocab", "vocab_back"])
