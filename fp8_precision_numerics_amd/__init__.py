@@ -4,8 +4,9 @@ AMD Instinct MI355X (gfx950).
 The compute path is the C-ABI library libfp8mi.so (include/fp8mi.h) built from
 the HIP sources under csrc/; this package is its Python binding (argument
 marshalling), a holder for one tensor's delayed-scaling buffers, and the
-sequencing of one FP8 linear layer (Fp8Linear) and of one gated feed-forward
-block (Fp8FeedForward), forward and backward.
+sequencing of one FP8 linear layer (Fp8Linear), of one gated feed-forward
+block (Fp8FeedForward) and of a model's two ends (Fp8VocabHead: embedding, last
+norm and loss), forward and backward.
 """
 
 from ._binding import (ACCUM_EXACT, ACCUM_MFMA_FP8, BF16, E4M3, E5M2, EXPORTED_SYMBOLS, F32, QUANTIZE_WORKSPACE_BYTES, Fp8Error, embedding_workspace_bytes, fp8_amax_update, fp8_gemm,  # noqa: F401
@@ -14,3 +15,4 @@ from ._binding import (ACCUM_EXACT, ACCUM_MFMA_FP8, BF16, E4M3, E5M2, EXPORTED_S
 from .feed_forward import Fp8FeedForward  # noqa: F401
 from .linear import Fp8Linear  # noqa: F401
 from .state import DelayedScalingState, Recipe  # noqa: F401
+from .vocab_head import Fp8VocabHead  # noqa: F401

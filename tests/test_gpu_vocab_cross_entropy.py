@@ -104,40 +104,41 @@ def gradient(p, accum, lse, rows, cols, fmt, scale):
     return d, np.where(live, np.abs(g) * (prob * np.expm1(B) + EW * (prob * (1 + np.abs(z - l)) + hit)), 0.0)
 
 
-def check_product(got, d, err, other, fo, so, scale, fmt, accum, what):
+def check_product(got, d, err, other, fo, so, scale, inv, fmt, accum, what):
     """got = codes(d) · other / scale, d [R x N], other: codes [N x K] as a GPU tensor."""
     r = gemm.requant_bracket(d, err, np.float32(scale), fmt)
     q = scaling.quantize(d.astype(np.float32), np.float32(scale), fmt)[0]
     v = codec.decode(q, fmt)
     open_ = np.maximum(r["hi"] - v, v - r["lo"])
     b = decoded(other, fo).cpu().numpy()
-    inv = np.float64(np.float32(1 / scale)) * so.item()
+    inv32, inv = np.float32(inv), np.float64(np.float32(inv)) * so.item()
     want = v @ b * inv
     mag = np.abs(v) @ np.abs(b) * inv
     if accum == "exact":
         bound = 1e-5 * mag
     else:  # any n: the run of 8 is completed with zeros
         n = (-v.shape[1]) % 8
-        bound = mfma8_bound(np.pad(q, ((0, 0), (0, n))), fmt, np.pad(u8(other).T, ((0, 0), (0, n))), fo, np.float32(1 / scale), so.item())
+        bound = mfma8_bound(np.pad(q, ((0, 0), (0, n))), fmt, np.pad(u8(other).T, ((0, 0), (0, n))), fo, inv32, so.item())
     got = d64(got)
     half = HALF[what[1]]
     check_close(got, want, bound + open_ @ np.abs(b) * inv + half * 1.001 * np.abs(want) + 2.0 ** -24 * mag, what[0])
 
 
-def check_backward(p, accum, lse, out, fmt, scale, rows=None, cols=None, types=(torch.float32, torch.float32)):
+def check_backward(p, accum, lse, out, fmt, scale, rows=None, cols=None, types=(torch.float32, torch.float32), inv=None):
     dx, dw, amax, sat = out
+    inv = 1 / scale if inv is None else inv.item()
     if dx is not None:
         d, err = gradient(p, accum, lse, rows, None, fmt, scale)
-        check_product(dx if rows is None else dx[rows], d, err, p.w, p.fw, p.sw, scale, fmt, accum, ("dx", types[0]))
+        check_product(dx if rows is None else dx[rows], d, err, p.w, p.fw, p.sw, scale, inv, fmt, accum, ("dx", types[0]))
         if rows is None and amax is not None:
             top = np.abs(d)
             assert (top - err).max() <= amax.item() * (1 + 1e-6) and amax.item() <= (top + err).max() * (1 + 1e-6)
             limit = codec.FORMATS[fmt].max_value
             lo, hi = np.sum((top - err) * scale * (1 - 1e-6) > limit), np.sum((top + err) * scale * (1 + 1e-6) > limit)
-            assert lo <= sat.item() <= hi
+            assert sat is None or lo <= sat.item() <= hi
     if dw is not None:
         d, err = gradient(p, accum, lse, None, cols, fmt, scale)
-        check_product(dw if cols is None else dw[cols], d.T, err.T, p.x, p.fx, p.sx, scale, fmt, accum, ("dw", types[1]))
+        check_product(dw if cols is None else dw[cols], d.T, err.T, p.x, p.fx, p.sx, scale, inv, fmt, accum, ("dw", types[1]))
 
 
 SMALL = [(1, 1, 16), (1, 1000, 16), (3, 17, 48), (5, 2, 4096), (16, 300, 64), (17, 257, 128), (33, 2500, 80), (100, 1000, 1040), (130, 515, 256), (250, 127, 144)]
