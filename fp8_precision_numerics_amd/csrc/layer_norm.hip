@@ -10,7 +10,10 @@
 //   dh = r (g - mean_n g - a mean_n(g a)) + dresidual
 //   dx = round(dh),  dbranch = round(drop'(dh)),  dweight_n = sum_m dy a,  dbias_n = sum_m dy
 //
-// HBM-bound, as the root-mean-square norm (rms_norm.hip), with its arrangement: a row
+// HBM-bound; measured on MI355X (bf16, residual, dropout): 8192 x 4096 with amax 44-45.5 us (235 MB, 5.2-5.3 TB/s, a copy's
+// rate), its gradient with both sums and the branch's 65.4 us (336 MB, 5.1 TB/s); 1777 x 1040 fp32 gradient 12 us, of which
+// the second launch takes 4; one row of 4096 4.0 us a call.
+// The arrangement is the root-mean-square norm's (rms_norm.hip): a row
 // stays in registers from the load to the encode, so x and the residual are read
 // once and the variance is the sum of (h - m)^2 of values that are there, not a
 // difference of two large sums.  A row of up to 1024 values belongs to a wavefront,
@@ -23,6 +26,8 @@
 // memory traffic.
 // Sums are fp32: per lane over its octets, then across lanes, so a term of a row of
 // up to 16384 values passes through at most about 40 roundings.
+#include <type_traits>
+
 #include "column_sums.hpp"
 #include "launch.hpp"
 #include "model_ends.hpp"
@@ -83,9 +88,9 @@ __device__ __forceinline__ void layer_encode(const LayerArgs& a, const Octet<XT>
 }
 
 // WG: a row per workgroup, whose size fits the row; otherwise a row per wavefront, four
-// side by side.
-template <int XT, int FMT, bool STATS, bool WG, int VPT>
-__global__ __launch_bounds__(WG ? 1024 : 256) void layernorm_kernel(LayerArgs a) {
+// side by side.  PRE: a row is requested while the one before it is worked on.
+template <int XT, int FMT, bool STATS, bool WG, int VPT, bool PRE>
+__global__ __launch_bounds__(WG ? (PRE ? 512 : 1024) : 256) void layernorm_kernel(LayerArgs a) {
   __shared__ float buf[2][kMaxWaves];
   const int TPR = WG ? blockDim.x : 64, RPB = WG ? 1 : 4;
   const int t = WG ? threadIdx.x : threadIdx.x & 63;
@@ -104,23 +109,35 @@ __global__ __launch_bounds__(WG ? 1024 : 256) void layernorm_kernel(LayerArgs a)
       if (a.bias) bs[v].load(a.bias, t + v * TPR);
     }
   }
-  LaneStats st;
-  int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * RPB + (WG ? 0 : threadIdx.x >> 6); row < a.rows; row += (int64_t)gridDim.x * RPB) {
-    const int64_t base = row * octets;
-    Octet<XT> h[VPT];
+  auto request = [&](int64_t row, Octet<XT>* h, Octet<XT>* res) {
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       h[v].clear();
-      if (t + v * TPR < octets) h[v].load_nt(a.x, base + t + v * TPR);
+      res[v].clear();
+      if (row < a.rows && t + v * TPR < octets) {
+        h[v].load_nt(a.x, row * octets + t + v * TPR);
+        if (a.residual) res[v].load_nt(a.residual, row * octets + t + v * TPR);
+      }
     }
-    if (join) {
-      Octet<XT> res[VPT];
+  };
+  LaneStats st;
+  int turn = 0;
+  Octet<XT> nh[VPT], nres[VPT];
+  if constexpr (PRE) request((int64_t)blockIdx.x * RPB + (WG ? 0 : threadIdx.x >> 6), nh, nres);
+  for (int64_t row = (int64_t)blockIdx.x * RPB + (WG ? 0 : threadIdx.x >> 6); row < a.rows; row += (int64_t)gridDim.x * RPB) {
+    const int64_t base = row * octets;
+    Octet<XT> h[VPT], res[VPT];
+    if constexpr (PRE) {
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
-        res[v].clear();
-        if (a.residual && t + v * TPR < octets) res[v].load_nt(a.residual, base + t + v * TPR);
+        h[v] = nh[v];
+        res[v] = nres[v];
       }
+      request(row + (int64_t)gridDim.x * RPB, nh, nres);
+    } else {
+      request(row, h, res);
+    }
+    if (join) {
 #pragma unroll
       for (int v = 0; v < VPT; ++v) join_branch<XT>(h[v], res[v], a.residual != nullptr, drop, base + t + v * TPR);
     }
@@ -246,24 +263,24 @@ struct LayerBackArgs {
   int64_t pitch;
   int64_t rows, cols;
   Dropout drop;
+  int lanes;          // threads a row: 64, or a multiple of it; a workgroup has blockDim.x / lanes rows side by side
 };
 
-// Two sums over the lanes of a row at once; as row_sum.
+// Two sums over the lanes of a row at once; as row_sum, of the row's `waves` waves from wave `w0` of the workgroup on.
 template <bool WG>
-__device__ __forceinline__ float2 row_sum2(float2 v, float2 (*buf)[kMaxWaves], int turn) {
+__device__ __forceinline__ float2 row_sum2(float2 v, float2 (*buf)[kMaxWaves], int turn, int w0, int waves) {
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) {
     v.x += __shfl_xor(v.x, off, 64);
     v.y += __shfl_xor(v.y, off, 64);
   }
   if constexpr (WG) {
-    const int waves = blockDim.x >> 6;
     if ((threadIdx.x & 63) == 0) buf[turn & 1][threadIdx.x >> 6] = v;
     __syncthreads();
-    v = buf[turn & 1][0];
+    v = buf[turn & 1][w0];
     for (int w = 1; w < waves; ++w) {
-      v.x += buf[turn & 1][w].x;
-      v.y += buf[turn & 1][w].y;
+      v.x += buf[turn & 1][w0 + w].x;
+      v.y += buf[turn & 1][w0 + w].y;
     }
   }
   return v;
@@ -318,19 +335,21 @@ struct BackRow {
 };
 
 // NT: the largest workgroup.  PRE: a row is requested while the one before it is worked on, which takes the place of
-// more workgroups (each costs a partial row).  Rows of more than 8192 values have workgroups of up to 1024
+// more workgroups.  Rows side by side in a workgroup add their sums up in LDS at the end: a partial row a
+// workgroup, not a row.  Rows of more than 8192 values have workgroups of up to 1024
 // threads, whose 128 registers do not hold another row (2000 x 16384: 76 us; with 512 threads of four octets and the row
 // requested ahead, which spills, 112).
+// WG: a row is several waves', otherwise one's.
 template <int XT, bool WG, int VPT, int NT, bool PRE>
 __global__ __launch_bounds__(NT) void layernorm_backward_kernel(LayerBackArgs a) {
   __shared__ float2 buf[2][kMaxWaves];
-  const int TPR = WG ? blockDim.x : 64, RPB = WG ? 1 : 4;
-  const int t = WG ? threadIdx.x : threadIdx.x & 63;
+  const int TPR = WG ? a.lanes : 64, RPB = blockDim.x / TPR;
+  const int side = threadIdx.x / TPR, t = threadIdx.x - side * TPR;
   const int64_t octets = a.cols / 8;
   const float inv_n = 1.0f / (float)a.cols;
   const Dropper drop(a.drop);
   const int64_t step = (int64_t)gridDim.x * RPB;
-  int64_t row = (int64_t)blockIdx.x * RPB + (WG ? 0 : threadIdx.x >> 6);
+  int64_t row = (int64_t)blockIdx.x * RPB + side;
   BackRow<XT, VPT> next;
   if constexpr (PRE) next.load(a, row, octets, t, TPR);
   Octet<XT> wt[VPT];
@@ -343,7 +362,9 @@ __global__ __launch_bounds__(NT) void layernorm_backward_kernel(LayerBackArgs a)
     for (int e = 0; e < 8; ++e) dw[v][e] = db[v][e] = 0.0f;
   }
   int turn = 0;
-  for (; row < a.rows; row += step) {
+  // WG: the rows side by side meet at barriers, so all go on until the first of them is past the end; a row
+  // past it has loaded zeros.
+  for (; row - (WG ? side : 0) < a.rows; row += step) {
     const int64_t base = row * octets;
     BackRow<XT, VPT> now;
     if constexpr (PRE) {
@@ -369,7 +390,8 @@ __global__ __launch_bounds__(NT) void layernorm_backward_kernel(LayerBackArgs a)
         db[v][e] += d[e];
       }
     }
-    sum = row_sum2<WG>(sum, buf, turn++);
+    sum = row_sum2<WG>(sum, buf, turn++, side * (TPR >> 6), TPR >> 6);
+    if (WG && row >= a.rows) continue;
     const float2 means = make_float2(sum.x * inv_n, sum.y * inv_n);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
@@ -380,29 +402,29 @@ __global__ __launch_bounds__(NT) void layernorm_backward_kernel(LayerBackArgs a)
     }
   }
   if (!a.dw && !a.db) return;
-  if constexpr (!WG) {
+  if (RPB > 1) {
     // the rows side by side add up in LDS, in a fixed order, one sum after the other
-    __shared__ float sums[4][64 * VPT * 8];
+    __shared__ float sums[NT < 1024 ? NT * VPT * 8 : 1];  // workgroups of more than 512 threads hold one row
     auto meet = [&](float (*v8)[8]) {
-      float* mine = sums[threadIdx.x >> 6];
-      __syncthreads();
+      if constexpr (NT < 1024) {
+        __syncthreads();
 #pragma unroll
-      for (int v = 0; v < VPT; ++v)
+        for (int v = 0; v < VPT; ++v)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) mine[(v * 8 + e) * 64 + t] = v8[v][e];
-      __syncthreads();
+          for (int e = 0; e < 8; ++e) sums[(v * 8 + e) * blockDim.x + threadIdx.x] = v8[v][e];
+        __syncthreads();
+        if (side == 0) {
+          for (int g = 1; g < RPB; ++g)
 #pragma unroll
-      for (int v = 0; v < VPT; ++v)
+            for (int v = 0; v < VPT; ++v)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          v8[v][e] = sums[0][(v * 8 + e) * 64 + t];
-#pragma unroll
-          for (int g = 1; g < 4; ++g) v8[v][e] += sums[g][(v * 8 + e) * 64 + t];
+              for (int e = 0; e < 8; ++e) v8[v][e] += sums[(v * 8 + e) * blockDim.x + g * TPR + t];
         }
+      }
     };
-    meet(dw);
-    meet(db);
-    if (threadIdx.x >= 64) return;
+    if (a.dw) meet(dw);
+    if (a.db) meet(db);
+    if (side != 0) return;
   }
   auto put = [&](float* to, float (*v8)[8]) {
     if (!to) return;
@@ -453,7 +475,7 @@ __global__ __launch_bounds__(NT) void layernorm_backward_long_kernel(LayerBackAr
       sum.x += part.x;
       sum.y += part.y;
     }
-    sum = row_sum2<true>(sum, buf, turn++);
+    sum = row_sum2<true>(sum, buf, turn++, 0, NT / 64);
     const float2 means = make_float2(sum.x / (float)a.cols, sum.y / (float)a.cols);
     for (int64_t o = t; o < octets; o += NT) {
       Octet<XT> dy, h, wt, dr;
@@ -501,23 +523,34 @@ __global__ __launch_bounds__(16 * kSumLanes) void layer_sums_kernel(const float*
 // ---------------------------------------------------------------------------
 // Launch
 // ---------------------------------------------------------------------------
-// Workgroups of the forward, as the root-mean-square norm's.
+// Workgroups of the forward: 1024 threads a compute unit, each with a row requested ahead (8192 x 4096 with dropout and
+// statistics: 45.5 us, with 768 threads 45.1, with 512 49.7, with 2048 47.6).  With statistics, up to four rows a wavefront or
+// workgroup stay in one workgroup, which writes them itself.
 int layer_groups(int64_t rows, int64_t octets, bool stats) {
   const int rpb = octets <= 128 ? 4 : 1;
   if (stats && rows <= 4 * rpb) return 1;
-  if (octets <= 128) return row_groups(rows, rpb, 8, 0);
-  if (octets <= 2048) return row_groups(rows, rpb, (stats ? 1024 : 2048) / row_threads(octets), 0);
+  if (octets <= 128) return row_groups(rows, rpb, 4, 0);
+  if (octets <= 2048) return row_groups(rows, rpb, 1024 / row_threads(octets), 0);
   return row_groups(rows, rpb, 2, 0);
 }
 
+// A row is requested ahead where a workgroup has more than one (8192 x 4096, dropout: 45.5 us against 48.7,
+// without dropout 43.2 and 45.8; 1777 x 1040 fp32, a row each: 13.7 and 11.8).  Rows of more than 8192 values need workgroups whose
+// registers do not hold another.
 template <int XT, int FMT, bool STATS>
 void layer_run(const LayerArgs& a, int g, hipStream_t st) {
   const int64_t o = a.cols / 8;
   const dim3 grid((unsigned)g);
-  if (o <= 64) hipLaunchKernelGGL((layernorm_kernel<XT, FMT, STATS, false, 1>), grid, dim3(256), 0, st, a);
-  else if (o <= 128) hipLaunchKernelGGL((layernorm_kernel<XT, FMT, STATS, false, 2>), grid, dim3(256), 0, st, a);
-  else if (o <= 2048) hipLaunchKernelGGL((layernorm_kernel<XT, FMT, STATS, true, 2>), grid, dim3(row_threads(o)), 0, st, a);
-  else hipLaunchKernelGGL((layernorm_long_kernel<XT, FMT, STATS, 1024>), grid, dim3(1024), 0, st, a);
+  const bool pre = a.rows > (int64_t)g * (o <= 128 ? 4 : 1);
+  auto run = [&](auto ahead) {
+    constexpr bool PRE = decltype(ahead)::value;
+    if (o <= 64) hipLaunchKernelGGL((layernorm_kernel<XT, FMT, STATS, false, 1, PRE>), grid, dim3(256), 0, st, a);
+    else if (o <= 128) hipLaunchKernelGGL((layernorm_kernel<XT, FMT, STATS, false, 2, PRE>), grid, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((layernorm_kernel<XT, FMT, STATS, true, 2, PRE>), grid, dim3(row_threads(o)), 0, st, a);
+  };
+  if (o > 2048) hipLaunchKernelGGL((layernorm_long_kernel<XT, FMT, STATS, 1024>), grid, dim3(1024), 0, st, a);
+  else if (pre && o <= 1024) run(std::true_type{});
+  else run(std::false_type{});
 }
 
 template <int XT, int FMT>
@@ -526,22 +559,30 @@ void layer_stats(const LayerArgs& a, bool stats, int g, hipStream_t st) {
   else layer_run<XT, FMT, false>(a, g, st);
 }
 
-// Workgroups of the gradient's kernel.  With a row requested ahead, two of wavefront rows a compute unit and as many of workgroup rows as make 512
-// octets (8192 x 4096, dropout: 66.0 us with one, 73.8 with two, whose partial rows cost more than they
-// gain; 4096 x 2048: 25.8, 21.1, with three 21.4; 8192 x 1040: 43.0, 26.2, with four 20.6; 8192 x 1024: 17.9, 17.5, 20.9).
+// Threads of a workgroup of the gradient's kernel: rows of less than 4096 values stand side by side in as many as 512 threads
+// hold (4096 x 2048: 18.3 us, with a row each 21.0; 8192 x 1536: 22.5, 26.2; but 8192 x 4096 67.6, 65.9).
+int layer_back_threads(int64_t octets) {
+  if (octets <= 128) return 256;
+  if (octets >= 512) return row_threads(octets);
+  return 512 / row_threads(octets) * row_threads(octets);
+}
+
+// Its workgroups: one a compute unit, which has a row requested ahead (8192 x 4096 with dropout: 66 us, with two, whose partial
+// rows cost more than they gain, 74; with one that requests none ahead 96, with two 71); two of
+// four wavefront rows (8192 x 1024: 17.5, with one 17.9, with four 20.9).
 int layer_back_groups(int64_t rows, int64_t octets, int64_t slots) {
-  if (octets <= 128) return row_groups(rows, 4, 2, slots);
-  const int64_t fill = (512 + octets / 2) / octets;
-  return row_groups(rows, 1, fill < 1 ? 1 : (int)fill, slots);
+  const int rpb = octets <= 128 ? 4 : layer_back_threads(octets) / row_threads(octets);
+  return row_groups(rows, rpb, octets <= 128 ? 2 : 1, slots);
 }
 
 template <int XT>
-void layer_back_run(const LayerBackArgs& a, int g, hipStream_t st) {
+void layer_back_run(LayerBackArgs a, int g, hipStream_t st) {
   const int64_t o = a.cols / 8;
   const dim3 grid((unsigned)g);
+  a.lanes = o <= 128 ? 64 : row_threads(o);
   if (o <= 64) hipLaunchKernelGGL((layernorm_backward_kernel<XT, false, 1, 256, true>), grid, dim3(256), 0, st, a);
   else if (o <= 128) hipLaunchKernelGGL((layernorm_backward_kernel<XT, false, 2, 256, true>), grid, dim3(256), 0, st, a);
-  else if (o <= 1024) hipLaunchKernelGGL((layernorm_backward_kernel<XT, true, 2, 512, true>), grid, dim3(row_threads(o)), 0, st, a);
+  else if (o <= 1024) hipLaunchKernelGGL((layernorm_backward_kernel<XT, true, 2, 512, true>), grid, dim3(layer_back_threads(o)), 0, st, a);
   else if (o <= 2048) hipLaunchKernelGGL((layernorm_backward_kernel<XT, true, 2, 1024, false>), grid, dim3(row_threads(o)), 0, st, a);
   else hipLaunchKernelGGL((layernorm_backward_long_kernel<XT, 1024>), grid, dim3(1024), 0, st, a);
 }
@@ -582,7 +623,7 @@ hipError_t launch_layernorm_backward(const void* dy, const void* h, const float*
                                      void* workspace, size_t workspace_bytes, hipStream_t stream) {
   if (cols == 0) return hipSuccess;
   const int sums = (dweight ? 1 : 0) + (dbias ? 1 : 0);
-  LayerBackArgs a{dy, h, mean, rstd, weight, dres, dx, dbranch, dweight, dbias, 0, rows, cols, drop};
+  LayerBackArgs a{dy, h, mean, rstd, weight, dres, dx, dbranch, dweight, dbias, 0, rows, cols, drop, 0};
   int g = 0;
   if (rows > 0) {
     g = layer_back_groups(rows, cols / 8, sums ? (int64_t)(workspace_bytes / (sums * cols * sizeof(float))) : 0);
