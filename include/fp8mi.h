@@ -685,8 +685,8 @@ FP8MI_API size_t fp8mi_embedding_workspace(int64_t rows, int64_t cols);
  *            each row for every 128 columns.  Where it is smaller than that for the whole
  *            vocabulary, the vocabulary is taken in pieces (at least 256 columns' worth is needed, else
  *            FP8MI_ERR_WORKSPACE; fp8mi_vocab_workspace tells).
- * Exponentials and sums are fp32, relative to each row's largest logit.  A NaN or infinite logit makes the row's
- * loss and lse NaN (an lse that no finite logit enters is NaN too).
+ * Exponentials and sums are fp32, relative to each row's largest logit.  A NaN or +Inf logit makes the row's
+ * loss and lse NaN; a logit of -Inf adds nothing (a row of nothing else: lse -Inf).
  * K must be a multiple of 16, K <= 2^22; M <= 2^23 - 16, M * K < 2^31; V >= 1; x and w 16-B aligned.
  */
 FP8MI_API int fp8_vocab_cross_entropy(const uint8_t* x, int fx, const uint8_t* w, int fw, int64_t M, int64_t V, int64_t K,

@@ -288,6 +288,40 @@ def test_special_values():
     assert np.allclose(loss.cpu(), [np.log(2.0), np.log(5.0)], atol=1e-6)
 
 
+def test_rows_of_infinite_logits():
+    """-Inf in all columns but one, in all but none, and a +Inf among them; int32 and int64 targets."""
+    announce("cross entropy infinite logits")
+    w = torch.full((70, 16), 0x38, dtype=torch.uint8, device=device())               # 1 in E4M3
+    w[5] = 0xB8                                                                      # -1
+    for M in (3, 35):
+        x = torch.zeros((M, 16), dtype=torch.uint8, device=device())
+        x[0, 0] = 0xFC                                                               # -Inf in E5M2: column 5 is +Inf, the others -Inf
+        x[1, 2] = 0xFC
+        for index in (torch.int32, torch.int64):
+            t = torch.zeros(M, dtype=index, device=device())
+            one, ws = scalar(1.0), torch.empty(1 << 16, dtype=torch.uint8, device=device())
+            loss, lse = torch.zeros(M, device=device()), torch.zeros(M, device=device())
+            fm.fp8_vocab_cross_entropy(x, "e5m2", w, "e4m3", one, one, t, loss, lse, workspace=ws)
+            assert torch.isnan(loss[:2]).all() and torch.isnan(lse[:2]).all() and np.allclose(lse[2:].cpu(), np.log(70.0), atol=1e-6)
+            down = torch.cat([w[:5], w[6:]])
+            fm.fp8_vocab_cross_entropy(x, "e5m2", down, "e4m3", one, one, t, loss, lse, workspace=ws)
+            assert (lse[:2] == -float("inf")).all() and torch.isnan(loss[:2]).all() and np.allclose(lse[2:].cpu(), np.log(69.0), atol=1e-6)
+
+
+@pytest.mark.parametrize("M,V,K", [(36001, 60033, 32), (20, 131201, 16384)])
+def test_operands_of_more_than_2_31_codes(M, V, K):
+    """Codes of the logits' gradient beyond 2^31 in one piece, and a weight of more than 2^31 codes: the last rows and columns are right."""
+    announce(f"cross entropy {M}x{V}x{K}")
+    p = Problem(M, V, K)
+    rows, cols = np.array([0, M - 2, M - 1]), np.array([0, V // 2, V - 1])
+    loss, lse = p.forward()
+    check_forward(p, "exact", loss, lse, rows)
+    assert torch.isfinite(lse).all()
+    types = (torch.bfloat16, torch.bfloat16)
+    out = p.backward(lse, "exact", 1, "e5m2", 20000.0, types)
+    check_backward(p, "exact", lse, out, "e5m2", 20000.0, rows, cols, types)
+
+
 def test_no_rows():
     announce("cross entropy no rows")
     p = Problem(0, 300, 64)
