@@ -308,17 +308,24 @@ struct LogitGradEpi {
             if (__builtin_expect(__builtin_fabsf(m * grad[i] * out) <= kMax, 1)) {
               word = cvt_pk<FMT, true>(d[2], d[3], cvt_pk<FMT, false>(d[0], d[1], 0u));
             } else {
-              word = encode4<FMT>(d[0], d[1], d[2], d[3]);
-              if (count && live[i]) {
+              // Each for itself: with an infinite dloss or scale a p of 0 gives NaN, but not in the padding.
 #pragma unroll
-                for (int e = 0; e < 4; ++e) st.sat += __builtin_fabsf(d[e]) > kMax ? 1u : 0u;
+              for (int e = 0; e < 4; ++e) {
+                const bool past = decltype(edge)::value && c + e >= cols_left;
+                d[e] = past ? 0.0f : d[e];
+                if (live[i] && !past) {
+                  st.max = __builtin_elementwise_maximum(st.max, __builtin_fabsf(p[e] * grad[i]));
+                  if (count) st.sat += __builtin_fabsf(d[e]) > kMax ? 1u : 0u;
+                }
               }
+              word = encode4<FMT>(d[0], d[1], d[2], d[3]);
             }
             word &= mask;
             if (q) *reinterpret_cast<uint32_t*>(rows_tile.at(r, c)) = word;
             if (q_t) *reinterpret_cast<uint32_t*>(cols_tile.at(c + (lane & 3), r & ~3)) = transpose_quad(word, pair);
           }
-        if (live[i]) st.max = __builtin_elementwise_maximum(st.max, __builtin_fabsf(top * grad[i]));
+        // (A top of 0 may be the padding's; a p of 0 with an infinite dloss has been seen to above.)
+        if (live[i] && top != 0.0f) st.max = __builtin_elementwise_maximum(st.max, __builtin_fabsf(top * grad[i]));
       }
     };
     if (cols_left == BN) rows(std::false_type{});

@@ -288,6 +288,38 @@ def test_special_values():
     assert np.allclose(loss.cpu(), [np.log(2.0), np.log(5.0)], atol=1e-6)
 
 
+@pytest.mark.parametrize("M", [5, 40, 300])
+@pytest.mark.parametrize("accum", ["exact", "mfma_fp8"])
+def test_infinite_dloss(M, accum):
+    """A row's infinite dloss saturates its codes, and the columns that pad the vocabulary stay zeros; where a probability is 0
+    the gradient is NaN, and so is amax."""
+    announce(f"cross entropy infinite dloss {M} {accum}")
+    V, K, scale = 130, 64, 8.0
+    p = Problem(M, V, K, spread=1.0, ignored=0.0)
+    p.t[2] = V - 1
+    p.dloss[2] = float("inf")
+    _, lse = p.forward(accum)
+    dx, dw, amax, sat = p.backward(lse, accum, scale=scale)
+    v = np.full(V, 57344.0)
+    v[p.t[2]] = -57344.0
+    w = decoded(p.w, p.fw).cpu().numpy()
+    inv = p.sw.item() / scale
+    # the codes are known; all other rows' are too small to saturate, so the count is the row's
+    mag = np.abs(v) @ np.abs(w) * inv
+    bound = 1e-5 * mag if accum == "exact" else mfma8_bound(np.pad(np.where(v > 0, 0x7B, 0xFB).astype(np.uint8)[None], ((0, 0), (0, (-V) % 8))), "e5m2", np.pad(u8(p.w).T, ((0, 0), (0, (-V) % 8))), p.fw, np.float32(1 / scale), p.sw.item())[0]
+    check_close(d64(dx)[2], v @ w * inv, bound + 2.0 ** -23 * mag, "dx of the infinite row")
+    assert torch.isfinite(dx).all() and torch.isfinite(dw).all()
+    assert amax.item() == float("inf") and sat.item() == V
+    p = Problem(M, V, K, spread=5000.0, ignored=0.0)
+    p.t[2] = V - 1
+    p.dloss[2] = float("inf")
+    _, lse = p.forward(accum)
+    dx, dw, amax, _ = p.backward(lse, accum, scale=scale)
+    assert torch.isnan(dx[2]).all() and torch.isnan(amax).all()
+    rest = torch.arange(M, device=device()) != 2
+    assert torch.isfinite(dx[rest]).all()
+
+
 def test_rows_of_infinite_logits():
     """-Inf in all columns but one, in all but none, and a +Inf among them; int32 and int64 targets."""
     announce("cross entropy infinite logits")
