@@ -660,8 +660,8 @@ def fp8_embedding_backward(tokens, dy, dtable, scale=1.0, base=None, workspace=N
 
 
 def vocab_workspace_bytes(tokens: int, vocab: int, hidden: int, pieces: int = 1) -> int:
-    """Workspace with which the vocabulary's cross entropy, forward and backward, takes the vocabulary in at most so
-    many pieces (0: the least that it accepts)."""
+    """Workspace of the vocabulary's cross entropy, forward and backward, that holds the vocabulary in so many pieces
+    (0: the least that it accepts; the gradient may take more, include/fp8mi.h)."""
     return int(load_library().fp8mi_vocab_workspace(tokens, vocab, hidden, pieces))
 
 

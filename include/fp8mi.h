@@ -723,8 +723,9 @@ FP8MI_API int fp8_vocab_cross_entropy_backward(const uint8_t* x, int fx, const u
                                      unsigned long long* sat, int accum, void* workspace, size_t workspace_bytes,
                                      void* stream);
 
-/* Bytes of workspace with which both calls take the vocabulary in at most `pieces` pieces (0: the least that
- * they accept).  0 for sizes that they refuse, and for no rows. */
+/* Bytes of workspace that hold the vocabulary in `pieces` pieces (0: the least that both calls
+ * accept).  The gradient takes more pieces where one would be longer than 2^31 / K or 2^22 columns, and up to four more
+ * where that fills the compute units better.  0 for sizes that they refuse, and for no rows. */
 FP8MI_API size_t fp8mi_vocab_workspace(int64_t M, int64_t V, int64_t K, int64_t pieces);
 
 #ifdef __cplusplus
