@@ -23,7 +23,7 @@
 //   token_joins_kernel   adds the partial rows of each run that crosses.
 // Measured on MI355X: lookup of 8192 rows of 4096 bf16 20.5 us (134 MB, 6.5 TB/s); gradient of a 65536 x 4096 bf16
 // table added to a base, 8192 tokens of a skewed distribution, 235 us (1.14 GB, 4.85 TB/s: a copy's rate), of which the
-// sort 10.8 and the joins 6 (with a kernel of its own that first filled every row: 318 us).
+// sort 10.8 and the joins 7 (with a kernel of its own that first filled every row: 318 us).
 #include "launch.hpp"
 #include "model_ends.hpp"
 #include "row_octets.hpp"
@@ -365,31 +365,81 @@ __global__ __launch_bounds__(kLookNT) void token_rows_kernel(SumArgs a) {
   else write_row<OT>(a, key, o, acc);
 }
 
-// A run that leaves the chunk in which it begins: its partial rows, in order.
+constexpr int kJoinLanes = 64, kJoinSides = kLookNT / kJoinLanes;
+// Octet `o` of the run that begins in `chunk` and leaves it: partial row 0 is what leaves this chunk, partial row i what
+// enters chunk + i, up to the one that holds the run's last token.
 template <int OT>
-__global__ __launch_bounds__(kLookNT) void token_joins_kernel(SumArgs a) {
-  int64_t chunk, o;
-  if (!chunk_of(a, &chunk, &o)) return;
-  const int64_t first = chunk * a.chunk, end = first + a.chunk;
-  if (end >= a.rows) return;
+__device__ __forceinline__ void join_run(const SumArgs& a, int64_t chunk, int64_t o, int lane, int side,
+                                         float (*sums)[8][kJoinLanes]) {
+  const int64_t end = (chunk + 1) * a.chunk, mine = end + (int64_t)lane * a.chunk;
   const uint32_t key = a.keys[end];
-  if (key == kNoToken || a.keys[end - 1] != key) return;                       // nothing leaves
-  if (first > 0 && a.keys[first] == key && a.keys[first - 1] == key) return;   // it began earlier
-  float acc[8];
-  auto add = [&](int64_t c, int side, bool begin) {
-    const float4* p = reinterpret_cast<const float4*>(a.partials + ((c * 2 + side) * a.octets + o) * 8);
-    const float4 lo = p[0], hi = p[1];
-    const float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  // the chunks that begin with the token: a lane looks at each of 64, and a longer run is measured by bisection
+  int count = 1 + __popcll(__ballot(mine < a.rows && a.keys[mine < a.rows ? mine : end] == key));
+  if (count == 65) {
+    const int64_t last = end + count_below(a.keys + end, (int)(a.rows - end), key, true) - 1;
+    count = (int)(last / a.chunk - chunk) + 1;
+  }
+  const int quarter = (count + kJoinSides - 1) / kJoinSides;
+  const int from = side * quarter, to = from + quarter < count ? from + quarter : count;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (o < a.octets) {
+    constexpr int U = 8;
+    for (int i = from; i < to; i += U) {
+      float4 v[U][2];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = begin ? f[e] : acc[e] + f[e];
-  };
-  add(chunk, 1, true);
-  // The chunks that the run enters: up to the one that holds its last token.
-  const int64_t last = end + count_below(a.keys + end, (int)(a.rows - end), key, true) - 1;
-  const int64_t final = last / a.chunk;
-#pragma unroll 4
-  for (int64_t c = chunk + 1; c <= final; ++c) add(c, 0, false);
+      for (int u = 0; u < U; ++u) {
+        v[u][0] = v[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i + u < to) {
+          const float4* p = reinterpret_cast<const float4*>(a.partials + (((chunk + i + u) * 2 + (i + u == 0 ? 1 : 0)) * a.octets + o) * 8);
+          v[u][0] = p[0];
+          v[u][1] = p[1];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float f[8] = {v[u][0].x, v[u][0].y, v[u][0].z, v[u][0].w, v[u][1].x, v[u][1].y, v[u][1].z, v[u][1].w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] += f[e];
+      }
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sums[side][e][lane] = acc[e];
+  __syncthreads();
+  if (side != 0 || o >= a.octets) return;
+#pragma unroll
+  for (int s = 1; s < kJoinSides; ++s)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] += sums[s][e][lane];
   write_row<OT>(a, key, o, acc);
+}
+
+// A run that leaves the chunk in which it begins: its partial rows, in order.  A workgroup has 64 octets of the
+// row, each of its waves a quarter of the partial rows, eight of them requested at once: the run of a
+// token that pads a batch is as long as the list (gradient of 8192 tokens of 4096 bf16 columns added in place, all of one token:
+// 51 us, with a lane down all partial rows 81; half of 65536 tokens of one: 344, 540).  It looks at `joins`
+// chunks at once, a lane each, and takes the runs that begin there one after the other: most chunks have none.
+template <int OT>
+__global__ __launch_bounds__(kLookNT) void token_joins_kernel(SumArgs a, int joins) {
+  __shared__ float sums[kJoinSides][8][kJoinLanes];
+  const int64_t slices = (a.octets + kJoinLanes - 1) / kJoinLanes, group = blockIdx.x / slices;
+  const int lane = threadIdx.x & (kJoinLanes - 1), side = threadIdx.x / kJoinLanes;
+  const int64_t o = lane + (blockIdx.x - group * slices) * kJoinLanes;
+  bool begins = false;
+  if (lane < joins) {
+    const int64_t first = (group * joins + lane) * a.chunk, end = first + a.chunk;
+    if (end < a.rows) {
+      const uint32_t key = a.keys[end];
+      begins = key != kNoToken && a.keys[end - 1] == key &&                      // it leaves
+               !(first > 0 && a.keys[first] == key && a.keys[first - 1] == key); // and did not begin earlier
+    }
+  }
+  // the same in every wave
+  for (unsigned long long left = __ballot(begins); left; left &= left - 1) {
+    const int64_t chunk = group * joins + __builtin_ctzll(left);
+    join_run<OT>(a, chunk, o, lane, side, sums);
+    __syncthreads();  // the sums are free
+  }
 }
 
 // base, or zeros without one, into the whole table: 16 bytes a lane and turn.
@@ -426,10 +476,16 @@ hipError_t lookup_run(const LookupArgs& a, int otype, unsigned grid, hipStream_t
 
 template <int OT>
 hipError_t sums_run(const SumArgs& a, int dytype, unsigned fill_groups, hipStream_t st) {
-  const dim3 sums((unsigned)a.sum_groups), all((unsigned)a.sum_groups + fill_groups);
+  const dim3 all((unsigned)a.sum_groups + fill_groups);
   if (dytype == kBF16) hipLaunchKernelGGL((token_rows_kernel<kBF16, OT>), all, dim3(kLookNT), 0, st, a);
   else hipLaunchKernelGGL((token_rows_kernel<kF32, OT>), all, dim3(kLookNT), 0, st, a);
-  if (a.chunks > 1) hipLaunchKernelGGL(token_joins_kernel<OT>, sums, dim3(kLookNT), 0, st, a);
+  if (a.chunks > 1) {
+    // As many chunks a workgroup as leave 16 workgroups a compute unit, and no more than a wave has lanes.
+    const int64_t slices = (a.octets + kJoinLanes - 1) / kJoinLanes;
+    int64_t joins = (slices * a.chunks + persistent_groups(16) - 1) / persistent_groups(16);
+    if (joins > kJoinLanes) joins = kJoinLanes;
+    hipLaunchKernelGGL(token_joins_kernel<OT>, dim3((unsigned)((a.chunks + joins - 1) / joins * slices)), dim3(kLookNT), 0, st, a, (int)joins);
+  }
   return hipGetLastError();
 }
 

@@ -130,6 +130,26 @@ def test_gradient_of_any_numbers(rows, vocab, cols, dtype):
     assert torch.equal(inplace, outs[0])
 
 
+@pytest.mark.parametrize("cols", [16, 528])
+@pytest.mark.parametrize("shift", [0, 5])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_runs_of_many_lengths(cols, shift, in_place):
+    """Runs of one token over 1 to 200 pieces of the sorted list of 16 each, and one value less and more, from two places in a piece; exact."""
+    announce(f"embedding runs {cols} {shift} {in_place}")
+    lengths = [shift] + [16 * n + more for n in (1, 2, 3, 4, 5, 8, 9, 32, 33, 62, 63, 64, 65, 66, 67, 128, 129, 200) for more in (-1, 0, 1)]
+    t = np.repeat(np.arange(len(lengths)), lengths)
+    assert 8192 < len(t) <= 65536                                # pieces of 16
+    vocab, gen = len(lengths) + 3, np.random.default_rng(shift)
+    gen.shuffle(t)
+    dy = gen.integers(-4, 5, size=(len(t), cols)).astype(np.float32)
+    base = gen.integers(-9, 10, size=(vocab, cols)).astype(np.float32)
+    dtable = torch.from_numpy(base).to(device()) if in_place else torch.full((vocab, cols), 7.0, device=device())
+    ws = torch.full((fm.embedding_workspace_bytes(len(t), cols),), 0xA5, dtype=torch.uint8, device=device())
+    fm.fp8_embedding_backward(to_tokens(t, torch.int32), torch.from_numpy(dy).to(device()), dtable, scale=0.5, base=dtable if in_place else None, workspace=ws)
+    want = me.embedding_grad(t, dy, vocab, 0.5, base if in_place else None)
+    assert np.array_equal(d64(dtable), want)
+
+
 def test_rows_are_added_in_the_order_of_the_tokens():
     announce("embedding gradient order")
     dy = randn(9, 16, 32, dtype=torch.float32)
