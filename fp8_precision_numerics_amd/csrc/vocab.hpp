@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "gemm_few_rows.hpp"
 #include "gemm_rounds.hpp"
 #include "vocab_epilogue.hpp"
 
@@ -15,6 +16,9 @@ constexpr int64_t kPieceCols = 256;
 // Rows of codes are padded to whole steps of the products that read them.
 inline int64_t up128(int64_t n) { return (n + 127) & ~int64_t(127); }
 inline int64_t up16(int64_t n) { return (n + 15) & ~int64_t(15); }
+
+// Few rows have exact products in either mode, the gradient's as the loss's: they have to be of the same logits.
+inline int logits_mode(int64_t M, int accum) { return M <= kFewRows ? (int)kAccumExact : accum; }
 
 // Workspace of the forward for M rows and pieces of P columns: the target's logit and the
 // carried pair of each row, then a pair a row for each tile (of at least 128 columns).

@@ -8,6 +8,8 @@
 // the sum of each of its rows (8 bytes a row and 256 columns: 1/64 of bf16 logits), a second kernel joins
 // them; a workspace too small for the whole vocabulary's is served in pieces, the joined
 // pair of each row carried from one to the next.
+// Measured on MI355X: 8192 x 65536 x 4096 exact 2.77-2.95 ms (1.49-1.58 PFLOP/s, the clock under the power limit), 1003 x 50021 x 4096
+// 0.305 ms (1.35), a row of 131072 x 4096 93 us (5.8 TB/s of the weight), 64 rows 121 us (FP8 cores 111); the joining kernel 5-6 us of each.
 #include "gemm_few_rows.hpp"
 #include "launch.hpp"
 #include "model_ends.hpp"
@@ -114,10 +116,14 @@ hipError_t launch_vocab_cross_entropy(const VocabOperands& o, int64_t V, const T
   j.partials = epi.partials = reinterpret_cast<float2*>(ws);
   // slots for the pairs of so many tiles
   const int64_t slots = (int64_t)(workspace_bytes - (size_t)(ws - reinterpret_cast<uint8_t*>(workspace))) / (o.M * 8);
+  // The streaming kernel reads and widens the rows anew for every 16 columns, which from about 9 rows on takes longer than the tiles'
+  // padding to 64 rows does, if there is a tile for every compute unit: 16 rows, 131072 x 4096 123 us against 110, 50021 x 1024 23 against
+  // 18, but 32000 x 4096 (250 tiles) 38 both; 8 rows 108 against 110.
+  const bool few = o.M <= kFewRows / 2 || (o.M <= kFewRows && (V + 127) / 128 < persistent_groups(1));
   for (int64_t col = 0; col < V;) {
     int64_t n = V - col;
     hipError_t e;
-    if (o.M <= kFewRows) {
+    if (few) {
       const auto run = [&](bool count_only) {
         epi.col0 = col;
         return launch_loss_few_rows(o.a, o.fa, o.b + col * o.K, o.fb, o.M, n, o.K, o.sinv_a, o.sinv_b, epi, count_only, &j.tiles, stream);
@@ -132,7 +138,7 @@ hipError_t launch_vocab_cross_entropy(const VocabOperands& o, int64_t V, const T
       const int64_t fit = slots * 128;  // the narrower tiles'
       if (n > fit) n = fit / kPieceCols * kPieceCols;
       epi.col0 = col;
-      e = launch_vocab_logits(o, col, n, epi, accum, &j.tiles, stream);
+      e = launch_vocab_logits(o, col, n, epi, logits_mode(o.M, accum), &j.tiles, stream);
     }
     if (e != hipSuccess) return e;
     j.first = col == 0;
