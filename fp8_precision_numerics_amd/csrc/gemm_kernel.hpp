@@ -826,10 +826,11 @@ __global__ __launch_bounds__(64 * WM* WN) void gemm_kernel(
         __syncthreads();
         emit(r0, r0 + PASS, tw);
         __syncthreads();
-        if (whole) pass.flush(tw, r0, st);
-        else pass.flush_partials(tw, r0, partials);
+        if (!whole) pass.flush_partials(tw, r0, partials);
+        else if constexpr (PRODUCT) pass.flush_product(tw, r0);
+        else pass.flush(tw, r0, st);
       }
-      if (rq.amax_bits || rq.sat) {
+      if (!PRODUCT && (rq.amax_bits || rq.sat)) {
         if (whole) publish_epilogue_stats(rq, st, reinterpret_cast<uint32_t*>(smem));
         else clear_epilogue_stats(rq);  // for the kernel that finishes the split product
       }

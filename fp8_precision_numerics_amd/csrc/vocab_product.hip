@@ -12,15 +12,17 @@
 namespace fp8mi {
 namespace {
 
+constexpr int64_t kShortK = 4 * kBK;
+
 template <int FA, int FB, int MODE>
 hipError_t product_shape(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, int64_t K, const float* sa, const float* sb,
                          const ProductEpi& epi, size_t workspace_bytes, hipStream_t st) {
   TileChoice c = choose_tile(M, N, K, MODE == kAccumMfma8, workspace_bytes, persistent_groups(1));
-  // A K of one or two steps is over before the output is written: the small tiles, three workgroups a compute unit, store
-  // and load side by side, which the estimate does not know.  dw of 50021 x 2048 from 219 rows, with the logits
-  // before it: 154 us (exact; FP8 cores 118) against 169 (132) on 256 x 256 tiles and 156 (126) on 128 x 128; 32000 x 4096 from 64 rows:
-  // 126, 139, 138; from 500 rows of 1024 no difference; from 1000 rows the large ones are the faster.
-  if (K <= 2 * kBK && c.split == 1) c.shape = 2;
+  // A K of up to four steps is over soon after its output begins to be written: the small tiles, three workgroups a compute unit, store
+  // and load side by side, which the estimate does not know.  dw with the logits before it, in us on 64 x 128, 128 x 128 and 256 x 256
+  // tiles: 50021 x 2048 from 219 rows, exact 133, 131, 138, FP8 cores 97, 100, 102; 32000 x 4096 from 64 rows 110, 109, 117 and 96, 100, 107;
+  // 50021 x 1024 from 500 rows 127, 125, 138 and 97, 96, 100; but from 1000 rows 225, 218, 214 and 174, 170, 159.
+  if (K <= kShortK && c.split == 1) c.shape = 2;
   if (c.shape == 0) {
     if constexpr (MODE == kAccumExact) return epi_run<256, 256, 2, 4, FA, FB, MODE, ProductEpi, 2, true>(A, B, M, N, K, sa, sb, epi, c.split, st);
     else return epi_run<256, 256, 4, 2, FA, FB, MODE, ProductEpi, 2, true>(A, B, M, N, K, sa, sb, epi, c.split, st);
@@ -58,7 +60,7 @@ hipError_t launch_vocab_product(const uint8_t* A, int64_t lda, int fa, const uin
     return product_fmt<kAccumExact>(a, fa, B, fb, count, N, K, sinv_a, sinv_b, epi, workspace_bytes, stream);
   };
   // The rows may be cut (the large tiles are square, so the sides may be named in either order).
-  const int64_t first = K <= 2 * kBK ? M : plan_rounds(N, M, K, accum == kAccumMfma8, workspace_bytes, persistent_groups(1)).first;
+  const int64_t first = K <= kShortK ? M : plan_rounds(N, M, K, accum == kAccumMfma8, workspace_bytes, persistent_groups(1)).first;
   const hipError_t e = rows(0, first);
   return e != hipSuccess || first == M ? e : rows(first, M - first);
 }
