@@ -7,8 +7,8 @@
 // Three products of 2 M V K operations on the matrix cores.  Of the M x V gradients only a piece's
 // codes exist at a time, row-major and transposed, the orientations in which the two products read
 // their first operand; dx grows over the pieces in fp32.
-// Measured on MI355X: 8192 x 65536 x 4096 on the FP8 cores in four pieces 5.15 ms (2.56 PFLOP/s of the three products: each piece's
-// codes 468 us, dx 412, dw 409); 219 x 50021 x 2048 exact, one piece, 230 us (65, 70, 95), which writes 205 MB of dw.
+// Measured on MI355X: 8192 x 65536 x 4096 on the FP8 cores in four pieces 5.13 ms (2.57 PFLOP/s of the three products: each piece's
+// codes 465 us, dx 412, dw 403); 219 x 50021 x 2048 exact, one piece, 214 us, which writes 205 MB of dw.
 #include "launch.hpp"
 #include "model_ends.hpp"
 #include "vocab_dispatch.hpp"
