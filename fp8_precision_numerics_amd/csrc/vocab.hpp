@@ -6,6 +6,7 @@
 
 #include "gemm_few_rows.hpp"
 #include "gemm_rounds.hpp"
+#include "gemm_tile.hpp"
 #include "vocab_epilogue.hpp"
 
 namespace fp8mi {
