@@ -18,11 +18,12 @@ template <int FA, int FB, int MODE>
 hipError_t product_shape(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, int64_t K, const float* sa, const float* sb,
                          const ProductEpi& epi, size_t workspace_bytes, hipStream_t st) {
   TileChoice c = choose_tile(M, N, K, MODE == kAccumMfma8, workspace_bytes, persistent_groups(1));
-  // A K of up to four steps is over soon after its output begins to be written: the small tiles, three workgroups a compute unit, store
+  // A K of up to four steps is over soon after its output begins to be written: smaller tiles, several workgroups a compute unit, store
   // and load side by side, which the estimate does not know.  dw with the logits before it, in us on 64 x 128, 128 x 128 and 256 x 256
-  // tiles: 50021 x 2048 from 219 rows, exact 133, 131, 138, FP8 cores 97, 100, 102; 32000 x 4096 from 64 rows 110, 109, 117 and 96, 100, 107;
-  // 50021 x 1024 from 500 rows 127, 125, 138 and 97, 96, 100; but from 1000 rows 225, 218, 214 and 174, 170, 159.
-  if (K <= kShortK && c.split == 1) c.shape = 2;
+  // tiles, exact and FP8 cores: 32000 x 4096 from 64 rows 110, 109, 117 and 96, 100, 107; 65536 x 4096 from 64 rows FP8 cores 177, 181, 190; 50021 x
+  // 2048 from 219 rows 133, 131, 138 and 97, 100, 102; 50021 x 1024 from 500 rows 127, 125, 138 and 97, 96, 100; 65536 x 4096 from 200 rows 330, 313,
+  // 317 and 238, 233, 234, from 500 rows 553, 517, 516 and 370, 350, 341; from 1000 rows (50021 x 1024) 225, 218, 214 and 174, 170, 159.
+  if (K <= kShortK && c.split == 1) c.shape = K <= kBK ? 2 : 1;
   if (c.shape == 0) {
     if constexpr (MODE == kAccumExact) return epi_run<256, 256, 2, 4, FA, FB, MODE, ProductEpi, 2, true>(A, B, M, N, K, sa, sb, epi, c.split, st);
     else return epi_run<256, 256, 4, 2, FA, FB, MODE, ProductEpi, 2, true>(A, B, M, N, K, sa, sb, epi, c.split, st);
