@@ -8,7 +8,7 @@
 // codes exist at a time, row-major and transposed, the orientations in which the two products read
 // their first operand; dx grows over the pieces in fp32.
 // Measured on MI355X: 8192 x 65536 x 4096 on the FP8 cores in four pieces 5.13 ms (2.57 PFLOP/s of the three products: each piece's
-// codes 465 us, dx 412, dw 403); 219 x 50021 x 2048 exact, one piece, 214 us, which writes 205 MB of dw.
+// codes 465 us, dx 412, dw 403); 219 x 50021 x 2048 exact, one piece, 202-207 us, which writes 205 MB of dw.
 #include "launch.hpp"
 #include "model_ends.hpp"
 #include "vocab_dispatch.hpp"
