@@ -643,7 +643,7 @@ def fp8_embedding(tokens, table, out, scale=1.0, fmt=None, sinv=None, stream=Non
 
 
 def embedding_workspace_bytes(rows: int, cols: int) -> int:
-    """Workspace of fp8_embedding_backward for so many tokens and columns."""
+    """Workspace of fp8_embedding_backward for any number of tokens up to `rows`."""
     return int(load_library().fp8mi_embedding_workspace(rows, cols))
 
 

@@ -5,6 +5,7 @@
 #include "api_common.hpp"
 #include "device_common.hpp"
 #include "model_ends.hpp"
+#include "token_chunks.hpp"
 #include "vocab.hpp"
 
 using namespace fp8mi;
@@ -134,7 +135,7 @@ int fp8_embedding_backward(const void* tokens, int itype, int64_t rows, const vo
   if (vocab * cols == 0 || (rows == 0 && base == dtable)) return FP8MI_OK;
   if (!dtable || (rows && (!tokens || !dy || !workspace))) return FP8MI_ERR_NULL;
   if (!aligned16(dy) || !aligned16(base) || !aligned16(dtable) || !index_aligned(tokens, itype)) return FP8MI_ERR_ALIGN;
-  if (rows && workspace_bytes < embedding_workspace(rows, cols)) return FP8MI_ERR_WORKSPACE;
+  if (rows && workspace_bytes < embedding_need(rows, cols)) return FP8MI_ERR_WORKSPACE;
   const int dev = check_device();
   if (dev != FP8MI_OK) return dev;
   return launched(launch_embedding_backward(tokens, itype == FP8MI_I64, rows, dy, dytype, vocab, cols, scale, base, dtable, ttype, workspace,

@@ -27,6 +27,7 @@
 #include "launch.hpp"
 #include "model_ends.hpp"
 #include "row_octets.hpp"
+#include "token_chunks.hpp"
 
 namespace fp8mi {
 namespace {
@@ -119,7 +120,6 @@ int row_lanes(int64_t octets) {
 // ---------------------------------------------------------------------------
 // Sort
 // ---------------------------------------------------------------------------
-constexpr int kSortBlock = 8192;
 constexpr int kSortWaves = 16;
 constexpr int kSortGroup = 32;                             // tokens a workgroup ranks
 constexpr int kSortPart = kSortBlock / (2 * kSortWaves);   // ids a half wave compares with
@@ -460,13 +460,6 @@ __global__ __launch_bounds__(256) void fill_rows_kernel(const uint4* base, uint4
   for (; i < count; i += step) dst[i] = base ? src[i] : (vec4){0u, 0u, 0u, 0u};
 }
 
-// Sorted tokens a chunk: 16 (two requests of eight rows a lane) until that makes 4096
-// chunks, which fill the device; then longer ones.
-int64_t chunk_size(int64_t rows) {
-  const int64_t c = (rows + 4095) / 4096;
-  return c < 16 ? 16 : (c + 7) / 8 * 8;
-}
-
 template <int TT>
 hipError_t lookup_run(const LookupArgs& a, int otype, unsigned grid, hipStream_t st) {
   if (otype == kBF16) hipLaunchKernelGGL((lookup_kernel<TT, kBF16>), dim3(grid), dim3(kLookNT), 0, st, a);
@@ -488,8 +481,6 @@ hipError_t sums_run(const SumArgs& a, int dytype, unsigned fill_groups, hipStrea
   }
   return hipGetLastError();
 }
-
-int64_t up16(int64_t bytes) { return (bytes + 15) & ~int64_t(15); }
 
 }  // namespace
 
@@ -517,11 +508,6 @@ hipError_t launch_embedding(const void* tokens, bool wide, int64_t rows, const v
   return lookup_run<kTableE5M2>(a, otype, grid, stream);
 }
 
-size_t embedding_workspace(int64_t rows, int64_t cols) {
-  const int64_t chunks = (rows + chunk_size(rows) - 1) / chunk_size(rows);
-  return (size_t)((rows > kSortBlock ? 4 : 2) * up16(rows * 4) + (chunks > 1 ? chunks * 2 * cols * 4 : 0));
-}
-
 hipError_t launch_embedding_backward(const void* tokens, bool wide, int64_t rows, const void* dy, int dytype,
                                      int64_t vocab, int64_t cols, float scale, const void* base, void* dtable,
                                      int ttype, void* workspace, hipStream_t stream) {
@@ -530,7 +516,7 @@ hipError_t launch_embedding_backward(const void* tokens, bool wide, int64_t rows
   uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
   auto take = [&]() {
     void* p = ws;
-    ws += up16(rows * 4);
+    ws += token_words(rows);
     return p;
   };
   SortArgs s{tokens, reinterpret_cast<uint32_t*>(take()), nullptr, rows, vocab, wide};
@@ -552,7 +538,7 @@ hipError_t launch_embedding_backward(const void* tokens, bool wide, int64_t rows
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   a.partials = reinterpret_cast<float*>(ws);
-  a.chunks = (int)((rows + a.chunk - 1) / a.chunk);
+  a.chunks = (int)chunk_count(rows);
   a.lanes = row_lanes(a.octets);
   a.slices = (int)((a.octets + a.lanes - 1) / a.lanes);
   a.sum_groups = (int)(((int64_t)a.chunks * a.lanes + kLookNT - 1) / kLookNT * a.slices);

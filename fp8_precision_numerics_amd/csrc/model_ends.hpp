@@ -25,10 +25,6 @@ hipError_t launch_layernorm_backward(const void* dy, const void* h, const float*
 hipError_t launch_embedding(const void* tokens, bool wide, int64_t rows, const void* table, int ttype, int64_t vocab,
                             int64_t cols, const float* sinv, float scale, void* out, int otype, hipStream_t stream);
 
-// Workspace of the gradient, and the most tokens that one call sorts.
-constexpr int64_t kMaxTokens = int64_t(1) << 20;
-size_t embedding_workspace(int64_t rows, int64_t cols);
-
 hipError_t launch_embedding_backward(const void* tokens, bool wide, int64_t rows, const void* dy, int dytype,
                                      int64_t vocab, int64_t cols, float scale, const void* base, void* dtable,
                                      int ttype, void* workspace, hipStream_t stream);

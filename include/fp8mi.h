@@ -655,7 +655,7 @@ FP8MI_API int fp8_embedding(const void* tokens, int itype, int64_t rows, const v
  *            two share their weight), or NULL: zeros.  It may be dtable itself; then only the rows of
  *            tokens that occur are touched.
  * dtable     device, [vocab x cols] of ttype (fp32 or bf16), all of it overwritten.
- * workspace  device scratch of at least fp8mi_embedding_workspace(rows, cols) bytes (else
+ * workspace  device scratch of fp8mi_embedding_workspace(rows, cols) bytes (less than the call needs:
  *            FP8MI_ERR_WORKSPACE).
  * cols must be a multiple of 16, cols <= 2^20; dy, base, dtable and workspace 16-B aligned.  The rows are added
  * in the order of t, in pieces whose ends depend on the tokens alone: the bits repeat.
@@ -664,7 +664,8 @@ FP8MI_API int fp8_embedding_backward(const void* tokens, int itype, int64_t rows
                            int64_t cols, float scale, const void* base, void* dtable, int ttype, void* workspace,
                            size_t workspace_bytes, void* stream);
 
-/* Bytes of workspace that fp8_embedding_backward asks for (0: sizes that it refuses, or no tokens). */
+/* Bytes of workspace that hold fp8_embedding_backward for any number of tokens up to `rows` (0: sizes that it
+ * refuses, or no tokens). */
 FP8MI_API size_t fp8mi_embedding_workspace(int64_t rows, int64_t cols);
 
 /*

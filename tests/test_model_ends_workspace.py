@@ -1,0 +1,57 @@
+"""What the workspace queries of the operators at both ends of a model promise, against what the calls use.  Host only: the
+sizes' arithmetic is asked of the code itself (plain C++, compiled here), and a call is made only where it is refused."""
+
+import ctypes
+import os
+import shutil
+import subprocess
+
+import pytest
+
+import fp8_precision_numerics_amd as fm
+
+EWS = -10
+P = ctypes.c_void_p(0x10000)  # never dereferenced
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "fp8_precision_numerics_amd", "csrc")
+SHIM = """#include "token_chunks.hpp"
+extern "C" size_t need(int64_t rows, int64_t cols) { return fp8mi::embedding_need(rows, cols); }
+extern "C" int64_t chunks(int64_t rows) { return fp8mi::chunk_count(rows); }
+"""
+
+
+@pytest.fixture(scope="module")
+def host(tmp_path_factory):
+    if shutil.which("g++") is None:
+        pytest.skip("no C++ compiler")
+    d = tmp_path_factory.mktemp("sizes")
+    (d / "shim.cpp").write_text(SHIM)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Wextra", "-Werror", "-shared", "-fPIC", "-I", CSRC, str(d / "shim.cpp"), "-o", str(d / "shim.so")],
+                   check=True, capture_output=True, text=True)
+    lib = ctypes.CDLL(str(d / "shim.so"))
+    lib.need.argtypes, lib.need.restype = [ctypes.c_int64] * 2, ctypes.c_size_t
+    lib.chunks.argtypes, lib.chunks.restype = [ctypes.c_int64], ctypes.c_int64
+    return lib
+
+
+# around the block of the sort, the last number of tokens in chunks of 16, and each later length of a chunk (24, 32, ..)
+ROWS = sorted({1, 15, 16, 17, 31, 8191, 8192, 8193, 40000, 65535, 65536, 65537, 70000, 1 << 20}
+              | {4096 * c + d for c in range(16, 257, 8) for d in (-1, 0, 1) if 4096 * c + d <= 1 << 20})
+
+
+@pytest.mark.parametrize("cols", [16, 64, 4096])
+def test_embedding_workspace_holds_any_fewer_tokens(host, cols):
+    """The size never falls as the tokens grow, so a scratch that is sized for the largest batch serves every smaller one."""
+    sizes = [fm.embedding_workspace_bytes(rows, cols) for rows in ROWS]
+    assert sizes == sorted(sizes)
+    for rows, size in zip(ROWS, sizes):
+        assert host.need(rows, cols) <= size and host.chunks(rows) <= 4096
+        if host.need(rows, cols) > 16:
+            assert fm.load_library().fp8_embedding_backward(P, 1, rows, P, 1, 256, cols, 1.0, None, P, 1, P, host.need(rows, cols) - 1, None) == EWS
+
+
+def test_a_head_has_room_for_the_lookups_of_fewer_tokens(host):
+    """70000 tokens and a vocabulary of bytes, whose loss asks for less than the lookup's gradient of 65536 tokens."""
+    T, H, V = 70000, 4096, 256
+    space = fm.Fp8VocabHead(T, H, V, pieces=1, device="cpu").workspace.numel()
+    for n in (1, 8193, 65536, 65537, T):
+        assert host.need(n, H) <= space
