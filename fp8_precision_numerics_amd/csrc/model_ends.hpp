@@ -35,10 +35,6 @@ hipError_t launch_fill_rows(const void* base, void* to, int64_t words, hipStream
 struct VocabOperands;  // vocab.hpp
 struct Targets;        // vocab_epilogue.hpp
 
-// Workspace with which the loss over M rows, a vocabulary of V and rows of K codes goes in at most
-// `pieces` pieces, forward and backward.
-size_t vocab_workspace(int64_t M, int64_t V, int64_t K, int64_t pieces);
-
 hipError_t launch_vocab_cross_entropy(const VocabOperands& o, int64_t V, const Targets& targets, float* loss, float* lse,
                                       int accum, void* workspace, size_t workspace_bytes, hipStream_t stream);
 

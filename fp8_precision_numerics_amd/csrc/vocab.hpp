@@ -8,22 +8,12 @@
 #include "gemm_rounds.hpp"
 #include "gemm_tile.hpp"
 #include "vocab_epilogue.hpp"
+#include "vocab_pieces.hpp"
 
 namespace fp8mi {
 
-// Pieces of the vocabulary are multiples of so many columns (the widest tile), but for the last.
-constexpr int64_t kPieceCols = 256;
-
-// Rows of codes are padded to whole steps of the products that read them.
-inline int64_t up128(int64_t n) { return (n + 127) & ~int64_t(127); }
-inline int64_t up16(int64_t n) { return (n + 15) & ~int64_t(15); }
-
 // Few rows have exact products in either mode, the gradient's as the loss's: they have to be of the same logits.
 inline int logits_mode(int64_t M, int accum) { return M <= kFewRows ? (int)kAccumExact : accum; }
-
-// Workspace of the forward for M rows and pieces of P columns: the target's logit and the
-// carried pair of each row, then a pair a row for each tile (of at least 128 columns).
-size_t vocab_loss_bytes(int64_t M, int64_t P);
 
 // One product of the loss: codes A [M x K] (hidden states) and B [N x K] (a piece of the
 // vocabulary's weight) with their formats and inverse scales.

@@ -16,19 +16,6 @@
 namespace fp8mi {
 namespace {
 
-int64_t up256(int64_t n) { return (n + 255) & ~int64_t(255); }
-
-// The codes both ways for pieces of P columns, and the fp32 sums of dx where there are several.
-int64_t grad_bytes(int64_t M, int64_t V, int64_t K, int64_t P) {
-  return up256(M * up128(P)) + up256(P * up128(M)) + (P < V ? up256(M * K * 4) : 0);
-}
-
-// The longest piece that the products' offsets reach.
-int64_t most_columns(int64_t K) {
-  const int64_t most = ((int64_t(1) << 31) - 1) / K / kPieceCols * kPieceCols;
-  return most < (int64_t(1) << 22) ? most : (int64_t(1) << 22);
-}
-
 // Estimate of the passes over pieces of P columns, in microseconds: the three products of each, and its
 // passes over dx's fp32 sums.
 double pieces_time(const VocabOperands& o, int64_t V, int64_t P, int accum) {
@@ -64,16 +51,6 @@ hipError_t launch_vocab_grad(const VocabOperands& o, int64_t col, int64_t N, con
   return vocab_launch(o, col + first, N - first, rest, mode, stream);
 }
 
-size_t vocab_workspace(int64_t M, int64_t V, int64_t K, int64_t pieces) {
-  int64_t P = pieces > 0 ? up256((V + pieces - 1) / pieces) : kPieceCols;
-  P = P < V ? P : V;
-  size_t back = (size_t)grad_bytes(M, V, K, P);
-  const size_t whole = (size_t)grad_bytes(M, V, K, V), fwd = vocab_loss_bytes(M, P);
-  // one piece needs no sums of dx, so it may be the smaller
-  if (V <= most_columns(K) && whole < back) back = whole;
-  return M == 0 ? 0 : (back > fwd ? back : fwd);
-}
-
 hipError_t launch_vocab_cross_entropy_backward(const VocabOperands& o, int64_t V, const Targets& targets, const float* lse,
                                                const float* dloss, int fmt, const float* scale, const float* scale_inv,
                                                void* dx, int dxtype, void* dw, int dwtype, float* amax,
@@ -87,12 +64,9 @@ hipError_t launch_vocab_cross_entropy_backward(const VocabOperands& o, int64_t V
   const int64_t dwsize = dwtype == kBF16 ? 2 : 4;
   if (M == 0) return dw ? launch_fill_rows(nullptr, dw, V * K * dwsize / 16, stream) : hipSuccess;
   // The longest piece that fits, then pieces of equal length.
-  const int64_t most = most_columns(K);
   int64_t P = V;
-  if (V > most || grad_bytes(M, V, K, V) > (int64_t)workspace_bytes) {
-    int64_t fit = ((int64_t)workspace_bytes - up256(M * K * 4) - 512) / (M + ldt) / kPieceCols * kPieceCols;
-    fit = fit < kPieceCols ? kPieceCols : fit;  // the entry point has seen to that much
-    fit = fit < most ? fit : most;
+  if (!grad_whole(M, V, K, workspace_bytes)) {
+    const int64_t fit = grad_longest(M, K, workspace_bytes);
     // As few pieces as fit, or up to four more where the estimate prefers them: tiles that fill whole rounds of
     // the compute units are worth another pass over dx's sums (8192 x 4096 x 65536 on the FP8 cores over 512 MiB: four pieces of 16384 columns 5.21 ms, the three that fit 5.40).
     const int64_t least = (V + fit - 1) / fit;

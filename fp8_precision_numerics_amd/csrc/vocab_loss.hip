@@ -101,10 +101,6 @@ hipError_t launch_vocab_logits(const VocabOperands& o, int64_t col, int64_t N, c
   return hipSuccess;
 }
 
-size_t vocab_loss_bytes(int64_t M, int64_t P) {
-  return (size_t)(up16(M * 4) + up16(M * 8) + M * 8 * ((P + 127) / 128));
-}
-
 hipError_t launch_vocab_cross_entropy(const VocabOperands& o, int64_t V, const Targets& targets, float* loss, float* lse,
                                       int accum, void* workspace, size_t workspace_bytes, hipStream_t stream) {
   uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);

@@ -1,0 +1,30 @@
+"""The vocabulary's cross entropy in pieces: the longest hidden size, whose vocabulary is longer than one piece may be.
+Tolerances as in test_gpu_vocab_cross_entropy.py."""
+
+import numpy as np
+import pytest
+import torch
+
+import fp8_precision_numerics_amd as fm
+from gpu_helpers import announce, device
+from test_gpu_vocab_cross_entropy import Problem, check_backward, check_forward, check_product, gradient
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+
+
+def test_one_piece_asked_for_where_there_are_two():
+    """300 columns of 2^22 values: the longest piece is 256 columns, so the size for one piece holds dx's sums."""
+    M, V, K = 17, 300, 1 << 22
+    announce(f"cross entropy {M}x{V}x{K}, workspace of one piece")
+    p = Problem(M, V, K)
+    ws = torch.full((fm.vocab_workspace_bytes(M, V, K, 1),), 0xA5, dtype=torch.uint8, device=device())
+    loss, lse = p.forward(workspace=ws)
+    check_forward(p, "exact", loss, lse, np.arange(M))
+    out = p.backward(lse, workspace=ws, scale=2000.0, types=(BF, BF))
+    check_backward(p, "exact", lse, (None,) + out[1:], "e5m2", 2000.0, cols=np.array([0, 255, 256, V - 1]), types=(BF, BF))
+    # dx at its first, middle and last columns
+    d, err = gradient(p, "exact", lse, None, None, "e5m2", 2000.0)
+    at = torch.cat([torch.arange(0, 64), torch.arange(K // 2, K // 2 + 64), torch.arange(K - 64, K)]).to(device())
+    check_product(out[0][:, at], d, err, p.w[:, at].contiguous(), p.fw, p.sw, 2000.0, 1 / 2000.0, "e5m2", "exact", ("dx", BF))
+    assert torch.isfinite(out[0].float()).all() and torch.isfinite(out[1].float()).all()

@@ -55,3 +55,17 @@ def test_a_head_has_room_for_the_lookups_of_fewer_tokens(host):
     space = fm.Fp8VocabHead(T, H, V, pieces=1, device="cpu").workspace.numel()
     for n in (1, 8193, 65536, 65537, T):
         assert host.need(n, H) <= space
+
+
+# (rows, vocabulary, hidden): small and large, odd, and hidden sizes at which the longest piece of the gradient, 2^31 codes of the weight, is shorter than the vocabulary
+VOCABS = [(1, 1, 16), (1, 131072, 4096), (3, 255, 48), (16, 300, 1024), (17, 257, 128), (63, 50021, 2048), (219, 50021, 2048), (1000, 3000, 64), (1003, 50021, 4096), (2047, 8201, 2048),
+          (2048, 32000, 4096), (8191, 65537, 4096), (8192, 65536, 4096), (1000, 40000, 65536), (16, 300, 1 << 22), (500, 600, 1 << 22), (17, 1800, 1 << 20), (7, 1 << 23, 16)]
+PIECES = (1, 2, 3, 4, 5, 8, 33, 1000)
+
+
+@pytest.mark.parametrize("M,V,K", VOCABS)
+def test_vocab_workspace_is_never_below_its_least(M, V, K):
+    """A size for any number of pieces is one that both calls accept."""
+    least = fm.vocab_workspace_bytes(M, V, K, 0)
+    assert all(fm.vocab_workspace_bytes(M, V, K, pieces) >= least for pieces in PIECES)
+    assert fm.load_library().fp8_vocab_cross_entropy_backward(P, 0, P, 0, M, V, K, P, P, P, 1, P, P, 1, P, P, P, 1, P, 1, None, None, 0, P, least - 1, None) == EWS
