@@ -14,30 +14,6 @@
 #include "vocab_dispatch.hpp"
 
 namespace fp8mi {
-namespace {
-
-// Estimate of the passes over pieces of P columns, in microseconds: the three products of each, and its
-// passes over dx's fp32 sums.
-double pieces_time(const VocabOperands& o, int64_t V, int64_t P, int accum) {
-  const int64_t cus = persistent_groups(1);
-  const bool fp8 = accum == kAccumMfma8;
-  double t = 0.0;
-  for (int64_t col = 0; col < V; col += P) {
-    const int64_t n = V - col < P ? V - col : P;
-    double one = plan_rounds(o.M, n, o.K, logits_mode(o.M, accum) == kAccumMfma8, 0, cus).us + plan_rounds(o.K, o.M, n, fp8, 0, cus).us +
-                 plan_rounds(o.K, n, o.M, fp8, 0, cus).us;
-    if (P < V) one += 8.0 * o.M * o.K / 5.0e6;
-    if (n == P && V / P > 1) {  // all whole pieces at once
-      t += one * (double)(V / P);
-      col += (V / P - 1) * P;
-    } else {
-      t += one;
-    }
-  }
-  return t;
-}
-
-}  // namespace
 
 hipError_t launch_vocab_grad(const VocabOperands& o, int64_t col, int64_t N, const LogitGradEpi& epi, int accum, hipStream_t stream) {
   const int mode = logits_mode(o.M, accum);
@@ -63,23 +39,7 @@ hipError_t launch_vocab_cross_entropy_backward(const VocabOperands& o, int64_t V
   const int64_t M = o.M, K = o.K, ldt = up128(M);
   const int64_t dwsize = dwtype == kBF16 ? 2 : 4;
   if (M == 0) return dw ? launch_fill_rows(nullptr, dw, V * K * dwsize / 16, stream) : hipSuccess;
-  // The longest piece that fits, then pieces of equal length.
-  int64_t P = V;
-  if (!grad_whole(M, V, K, workspace_bytes)) {
-    const int64_t fit = grad_longest(M, K, workspace_bytes);
-    // As few pieces as fit, or up to four more where the estimate prefers them: tiles that fill whole rounds of
-    // the compute units are worth another pass over dx's sums (8192 x 4096 x 65536 on the FP8 cores over 512 MiB: four pieces of 16384 columns 5.21 ms, the three that fit 5.40).
-    const int64_t least = (V + fit - 1) / fit;
-    double best = 1e300;
-    for (int64_t pieces = least; pieces <= least + 4; ++pieces) {
-      const int64_t p = up256((V + pieces - 1) / pieces);
-      const double t = pieces_time(o, V, p, accum);
-      if (t < best) {
-        best = t;
-        P = p;
-      }
-    }
-  }
+  const int64_t P = grad_piece(M, V, K, workspace_bytes, logits_mode(M, accum) == kAccumMfma8, accum == kAccumMfma8, persistent_groups(1));
   uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
   uint8_t* const q = ws;
   uint8_t* const q_t = q + up256(M * up128(P));

@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "gemm_rounds.hpp"
+
 namespace fp8mi {
 
 // Pieces of the vocabulary are multiples of so many columns (the widest tile), but for the last.
@@ -35,10 +37,11 @@ inline bool grad_whole(int64_t M, int64_t V, int64_t K, size_t workspace_bytes) 
   return V <= most_columns(K) && grad_bytes(M, V, K, V) <= (int64_t)workspace_bytes;
 }
 
-// Otherwise: the longest piece that it holds (the entry point has seen to kPieceCols).
+// Otherwise: the longest piece that it holds (the entry point has seen to kPieceCols).  Whole steps of the codes
+// leave nothing to round up, so a size that was asked for pieces of so many columns holds them.
 inline int64_t grad_longest(int64_t M, int64_t K, size_t workspace_bytes) {
   const int64_t most = most_columns(K);
-  int64_t fit = ((int64_t)workspace_bytes - up256(M * K * 4) - 512) / (M + up128(M)) / kPieceCols * kPieceCols;
+  int64_t fit = ((int64_t)workspace_bytes - up256(M * K * 4)) / (M + up128(M)) / kPieceCols * kPieceCols;
   fit = fit < kPieceCols ? kPieceCols : fit;
   return fit < most ? fit : most;
 }
@@ -55,6 +58,43 @@ inline size_t vocab_workspace(int64_t M, int64_t V, int64_t K, int64_t pieces) {
   // one piece needs no sums of dx, so it may be the smaller
   if (V <= most && whole < back) back = whole;
   return back > fwd ? back : fwd;
+}
+
+// Estimate of the gradient's passes over pieces of P columns, in microseconds: the three products of each, and its
+// passes over dx's fp32 sums.  `fp8_logits`, `fp8`: the logits' and the products' cores.
+inline double pieces_time(int64_t M, int64_t V, int64_t K, int64_t P, bool fp8_logits, bool fp8, int64_t cus) {
+  double t = 0.0;
+  for (int64_t col = 0; col < V; col += P) {
+    const int64_t n = V - col < P ? V - col : P;
+    double one = plan_rounds(M, n, K, fp8_logits, 0, cus).us + plan_rounds(K, M, n, fp8, 0, cus).us + plan_rounds(K, n, M, fp8, 0, cus).us;
+    if (P < V) one += 8.0 * M * K / 5.0e6;
+    if (n == P && V / P > 1) {  // all whole pieces at once
+      t += one * (double)(V / P);
+      col += (V / P - 1) * P;
+    } else {
+      t += one;
+    }
+  }
+  return t;
+}
+
+// Columns of the gradient's pieces: the whole vocabulary where the workspace holds it.  Otherwise equal pieces, as few as
+// fit, or up to four more where the estimate prefers them: tiles that fill whole rounds of the compute units are worth another
+// pass over dx's sums (8192 x 4096 x 65536 on the FP8 cores over 512 MiB: four pieces of 16384 columns 5.21 ms, the three that fit 5.40).
+inline int64_t grad_piece(int64_t M, int64_t V, int64_t K, size_t workspace_bytes, bool fp8_logits, bool fp8, int64_t cus) {
+  if (grad_whole(M, V, K, workspace_bytes)) return V;
+  const int64_t fit = grad_longest(M, K, workspace_bytes), least = (V + fit - 1) / fit;
+  int64_t P = fit;
+  double best = 1e300;
+  for (int64_t pieces = least; pieces <= least + 4; ++pieces) {
+    const int64_t p = up256((V + pieces - 1) / pieces);
+    const double t = pieces_time(M, V, K, p, fp8_logits, fp8, cus);
+    if (t < best) {
+      best = t;
+      P = p;
+    }
+  }
+  return P;
 }
 
 }  // namespace fp8mi

@@ -14,8 +14,14 @@ EWS = -10
 P = ctypes.c_void_p(0x10000)  # never dereferenced
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "fp8_precision_numerics_amd", "csrc")
 SHIM = """#include "token_chunks.hpp"
+#include "vocab_pieces.hpp"
 extern "C" size_t need(int64_t rows, int64_t cols) { return fp8mi::embedding_need(rows, cols); }
 extern "C" int64_t chunks(int64_t rows) { return fp8mi::chunk_count(rows); }
+extern "C" int64_t most(int64_t k) { return fp8mi::most_columns(k); }
+extern "C" int whole(int64_t m, int64_t v, int64_t k, size_t bytes) { return fp8mi::grad_whole(m, v, k, bytes); }
+extern "C" int64_t longest(int64_t m, int64_t k, size_t bytes) { return fp8mi::grad_longest(m, k, bytes); }
+extern "C" int64_t piece(int64_t m, int64_t v, int64_t k, size_t bytes, int fp8) { return fp8mi::grad_piece(m, v, k, bytes, fp8 != 0, fp8 != 0, 256); }
+extern "C" int64_t grad_bytes(int64_t m, int64_t v, int64_t k, int64_t p) { return fp8mi::grad_bytes(m, v, k, p); }
 """
 
 
@@ -30,6 +36,10 @@ def host(tmp_path_factory):
     lib = ctypes.CDLL(str(d / "shim.so"))
     lib.need.argtypes, lib.need.restype = [ctypes.c_int64] * 2, ctypes.c_size_t
     lib.chunks.argtypes, lib.chunks.restype = [ctypes.c_int64], ctypes.c_int64
+    for name, args in (("most", "i"), ("whole", "iiis"), ("longest", "iis"), ("piece", "iiisc"), ("grad_bytes", "iiii")):
+        f = getattr(lib, name)
+        f.argtypes = [dict(i=ctypes.c_int64, s=ctypes.c_size_t, c=ctypes.c_int)[a] for a in args]
+        f.restype = ctypes.c_int if name == "whole" else ctypes.c_int64
     return lib
 
 
@@ -69,3 +79,23 @@ def test_vocab_workspace_is_never_below_its_least(M, V, K):
     least = fm.vocab_workspace_bytes(M, V, K, 0)
     assert all(fm.vocab_workspace_bytes(M, V, K, pieces) >= least for pieces in PIECES)
     assert fm.load_library().fp8_vocab_cross_entropy_backward(P, 0, P, 0, M, V, K, P, P, P, 1, P, P, 1, P, P, P, 1, P, 1, None, None, 0, P, least - 1, None) == EWS
+
+
+@pytest.mark.parametrize("M,V,K", VOCABS)
+def test_vocab_workspace_holds_the_pieces_it_was_asked_for(host, M, V, K):
+    """A workspace for so many pieces serves the gradient in no more, but where the longest piece asks for it; what the estimate
+    then takes is at most four more of them, and always fits."""
+    for pieces in PIECES:
+        size = fm.vocab_workspace_bytes(M, V, K, pieces)
+        least = 1 if host.whole(M, V, K, size) else -(-V // host.longest(M, K, size))
+        assert least <= max(pieces, -(-V // host.most(K))), pieces
+        for fp8 in (0, 1):
+            P = host.piece(M, V, K, size, fp8)
+            assert host.grad_bytes(M, V, K, P) <= size and P <= host.most(K) and -(-V // P) <= least + 4 and (P == V or P % 256 == 0)
+
+
+def test_pieces_of_a_training_step(host):
+    """8192 x 65536 x 4096: 2, 4 and 8 pieces asked for are 2, 4 and 8 that fit."""
+    for pieces in (1, 2, 4, 8):
+        size = fm.vocab_workspace_bytes(8192, 65536, 4096, pieces)
+        assert (1 if host.whole(8192, 65536, 4096, size) else -(-65536 // host.longest(8192, 4096, size))) == pieces
