@@ -34,8 +34,6 @@
 namespace fp8mi {
 namespace {
 
-constexpr int kWavesFew = 8;
-
 // Bytes [16 i, 16 i + 16) and [64 + 16 i, 64 + 16 i + 16) of a 128-byte K step (i: lane
 // group), so that the four lanes of a row read 64 contiguous bytes.
 struct Slice {
@@ -188,34 +186,21 @@ __global__ __launch_bounds__(64 * kWavesFew) void gemm_few_rows_kernel(const uin
   }
 }
 
-// Waves that share a tile's K: as many as give the chip about 8 a compute unit.
-int few_split(int64_t N) {
-  const int64_t tiles = (N + 15) / 16;
-  int split = 1;
-  while (split < kWavesFew && tiles * split < persistent_groups(8)) split *= 2;
-  return split;
-}
-
-int few_groups(int64_t N) {
-  const int64_t tiles = (N + 15) / 16, tiles_wg = kWavesFew / few_split(N);
-  return (int)((tiles + tiles_wg - 1) / tiles_wg);
-}
-
 template <int FA, int FB, bool GATED, class EPI>
 hipError_t few_run(const uint8_t* A, const uint8_t* B, int64_t M, int64_t N, int64_t K, const float* sa,
-                   const float* sb, const EPI& epi, hipStream_t st) {
-  hipLaunchKernelGGL((gemm_few_rows_kernel<FA, FB, GATED, EPI>), dim3((unsigned)few_groups(N)), dim3(64 * kWavesFew), 0,
-                     st, A, B, (int)M, (int)N, (int)K, sa, sb, epi, few_split(N));
+                   const float* sb, const EPI& epi, int split, hipStream_t st) {
+  hipLaunchKernelGGL((gemm_few_rows_kernel<FA, FB, GATED, EPI>), dim3((unsigned)few_groups(N, split)), dim3(64 * kWavesFew),
+                     0, st, A, B, (int)M, (int)N, (int)K, sa, sb, epi, split);
   return hipGetLastError();
 }
 
 template <bool GATED, class EPI>
 hipError_t few_fmt(const uint8_t* A, int fa, const uint8_t* B, int fb, int64_t M, int64_t N, int64_t K,
-                   const float* sa, const float* sb, const EPI& epi, hipStream_t st) {
-  if (fa == kE4M3 && fb == kE4M3) return few_run<kE4M3, kE4M3, GATED>(A, B, M, N, K, sa, sb, epi, st);
-  if (fa == kE5M2 && fb == kE4M3) return few_run<kE5M2, kE4M3, GATED>(A, B, M, N, K, sa, sb, epi, st);
-  if (fa == kE4M3 && fb == kE5M2) return few_run<kE4M3, kE5M2, GATED>(A, B, M, N, K, sa, sb, epi, st);
-  return few_run<kE5M2, kE5M2, GATED>(A, B, M, N, K, sa, sb, epi, st);
+                   const float* sa, const float* sb, const EPI& epi, int split, hipStream_t st) {
+  if (fa == kE4M3 && fb == kE4M3) return few_run<kE4M3, kE4M3, GATED>(A, B, M, N, K, sa, sb, epi, split, st);
+  if (fa == kE5M2 && fb == kE4M3) return few_run<kE5M2, kE4M3, GATED>(A, B, M, N, K, sa, sb, epi, split, st);
+  if (fa == kE4M3 && fb == kE5M2) return few_run<kE4M3, kE5M2, GATED>(A, B, M, N, K, sa, sb, epi, split, st);
+  return few_run<kE5M2, kE5M2, GATED>(A, B, M, N, K, sa, sb, epi, split, st);
 }
 
 }  // namespace
@@ -223,16 +208,17 @@ hipError_t few_fmt(const uint8_t* A, int fa, const uint8_t* B, int fb, int64_t M
 hipError_t launch_gemm_few_rows(const uint8_t* A, int fa, const uint8_t* B, int fb, int64_t M, int64_t N, int64_t K,
                                 const float* sinv_a, const float* sinv_b, const EpiArgs& epi, bool gated,
                                 hipStream_t stream) {
-  if (gated) return few_fmt<true>(A, fa, B, fb, M, N, K, sinv_a, sinv_b, epi, stream);
-  return few_fmt<false>(A, fa, B, fb, M, N, K, sinv_a, sinv_b, epi, stream);
+  const int split = few_split(N, persistent_groups(8));
+  if (gated) return few_fmt<true>(A, fa, B, fb, M, N, K, sinv_a, sinv_b, epi, split, stream);
+  return few_fmt<false>(A, fa, B, fb, M, N, K, sinv_a, sinv_b, epi, split, stream);
 }
 
 hipError_t launch_loss_few_rows(const uint8_t* A, int fa, const uint8_t* B, int fb, int64_t M, int64_t N, int64_t K,
-                                const float* sinv_a, const float* sinv_b, const LossEpi& epi, bool count_only,
-                                int* groups, hipStream_t stream) {
-  *groups = few_groups(N);
-  if (count_only) return hipSuccess;
-  return few_fmt<false>(A, fa, B, fb, M, N, K, sinv_a, sinv_b, epi, stream);
+                                const float* sinv_a, const float* sinv_b, const LossEpi& epi, int64_t slots, int* groups,
+                                hipStream_t stream) {
+  const int split = few_split(N, persistent_groups(8), slots);
+  *groups = (int)few_groups(N, split);
+  return few_fmt<false>(A, fa, B, fb, M, N, K, sinv_a, sinv_b, epi, split, stream);
 }
 
 }  // namespace fp8mi

@@ -119,21 +119,12 @@ hipError_t launch_vocab_cross_entropy(const VocabOperands& o, int64_t V, const T
   for (int64_t col = 0; col < V;) {
     int64_t n = V - col;
     hipError_t e;
+    const int64_t fit = slots * 128;  // the narrower tiles', and the streaming kernel's with a wave a tile
+    if (n > fit) n = fit / kPieceCols * kPieceCols;
+    epi.col0 = col;
     if (few) {
-      const auto run = [&](bool count_only) {
-        epi.col0 = col;
-        return launch_loss_few_rows(o.a, o.fa, o.b + col * o.K, o.fb, o.M, n, o.K, o.sinv_a, o.sinv_b, epi, count_only, &j.tiles, stream);
-      };
-      run(true);
-      while (j.tiles > slots) {  // half the columns, in whole tiles of 16
-        n = (n / 2 + 15) / 16 * 16;
-        run(true);
-      }
-      e = run(false);
+      e = launch_loss_few_rows(o.a, o.fa, o.b + col * o.K, o.fb, o.M, n, o.K, o.sinv_a, o.sinv_b, epi, slots, &j.tiles, stream);
     } else {
-      const int64_t fit = slots * 128;  // the narrower tiles'
-      if (n > fit) n = fit / kPieceCols * kPieceCols;
-      epi.col0 = col;
       e = launch_vocab_logits(o, col, n, epi, logits_mode(o.M, accum), &j.tiles, stream);
     }
     if (e != hipSuccess) return e;

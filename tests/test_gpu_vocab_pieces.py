@@ -28,3 +28,17 @@ def test_one_piece_asked_for_where_there_are_two():
     at = torch.cat([torch.arange(0, 64), torch.arange(K // 2, K // 2 + 64), torch.arange(K - 64, K)]).to(device())
     check_product(out[0][:, at], d, err, p.w[:, at].contiguous(), p.fw, p.sw, 2000.0, 1 / 2000.0, "e5m2", "exact", ("dx", BF))
     assert torch.isfinite(out[0].float()).all() and torch.isfinite(out[1].float()).all()
+
+
+@pytest.mark.parametrize("M,V,K", [(1, 32000, 256), (3, 4100, 1040), (8, 70000, 64), (16, 9000, 48)])
+def test_few_rows_with_the_least_that_holds_the_vocabulary(M, V, K):
+    """A pair a row for every 128 columns, as documented, serves the vocabulary whole; half of it in two pieces; nothing behind it is touched."""
+    announce(f"cross entropy of few rows {M}x{V}x{K}, least workspace of the whole vocabulary")
+    p = Problem(M, V, K)
+    up16 = lambda n: (n + 15) // 16 * 16  # noqa: E731
+    for columns in (V, V // 2, 256):
+        size = up16(M * 4) + up16(M * 8) + M * 8 * -(-columns // 128)
+        space = torch.full((size + 4096,), 0xA5, dtype=torch.uint8, device=device())
+        loss, lse = p.forward(workspace=space[:size])
+        check_forward(p, "exact", loss, lse, np.arange(M))
+        assert (space[size:] == 0xA5).all()

@@ -15,12 +15,16 @@ P = ctypes.c_void_p(0x10000)  # never dereferenced
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "fp8_precision_numerics_amd", "csrc")
 SHIM = """#include "token_chunks.hpp"
 #include "vocab_pieces.hpp"
+#include "few_rows_shape.hpp"
 extern "C" size_t need(int64_t rows, int64_t cols) { return fp8mi::embedding_need(rows, cols); }
 extern "C" int64_t chunks(int64_t rows) { return fp8mi::chunk_count(rows); }
 extern "C" int64_t most(int64_t k) { return fp8mi::most_columns(k); }
 extern "C" int whole(int64_t m, int64_t v, int64_t k, size_t bytes) { return fp8mi::grad_whole(m, v, k, bytes); }
 extern "C" int64_t longest(int64_t m, int64_t k, size_t bytes) { return fp8mi::grad_longest(m, k, bytes); }
 extern "C" int64_t piece(int64_t m, int64_t v, int64_t k, size_t bytes, int fp8) { return fp8mi::grad_piece(m, v, k, bytes, fp8 != 0, fp8 != 0, 256); }
+extern "C" size_t loss_bytes(int64_t m, int64_t p) { return fp8mi::vocab_loss_bytes(m, p); }
+extern "C" int64_t few_split(int64_t n, int64_t waves, int64_t most) { return fp8mi::few_split(n, waves, most); }
+extern "C" int64_t few_groups(int64_t n, int split) { return fp8mi::few_groups(n, split); }
 extern "C" int64_t grad_bytes(int64_t m, int64_t v, int64_t k, int64_t p) { return fp8mi::grad_bytes(m, v, k, p); }
 """
 
@@ -36,10 +40,11 @@ def host(tmp_path_factory):
     lib = ctypes.CDLL(str(d / "shim.so"))
     lib.need.argtypes, lib.need.restype = [ctypes.c_int64] * 2, ctypes.c_size_t
     lib.chunks.argtypes, lib.chunks.restype = [ctypes.c_int64], ctypes.c_int64
-    for name, args in (("most", "i"), ("whole", "iiis"), ("longest", "iis"), ("piece", "iiisc"), ("grad_bytes", "iiii")):
+    for name, args in (("most", "i"), ("whole", "iiis"), ("longest", "iis"), ("piece", "iiisc"), ("grad_bytes", "iiii"), ("loss_bytes", "ii"), ("few_split", "iii"),
+                       ("few_groups", "ic")):
         f = getattr(lib, name)
         f.argtypes = [dict(i=ctypes.c_int64, s=ctypes.c_size_t, c=ctypes.c_int)[a] for a in args]
-        f.restype = ctypes.c_int if name == "whole" else ctypes.c_int64
+        f.restype = dict(whole=ctypes.c_int, loss_bytes=ctypes.c_size_t).get(name, ctypes.c_int64)
     return lib
 
 
@@ -99,3 +104,19 @@ def test_pieces_of_a_training_step(host):
     for pieces in (1, 2, 4, 8):
         size = fm.vocab_workspace_bytes(8192, 65536, 4096, pieces)
         assert (1 if host.whole(8192, 65536, 4096, size) else -(-65536 // host.longest(8192, 4096, size))) == pieces
+
+
+def test_few_rows_fit_where_a_pair_for_every_128_columns_does(host):
+    """The streaming kernel leaves a pair a workgroup: with the documented bytes for the whole vocabulary its workgroups are no more than
+    the pairs, and with room for more they are as many as without a limit."""
+    for V in (1, 16, 100, 128, 129, 1000, 16384, 32000, 50021, 65536, 131072, 1 << 20):
+        for M in (1, 3, 8, 16):
+            slots = (host.loss_bytes(M, V) - host.loss_bytes(M, 0)) // (8 * M)
+            assert slots == -(-V // 128)
+            for waves in (512, 2048, 2432):
+                free = host.few_split(V, waves, 1 << 62)
+                split = host.few_split(V, waves, slots)
+                assert split in (1, 2, 4, 8) and host.few_groups(V, split) <= slots
+                assert split == free or host.few_groups(V, 2 * split) > slots
+                assert host.few_split(V, waves, host.few_groups(V, free)) == free
+    assert host.few_split(32000, 2048, 1 << 62) == 2 and host.few_groups(32000, 2) == 500 and host.few_split(32000, 2048, 250) == 1
