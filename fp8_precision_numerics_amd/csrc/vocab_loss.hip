@@ -116,11 +116,13 @@ hipError_t launch_vocab_cross_entropy(const VocabOperands& o, int64_t V, const T
   // padding to 64 rows does, if there is a tile for every compute unit: 16 rows, 131072 x 4096 123 us against 110, 50021 x 1024 23 against
   // 18, but 32000 x 4096 (250 tiles) 38 both; 8 rows 108 against 110.
   const bool few = o.M <= kFewRows / 2 || (o.M <= kFewRows && (V + 127) / 128 < persistent_groups(1));
+  const int64_t longest = few ? kFewColumns : launch_columns(o.M);
   for (int64_t col = 0; col < V;) {
     int64_t n = V - col;
     hipError_t e;
     const int64_t fit = slots * 128;  // the narrower tiles', and the streaming kernel's with a wave a tile
     if (n > fit) n = fit / kPieceCols * kPieceCols;
+    if (n > longest) n = longest;
     epi.col0 = col;
     if (few) {
       e = launch_loss_few_rows(o.a, o.fa, o.b + col * o.K, o.fb, o.M, n, o.K, o.sinv_a, o.sinv_b, epi, slots, &j.tiles, stream);

@@ -26,21 +26,27 @@ inline int64_t grad_bytes(int64_t M, int64_t V, int64_t K, int64_t P) {
   return up256(M * up128(P)) + up256(P * up128(M)) + (P < V ? up256(M * K * 4) : 0);
 }
 
-// The longest piece that the gradient's products' offsets reach.
-inline int64_t most_columns(int64_t K) {
-  const int64_t most = ((int64_t(1) << 31) - 1) / K / kPieceCols * kPieceCols;
-  return most < (int64_t(1) << 22) ? most : (int64_t(1) << 22);
+// Columns of one launch of the logits' products, whose threads have to be fewer than 2^32: 256 a tile of 64 x 128, and
+// 512 for 128 columns of the streaming kernel.
+inline int64_t launch_columns(int64_t M) { return ((int64_t(1) << 24) - 1) / ((M + 63) / 64) * 128 / kPieceCols * kPieceCols; }
+constexpr int64_t kFewColumns = int64_t(1) << 29;
+
+// The longest piece of the gradient: what its products' offsets reach, and a launch.
+inline int64_t most_columns(int64_t M, int64_t K) {
+  int64_t most = ((int64_t(1) << 31) - 1) / K / kPieceCols * kPieceCols;
+  most = most < (int64_t(1) << 22) ? most : (int64_t(1) << 22);
+  return most < launch_columns(M) ? most : launch_columns(M);
 }
 
 // Whether a workspace holds the gradient's vocabulary whole.
 inline bool grad_whole(int64_t M, int64_t V, int64_t K, size_t workspace_bytes) {
-  return V <= most_columns(K) && grad_bytes(M, V, K, V) <= (int64_t)workspace_bytes;
+  return V <= most_columns(M, K) && grad_bytes(M, V, K, V) <= (int64_t)workspace_bytes;
 }
 
 // Otherwise: the longest piece that it holds (the entry point has seen to kPieceCols).  Whole steps of the codes
 // leave nothing to round up, so a size that was asked for pieces of so many columns holds them.
 inline int64_t grad_longest(int64_t M, int64_t K, size_t workspace_bytes) {
-  const int64_t most = most_columns(K);
+  const int64_t most = most_columns(M, K);
   int64_t fit = ((int64_t)workspace_bytes - up256(M * K * 4)) / (M + up128(M)) / kPieceCols * kPieceCols;
   fit = fit < kPieceCols ? kPieceCols : fit;
   return fit < most ? fit : most;
@@ -50,7 +56,7 @@ inline int64_t grad_longest(int64_t M, int64_t K, size_t workspace_bytes) {
 // directions take), or as many more as the longest piece asks for.
 inline size_t vocab_workspace(int64_t M, int64_t V, int64_t K, int64_t pieces) {
   if (M == 0) return 0;
-  const int64_t asked = pieces > 0 ? up256((V + pieces - 1) / pieces) : kPieceCols, most = most_columns(K);
+  const int64_t asked = pieces > 0 ? up256((V + pieces - 1) / pieces) : kPieceCols, most = most_columns(M, K);
   // A vocabulary that is longer than the longest piece needs dx's sums, however few pieces are asked for.
   const int64_t P = asked < most ? asked : most;
   size_t back = (size_t)grad_bytes(M, V, K, P < V ? P : V);

@@ -42,3 +42,28 @@ def test_few_rows_with_the_least_that_holds_the_vocabulary(M, V, K):
         loss, lse = p.forward(workspace=space[:size])
         check_forward(p, "exact", loss, lse, np.arange(M))
         assert (space[size:] == 0xA5).all()
+
+
+def test_a_vocabulary_of_more_columns_than_one_launch_has():
+    """2^30 + 300 columns: more threads than a launch takes, so two pieces, though the workspace holds more.  A row of x that is 1 at
+    its first place makes each logit a code of the weight, one of nine in turn, so lse is a sum of nine terms: SUMS of it for the exponentials and
+    their sums (a lane of the joining kernel adds 2^15 pairs, each tile's over 128 columns: 2^15 roundings of 2^-24 at most)."""
+    announce("cross entropy 1 x (2^30 + 300) x 16")
+    V, K = (1 << 30) + 300, 16
+    codes = torch.arange(0x28, 0x31, dtype=torch.uint8, device=device())
+    w = torch.zeros((V, K), dtype=torch.uint8, device=device())
+    step = 9 << 24
+    for v in range(0, V, step):
+        n = min(step, V - v)
+        w[v:v + n, 0] = codes.repeat(-(-n // 9))[:n]
+    x = torch.zeros((1, K), dtype=torch.uint8, device=device())
+    x[0, 0] = 0x38                                                                   # 1
+    one, loss, lse = torch.ones(1, device=device()), torch.zeros(1, device=device()), torch.zeros(1, device=device())
+    z = codes.view(torch.float8_e4m3fn).double().cpu().numpy()
+    count = np.array([len(range(i, V, 9)) for i in range(9)], dtype=np.float64)
+    want = np.log(np.sum(count * np.exp(z)))
+    ws = torch.empty(1 << 28, dtype=torch.uint8, device=device())
+    for target in (0, (1 << 29) + 5, V - 1):
+        fm.fp8_vocab_cross_entropy(x, "e4m3", w, "e4m3", one, one, torch.tensor([target], device=device()), loss, lse, workspace=ws)
+        tol = 2.0 ** -9 + 1e-5 + 32 * 2.0 ** -24 * want
+        assert abs(lse.item() - want) <= tol and abs(loss.item() - (want - z[target % 9])) <= tol

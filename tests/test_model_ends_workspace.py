@@ -18,7 +18,9 @@ SHIM = """#include "token_chunks.hpp"
 #include "few_rows_shape.hpp"
 extern "C" size_t need(int64_t rows, int64_t cols) { return fp8mi::embedding_need(rows, cols); }
 extern "C" int64_t chunks(int64_t rows) { return fp8mi::chunk_count(rows); }
-extern "C" int64_t most(int64_t k) { return fp8mi::most_columns(k); }
+extern "C" int64_t most(int64_t m, int64_t k) { return fp8mi::most_columns(m, k); }
+extern "C" int64_t launch_columns(int64_t m) { return fp8mi::launch_columns(m); }
+extern "C" int64_t few_columns() { return fp8mi::kFewColumns; }
 extern "C" int whole(int64_t m, int64_t v, int64_t k, size_t bytes) { return fp8mi::grad_whole(m, v, k, bytes); }
 extern "C" int64_t longest(int64_t m, int64_t k, size_t bytes) { return fp8mi::grad_longest(m, k, bytes); }
 extern "C" int64_t piece(int64_t m, int64_t v, int64_t k, size_t bytes, int fp8) { return fp8mi::grad_piece(m, v, k, bytes, fp8 != 0, fp8 != 0, 256); }
@@ -40,7 +42,7 @@ def host(tmp_path_factory):
     lib = ctypes.CDLL(str(d / "shim.so"))
     lib.need.argtypes, lib.need.restype = [ctypes.c_int64] * 2, ctypes.c_size_t
     lib.chunks.argtypes, lib.chunks.restype = [ctypes.c_int64], ctypes.c_int64
-    for name, args in (("most", "i"), ("whole", "iiis"), ("longest", "iis"), ("piece", "iiisc"), ("grad_bytes", "iiii"), ("loss_bytes", "ii"), ("few_split", "iii"),
+    for name, args in (("most", "ii"), ("launch_columns", "i"), ("few_columns", ""), ("whole", "iiis"), ("longest", "iis"), ("piece", "iiisc"), ("grad_bytes", "iiii"), ("loss_bytes", "ii"), ("few_split", "iii"),
                        ("few_groups", "ic")):
         f = getattr(lib, name)
         f.argtypes = [dict(i=ctypes.c_int64, s=ctypes.c_size_t, c=ctypes.c_int)[a] for a in args]
@@ -93,10 +95,10 @@ def test_vocab_workspace_holds_the_pieces_it_was_asked_for(host, M, V, K):
     for pieces in PIECES:
         size = fm.vocab_workspace_bytes(M, V, K, pieces)
         least = 1 if host.whole(M, V, K, size) else -(-V // host.longest(M, K, size))
-        assert least <= max(pieces, -(-V // host.most(K))), pieces
+        assert least <= max(pieces, -(-V // host.most(M, K))), pieces
         for fp8 in (0, 1):
             P = host.piece(M, V, K, size, fp8)
-            assert host.grad_bytes(M, V, K, P) <= size and P <= host.most(K) and -(-V // P) <= least + 4 and (P == V or P % 256 == 0)
+            assert host.grad_bytes(M, V, K, P) <= size and P <= host.most(M, K) and -(-V // P) <= least + 4 and (P == V or P % 256 == 0)
 
 
 def test_pieces_of_a_training_step(host):
@@ -120,3 +122,12 @@ def test_few_rows_fit_where_a_pair_for_every_128_columns_does(host):
                 assert split == free or host.few_groups(V, 2 * split) > slots
                 assert host.few_split(V, waves, host.few_groups(V, free)) == free
     assert host.few_split(32000, 2048, 1 << 62) == 2 and host.few_groups(32000, 2) == 500 and host.few_split(32000, 2048, 250) == 1
+
+
+def test_a_launch_has_fewer_than_2_32_threads(host):
+    """Whatever the workspace holds: a launch of the logits' product on the smallest tiles, and of the streaming kernel."""
+    for M in (1, 16, 17, 64, 65, 8192, 1 << 20, (1 << 23) - 16):
+        n = host.launch_columns(M)
+        assert n >= 256 and n % 256 == 0 and -(-M // 64) * -(-n // 128) * 256 < 1 << 32
+        assert host.most(M, 16) <= n
+    assert host.few_columns() % 256 == 0 and host.few_groups(host.few_columns(), 1) * 512 < 1 << 32
