@@ -509,13 +509,14 @@ __global__ __launch_bounds__(NT) void layernorm_backward_long_kernel(LayerBackAr
   }
 }
 
-// The partial rows' sums: 16 columns a workgroup, dweight's columns first, then dbias's.
+// The partial rows' sums: 16 columns a workgroup, dweight's columns first, then dbias's; `first`: the launch's first of those.
 __global__ __launch_bounds__(16 * kSumLanes) void layer_sums_kernel(const float* dw, const float* db, int64_t pitch,
                                                                    int count, int64_t cols, float* dweight,
-                                                                   float* dbias) {
+                                                                   float* dbias, int64_t first) {
   const int64_t groups = cols / 16;  // cols is a multiple of 16
-  const bool second = !dw || blockIdx.x >= groups;
-  const int64_t c = (int64_t)(blockIdx.x - (dw && second ? groups : 0)) * 16 + (threadIdx.x & 15);
+  const int64_t block = first + blockIdx.x;
+  const bool second = !dw || block >= groups;
+  const int64_t c = (block - (dw && second ? groups : 0)) * 16 + (threadIdx.x & 15);
   const float v = column_sum(second ? db : dw, count, pitch, c, true);
   if (threadIdx.x < 16) (second ? dbias : dweight)[c] = v;
 }
@@ -639,8 +640,11 @@ hipError_t launch_layernorm_backward(const void* dy, const void* h, const float*
     if (e != hipSuccess) return e;
   }
   if (sums && g != 1) {
-    hipLaunchKernelGGL(layer_sums_kernel, dim3((unsigned)(sums * (cols / 16))), dim3(16 * kSumLanes), 0, stream, a.dw,
-                       a.db, a.pitch, g, cols, dweight, dbias);
+    // (a launch has fewer than 2^32 threads)
+    const int64_t blocks = sums * (cols / 16), most = int64_t(1) << 21;
+    for (int64_t first = 0; first < blocks; first += most)
+      hipLaunchKernelGGL(layer_sums_kernel, dim3((unsigned)(blocks - first < most ? blocks - first : most)), dim3(16 * kSumLanes),
+                         0, stream, a.dw, a.db, a.pitch, g, cols, dweight, dbias, first);
     return hipGetLastError();
   }
   return hipSuccess;
