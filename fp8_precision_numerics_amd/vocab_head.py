@@ -33,8 +33,8 @@ class Fp8VocabHead:
                  recipe: Recipe = Recipe(), accum: str = "exact", device="cuda"):
         if recipe.fmt_fwd != "e4m3" or recipe.fmt_bwd != "e5m2":
             raise ValueError("Fp8VocabHead implements the HYBRID recipe (E4M3 forward, E5M2 backward)")
-        if not 0.0 <= dropout < 1.0:
-            raise ValueError(f"dropout must be in [0, 1), got {dropout}")
+        if not 0.0 <= dropout < 1.0 or round(dropout * 65536) > 65535:
+            raise ValueError(f"dropout must be in [0, 1), in steps of 2^-16, got {dropout}")
         dev = torch.device(device)
         self.shape, self.eps, self.dropout, self.accum = (tokens, hidden, vocab), eps, dropout, accum
         self.state_n, self.state_w = (DelayedScalingState(recipe.fmt_fwd, recipe.history_len, device=dev) for _ in range(2))
@@ -50,9 +50,11 @@ class Fp8VocabHead:
         self._cast = False  # the weight has codes
         self._kept = False  # the buffers and scales are those of one training forward
 
-    def _check(self, t, shape, name):
+    def _check(self, t, shape, name, dtype=None):
         if tuple(t.shape) != shape:
             raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
+        if dtype is not None and t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
 
     def _need_codes(self):
         if not self._cast:
@@ -73,7 +75,7 @@ class Fp8VocabHead:
         _b.fp8_embedding(tokens, self.qw, out, scale=scale, fmt=self.state_w.fmt, sinv=self.state_w.scale_inv_used, stream=stream)
 
     def embed_backward(self, tokens, dy, dw, scale: float = 1.0, stream=None):
-        """Adds the lookup's gradient (dy [n x hidden], n up to the head's tokens) to dw [vocab x hidden], which holds the projection's."""
+        """Adds the lookup's gradient (dy [n x hidden], n up to the head's tokens and 2^20) to dw [vocab x hidden], which holds the projection's."""
         T, H, V = self.shape
         self._check(dw, (V, H), "dw")
         if tokens.numel() > T:
@@ -92,8 +94,12 @@ class Fp8VocabHead:
         self._check(x, (T, H), "x")
         self._check(targets, (T,), "targets")
         drop = self.dropout if train else 0.0
-        if drop and rng is None:
-            raise ValueError("a training forward with dropout needs rng")
+        if drop:
+            if rng is None:
+                raise ValueError("a training forward with dropout needs rng")
+            self._check(rng, (2,), "rng", torch.int64)
+        if lse is not None:
+            self._check(lse, (T,), "lse", torch.float32)
         if train:
             self._kept = False
             with _on(stream):
