@@ -1,4 +1,5 @@
-"""The vocabulary's cross entropy in pieces: the longest hidden size, whose vocabulary is longer than one piece may be.
+"""The vocabulary's cross entropy in pieces: the longest hidden size, whose vocabulary is longer than one piece may be, the least
+workspaces, more columns than one launch has, and what pieces and cut products leave (statistics, sums, either gradient alone).
 Tolerances as in test_gpu_vocab_cross_entropy.py."""
 
 import numpy as np
@@ -6,8 +7,11 @@ import pytest
 import torch
 
 import fp8_precision_numerics_amd as fm
+import vocab_cases
+import vocab_product_cases
 from gpu_helpers import announce, device
-from test_gpu_vocab_cross_entropy import Problem, check_backward, check_forward, check_product, gradient
+from test_gpu_feed_forward import EW
+from test_gpu_vocab_cross_entropy import Problem, check_backward, check_forward, check_product, decoded, gradient
 
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
@@ -67,3 +71,73 @@ def test_a_vocabulary_of_more_columns_than_one_launch_has():
         fm.fp8_vocab_cross_entropy(x, "e4m3", w, "e4m3", one, one, torch.tensor([target], device=device()), loss, lse, workspace=ws)
         tol = 2.0 ** -9 + 1e-5 + 32 * 2.0 ** -24 * want
         assert abs(lse.item() - want) <= tol and abs(loss.item() - (want - z[target % 9])) <= tol
+
+
+def check_statistics(p, accum, lse, amax, sat, fmt, scale):
+    """amax and the count against d of all rows and columns, in fp64 on the device.  The bound of a logit on the FP8 cores: a run of eight products
+    loses less than 2^(E - 12) of each, E the exponent of the largest (gpu_helpers), so less than 8 2^-12 of that one, hence of the sum of magnitudes; then its fp32 sums."""
+    a, s = decoded(p.x, p.fx), p.sx.double() * p.sw.double()
+    part = 1e-5 if accum == "exact" or p.M <= 16 else 2.0 ** -9 + 2 * (p.K / 8 + 2) * 2.0 ** -24
+    t, g, l = torch.from_numpy(p.t).to(device())[:, None], p.dloss.double()[:, None], lse.double()[:, None]
+    live = (t >= 0) & (t < p.V)
+    limit = 448.0 if fmt == "e4m3" else 57344.0
+    low = high = 0.0
+    least = most = 0
+    for c in range(0, p.V, 1024):
+        b = decoded(p.w[c:c + 1024], p.fw)
+        z, B = a @ b.t() * s, part * (a.abs() @ b.abs().t()) * s
+        hit = (t == torch.arange(c, c + b.shape[0], device=device())).double()
+        prob = (z - l).exp()
+        d = torch.where(live, (g * (prob - hit)).abs(), 0.0)
+        err = torch.where(live, g.abs() * (prob * torch.expm1(B) + EW * (prob * (1 + (z - l).abs()) + hit)), 0.0)
+        low, high = max(low, (d - err).max().item()), max(high, (d + err).max().item())
+        least += ((d - err) * scale * (1 - 1e-6) > limit).sum().item()
+        most += ((d + err) * scale * (1 + 1e-6) > limit).sum().item()
+    assert low <= amax.item() * (1 + 1e-6) and amax.item() <= high * (1 + 1e-6), (low, amax.item(), high)
+    assert least <= sat.item() <= most and most > 0, (least, sat.item(), most)
+
+
+@pytest.mark.parametrize("M,V,K", list(vocab_cases.LOGITS) + [c for c in vocab_product_cases.CUT if c not in vocab_cases.LOGITS])
+@pytest.mark.parametrize("accum", ["exact", "mfma_fp8"])
+def test_statistics_of_large_products(M, V, K, accum):
+    """On every tile shape of the logits, in one launch and in two, in one piece and in several."""
+    announce(f"cross entropy statistics {M}x{V}x{K} {accum}")
+    p = Problem(M, V, K, seed=5)
+    lse = p.forward(accum)[1]
+    for pieces in (1, 2):
+        _, _, amax, sat = p.backward(lse, accum, pieces, "e5m2", 30000.0, (BF, BF))
+        check_statistics(p, accum, lse, amax, sat, "e5m2", 30000.0)
+
+
+@pytest.mark.parametrize("case", vocab_product_cases.CUT)
+@pytest.mark.parametrize("accum", ["exact", "mfma_fp8"])
+def test_products_cut_in_two(case, accum):
+    """Rows on either side of the cut: dx where earlier pieces are added to it, dw."""
+    announce(f"cross entropy cut products {case} {accum}")
+    M, V, K = case
+    pieces, P, dx_cut, dw_cut = vocab_product_cases.CUT[case]
+    p = Problem(M, V, K, seed=8)
+    lse = p.forward(accum)[1]
+    rows, cols = np.unique([0, dx_cut - 1, min(dx_cut, M - 1), M - 1]), np.unique([0, dw_cut - 1, min(dw_cut, V - 1), min(P + 1, V - 1), V - 1])
+    for types in ((BF, BF), (torch.float32, torch.float32)):
+        out = p.backward(lse, accum, pieces, "e5m2", 30000.0, types)
+        check_backward(p, accum, lse, out, "e5m2", 30000.0, rows, cols, types)
+        assert torch.isfinite(out[0].float()).all() and torch.isfinite(out[1].float()).all()
+        assert (out[0][torch.from_numpy((p.t < 0) | (p.t >= V)).to(device())] == 0).all()
+
+
+@pytest.mark.parametrize("M,V,K", [(5, 2000, 4096), (33, 2500, 80), (130, 1515, 256), (300, 5000, 144)])
+@pytest.mark.parametrize("accum", ["exact", "mfma_fp8"])
+def test_either_gradient_alone(M, V, K, accum):
+    """The same bits as together, whatever the pieces: their length goes by the sizes and the workspace, not by what is asked for."""
+    announce(f"cross entropy one gradient {M}x{V}x{K} {accum}")
+    p = Problem(M, V, K)
+    lse = p.forward(accum)[1]
+    for pieces in (0, 1, 2, 3):
+        for types in ((BF, torch.float32), (torch.float32, BF)):
+            both = p.backward(lse, accum, pieces, "e5m2", 40000.0, types)
+            dx = p.backward(lse, accum, pieces, "e5m2", 40000.0, (types[0], None))
+            dw = p.backward(lse, accum, pieces, "e5m2", 40000.0, (None, types[1]))
+            assert torch.equal(dx[0], both[0]) and torch.equal(dw[1], both[1]), (pieces, types)
+            for alone in (dx, dw):
+                assert torch.equal(alone[2], both[2]) and torch.equal(alone[3], both[3])
