@@ -19,11 +19,23 @@ hipError_t product_shape(const uint8_t* A, const uint8_t* B, int64_t M, int64_t 
                          const ProductEpi& epi, size_t workspace_bytes, hipStream_t st) {
   TileChoice c = choose_tile(M, N, K, MODE == kAccumMfma8, workspace_bytes, persistent_groups(1));
   // A K of up to four steps is over soon after its output begins to be written: smaller tiles, several workgroups a compute unit, store
-  // and load side by side, which the estimate does not know.  dw with the logits before it, in us on 64 x 128, 128 x 128 and 256 x 256
-  // tiles, exact and FP8 cores: 32000 x 4096 from 64 rows 110, 109, 117 and 96, 100, 107; 65536 x 4096 from 64 rows FP8 cores 177, 181, 190; 50021 x
-  // 2048 from 219 rows 133, 131, 138 and 97, 100, 102; 50021 x 1024 from 500 rows 127, 125, 138 and 97, 96, 100; 65536 x 4096 from 200 rows 330, 313,
-  // 317 and 238, 233, 234, from 500 rows 553, 517, 516 and 370, 350, 341; from 1000 rows (50021 x 1024) 225, 218, 214 and 174, 170, 159.
-  if (K <= kShortK && c.split == 1) c.shape = K <= kBK ? 2 : 1;
+  // and load side by side, which the estimate does not know; and on the FP8 cores, whose steps are half as long, the traffic of 128 x 128 tiles
+  // shows from three steps on, where there are rounds enough of the large ones to hide their ends.  dw with the logits before it, in us on
+  // 64 x 128, 128 x 128 and 256 x 256 tiles, all of one run (65536 x 4096: 16 rounds of 256 x 256 tiles on 256 compute units; 32000 x 4096: 7.8;
+  // 50021 x 2048: 6.1; 50021 x 1024: 3.1):
+  //   exact      rows   65536 x 4096    32000 x 4096    50021 x 2048    50021 x 1024
+  //                64   222 218 225     115 115 121      89  92  96      52  54  59
+  //               200   328 311 314     174 167 171     139 134 142      80  80  88
+  //               300   458 437 437     248 237 241     195 186 195     108 105 114
+  //               500   549 512 511     277 260 262     240 228 234     135 132 142
+  //   FP8 cores    64   176 180 188     102 106 111      77  83  86      46  49  53
+  //               200   236 227 226     131 127 129     103 105 108      63  64  68
+  //               300   315 300 291     162 154 154     152 152 154      91  91  95
+  //               500   367 347 335     188 178 176     166 161 161     101  99 102
+  if (K <= kShortK && c.split == 1) {
+    const bool rounds = ((M + 255) / 256) * ((N + 255) / 256) > 7 * (int64_t)persistent_groups(1);
+    c.shape = K <= kBK ? 2 : MODE == kAccumMfma8 && K > 2 * kBK && rounds ? 0 : 1;
+  }
   if (c.shape == 0) {
     if constexpr (MODE == kAccumExact) return epi_run<256, 256, 2, 4, FA, FB, MODE, ProductEpi, 2, true>(A, B, M, N, K, sa, sb, epi, c.split, st);
     else return epi_run<256, 256, 4, 2, FA, FB, MODE, ProductEpi, 2, true>(A, B, M, N, K, sa, sb, epi, c.split, st);

@@ -141,3 +141,17 @@ def test_either_gradient_alone(M, V, K, accum):
             assert torch.equal(dx[0], both[0]) and torch.equal(dw[1], both[1]), (pieces, types)
             for alone in (dx, dw):
                 assert torch.equal(alone[2], both[2]) and torch.equal(alone[3], both[3])
+
+
+@pytest.mark.parametrize("M,V,K", [(300, 30001, 4096), (509, 116000, 1024)])
+def test_short_products_of_many_tiles(M, V, K):
+    """dw of three and four steps on the FP8 cores, whose tiles are more than seven a compute unit: the rows of the first and the last of them."""
+    announce(f"cross entropy dw {M}x{V}x{K}")
+    assert 256 < M <= 512 and -(-V // 256) * -(-K // 256) > 7 * 256
+    p = Problem(M, V, K, seed=4)
+    lse = p.forward("mfma_fp8")[1]
+    cols = np.array([0, 255, V // 2, V - V % 256 - 1, V - 1])
+    for types in ((None, BF), (None, torch.float32)):
+        out = p.backward(lse, "mfma_fp8", 1, "e5m2", 20000.0, types)
+        check_backward(p, "mfma_fp8", lse, out, "e5m2", 20000.0, cols=cols, types=types)
+        assert torch.isfinite(out[1].float()).all()
