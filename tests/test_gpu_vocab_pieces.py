@@ -155,3 +155,19 @@ def test_short_products_of_many_tiles(M, V, K):
         out = p.backward(lse, "mfma_fp8", 1, "e5m2", 20000.0, types)
         check_backward(p, "mfma_fp8", lse, out, "e5m2", 20000.0, cols=cols, types=types)
         assert torch.isfinite(out[1].float()).all()
+
+
+@pytest.mark.parametrize("case", vocab_product_cases.SPLIT)
+@pytest.mark.parametrize("accum", ["exact", "mfma_fp8"])
+def test_split_products_of_several_pieces(case, accum):
+    """dx's parts are joined and added to the sums of the pieces before."""
+    announce(f"cross entropy split products {case} {accum}")
+    M, V, K = case
+    p = Problem(M, V, K, seed=6)
+    lse = p.forward(accum)[1]
+    rows, cols = np.array([0, 1, M // 2, M - 1]), np.array([0, 30207 % V, V - 1])
+    for types in ((BF, BF), (torch.float32, torch.float32)):
+        space = torch.full((vocab_product_cases.SPLIT[case][0] + 4096,), 0xA5, dtype=torch.uint8, device=device())
+        out = p.backward(lse, accum, None, "e5m2", 20000.0, types, workspace=space[:-4096])
+        assert (space[-4096:] == 0xA5).all()
+        check_backward(p, accum, lse, out, "e5m2", 20000.0, rows, cols, types)
