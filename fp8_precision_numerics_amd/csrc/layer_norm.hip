@@ -337,8 +337,8 @@ struct BackRow {
 // NT: the largest workgroup.  PRE: a row is requested while the one before it is worked on, which takes the place of
 // more workgroups.  Rows side by side in a workgroup add their sums up in LDS at the end: a partial row a
 // workgroup, not a row.  Rows of more than 8192 values have workgroups of up to 1024
-// threads, whose 128 registers do not hold another row (2000 x 16384: 76 us; with 512 threads of four octets and the row
-// requested ahead, which spills, 112).
+// threads, whose 128 registers do not hold another row, nor all of one: 28 bytes a lane spill (fp32: 52).  2000 x 16384 bf16 with a
+// residual 76 us (3.4 TB/s), with the branch's 90; with 512 threads of four octets and the row requested ahead, which spills more, 112.
 // WG: a row is several waves', otherwise one's.
 template <int XT, bool WG, int VPT, int NT, bool PRE>
 __global__ __launch_bounds__(NT) void layernorm_backward_kernel(LayerBackArgs a) {
@@ -536,7 +536,7 @@ int layer_groups(int64_t rows, int64_t octets, bool stats) {
 }
 
 // A row is requested ahead where a workgroup has more than one (8192 x 4096, dropout: 45.5 us against 48.7,
-// without dropout 43.2 and 45.8; 1777 x 1040 fp32, a row each: 13.7 and 11.8).  Rows of more than 8192 values need workgroups whose
+// without dropout 43.2 and 45.8; 1777 x 1040 fp32 with a residual and statistics, a row each: 13.7 and 11.8).  Rows of more than 8192 values need workgroups whose
 // registers do not hold another.
 template <int XT, int FMT, bool STATS>
 void layer_run(const LayerArgs& a, int g, hipStream_t st) {
@@ -561,7 +561,7 @@ void layer_stats(const LayerArgs& a, bool stats, int g, hipStream_t st) {
 }
 
 // Threads of a workgroup of the gradient's kernel: rows of less than 4096 values stand side by side in as many as 512 threads
-// hold (4096 x 2048: 18.3 us, with a row each 21.0; 8192 x 1536: 22.5, 26.2; but 8192 x 4096 67.6, 65.9).
+// hold (bf16 with a residual, 4096 x 2048: 18.3 us, with a row each 21.0; 8192 x 1536: 22.5, 26.2; but 8192 x 4096 with dropout 67.6, 65.9).
 int layer_back_threads(int64_t octets) {
   if (octets <= 128) return 256;
   if (octets >= 512) return row_threads(octets);
