@@ -56,7 +56,7 @@ inline int64_t grad_longest(int64_t M, int64_t K, size_t workspace_bytes) {
 // directions take), or as many more as the longest piece asks for.
 inline size_t vocab_workspace(int64_t M, int64_t V, int64_t K, int64_t pieces) {
   if (M == 0) return 0;
-  const int64_t asked = pieces > 0 ? up256((V + pieces - 1) / pieces) : kPieceCols, most = most_columns(M, K);
+  const int64_t asked = pieces > 0 ? up256((V - 1) / pieces + 1) : kPieceCols, most = most_columns(M, K);
   // A vocabulary that is longer than the longest piece needs dx's sums, however few pieces are asked for.
   const int64_t P = asked < most ? asked : most;
   size_t back = (size_t)grad_bytes(M, V, K, P < V ? P : V);

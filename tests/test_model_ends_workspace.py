@@ -77,7 +77,7 @@ def test_a_head_has_room_for_the_lookups_of_fewer_tokens(host):
 # (rows, vocabulary, hidden): small and large, odd, and hidden sizes at which the longest piece of the gradient, 2^31 codes of the weight, is shorter than the vocabulary
 VOCABS = [(1, 1, 16), (1, 131072, 4096), (3, 255, 48), (16, 300, 1024), (17, 257, 128), (63, 50021, 2048), (219, 50021, 2048), (1000, 3000, 64), (1003, 50021, 4096), (2047, 8201, 2048),
           (2048, 32000, 4096), (8191, 65537, 4096), (8192, 65536, 4096), (1000, 40000, 65536), (16, 300, 1 << 22), (500, 600, 1 << 22), (17, 1800, 1 << 20), (7, 1 << 23, 16)]
-PIECES = (1, 2, 3, 4, 5, 8, 33, 1000)
+PIECES = (1, 2, 3, 4, 5, 8, 33, 1000, (1 << 63) - 1)
 
 
 @pytest.mark.parametrize("M,V,K", VOCABS)
