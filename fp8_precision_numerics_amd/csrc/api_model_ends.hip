@@ -32,16 +32,22 @@ bool index_aligned(const void* p, int t) { return (reinterpret_cast<uintptr_t>(p
 
 constexpr int64_t kMaxVocabK = int64_t(1) << 22;  // 256 rows of a piece in a 31-bit offset
 
+// Sizes of the loss and its gradient.
+int check_vocab_sizes(int64_t M, int64_t V, int64_t K) {
+  if (M < 0 || V < 1 || K <= 0 || M > kMaxGemmK - 16 || V > kMaxDim || K > kMaxVocabK) return FP8MI_ERR_SHAPE;
+  if (!dims_ok(M, K) || !dims_ok(V, K) || M * K > kMaxBufferBytes) return FP8MI_ERR_SHAPE;
+  if (((M + 63) / 64) * ((V + 127) / 128 + 1) > kMaxDim) return FP8MI_ERR_SHAPE;
+  return (K & 15) != 0 ? FP8MI_ERR_ALIGN : FP8MI_OK;
+}
+
 // What the loss's two entry points share, M != 0.
 int check_vocab(const uint8_t* x, int fx, const uint8_t* w, int fw, int64_t M, int64_t V, int64_t K, const float* sinv_x,
                 const float* sinv_w, const void* targets, int itype, int accum, const void* workspace) {
   if (!fmt_ok(fx) || !fmt_ok(fw)) return FP8MI_ERR_FORMAT;
   if (!index_ok(itype)) return FP8MI_ERR_DTYPE;
   if (!accum_ok(accum)) return FP8MI_ERR_ACCUM;
-  if (M < 0 || V < 1 || K <= 0 || M > kMaxGemmK - 16 || V > kMaxDim || K > kMaxVocabK) return FP8MI_ERR_SHAPE;
-  if (!dims_ok(M, K) || !dims_ok(V, K) || M * K > kMaxBufferBytes) return FP8MI_ERR_SHAPE;
-  if (((M + 63) / 64) * ((V + 127) / 128 + 1) > kMaxDim) return FP8MI_ERR_SHAPE;
-  if ((K & 15) != 0) return FP8MI_ERR_ALIGN;
+  const int bad = check_vocab_sizes(M, V, K);
+  if (bad != FP8MI_OK) return bad;
   if (workspace && !aligned16(workspace)) return FP8MI_ERR_ALIGN;
   if (M == 0) return FP8MI_OK;
   if (!x || !w || !sinv_x || !sinv_w || !targets || !workspace) return FP8MI_ERR_NULL;
@@ -143,7 +149,7 @@ int fp8_embedding_backward(const void* tokens, int itype, int64_t rows, const vo
 }
 
 size_t fp8mi_vocab_workspace(int64_t M, int64_t V, int64_t K, int64_t pieces) {
-  if (M < 0 || V < 1 || K <= 0 || M > kMaxGemmK - 16 || V > kMaxDim || K > kMaxVocabK || pieces < 0) return 0;
+  if (check_vocab_sizes(M, V, K) != FP8MI_OK || pieces < 0) return 0;
   return vocab_workspace(M, V, K, pieces);
 }
 

@@ -131,3 +131,12 @@ def test_a_launch_has_fewer_than_2_32_threads(host):
         assert n >= 256 and n % 256 == 0 and -(-M // 64) * -(-n // 128) * 256 < 1 << 32
         assert host.most(M, 16) <= n
     assert host.few_columns() % 256 == 0 and host.few_groups(host.few_columns(), 1) * 512 < 1 << 32
+
+
+@pytest.mark.parametrize("M,V,K", [(1 << 20, 100, 2048), (32, 1000, 72), (1 << 23, 100, 16), ((1 << 23) - 16, 1 << 30, 16), (32, 1 << 31, 16), (32, 1000, (1 << 22) + 16), (-1, 10, 16), (4, 0, 16)])
+def test_no_workspace_for_a_loss_that_is_refused(M, V, K):
+    """0 where the calls answer an error about their sizes."""
+    for call in (lambda: fm.load_library().fp8_vocab_cross_entropy(P, 0, P, 0, M, V, K, P, P, P, 1, P, P, 1, P, 16, None),
+                 lambda: fm.load_library().fp8_vocab_cross_entropy_backward(P, 0, P, 0, M, V, K, P, P, P, 1, P, P, 1, P, P, P, 1, P, 1, None, None, 0, P, 16, None)):
+        assert call() in (-2, -3)
+    assert all(fm.vocab_workspace_bytes(M, V, K, pieces) == 0 for pieces in (0, 1, 4))
