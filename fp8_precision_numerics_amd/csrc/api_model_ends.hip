@@ -127,7 +127,7 @@ int fp8_embedding(const void* tokens, int itype, int64_t rows, const void* table
 }
 
 size_t fp8mi_embedding_workspace(int64_t rows, int64_t cols) {
-  if (rows < 0 || cols < 0 || rows > kMaxTokens || cols > kMaxEmbedCols) return 0;
+  if (rows < 0 || cols < 0 || rows > kMaxTokens || cols > kMaxEmbedCols || (cols & 15) != 0) return 0;
   return embedding_workspace(rows, cols);
 }
 

@@ -140,3 +140,9 @@ def test_no_workspace_for_a_loss_that_is_refused(M, V, K):
                  lambda: fm.load_library().fp8_vocab_cross_entropy_backward(P, 0, P, 0, M, V, K, P, P, P, 1, P, P, 1, P, P, P, 1, P, 1, None, None, 0, P, 16, None)):
         assert call() in (-2, -3)
     assert all(fm.vocab_workspace_bytes(M, V, K, pieces) == 0 for pieces in (0, 1, 4))
+
+
+@pytest.mark.parametrize("rows,cols", [(100, 24), (100, 8), (100, -16), (-1, 64), ((1 << 20) + 1, 64), (100, (1 << 20) + 16)])
+def test_no_workspace_for_a_lookup_that_is_refused(rows, cols):
+    assert fm.load_library().fp8_embedding_backward(P, 1, rows, P, 1, 256, cols, 1.0, None, P, 1, P, 16, None) in (-2, -3)
+    assert fm.embedding_workspace_bytes(rows, cols) == 0
